@@ -34,7 +34,8 @@ def _append(name, tokens, requests, heads, kv_heads, dim, page, source, dtype, r
     """`tokens` new tokens of `requests` requests; the first `rotary` values
     of every head are rotated."""
     return {"op": "append", "name": name, "tokens": tokens, "requests": requests, "heads": heads,
-            "kv_heads": kv_heads, "dim": dim, "page": page, "source": source, "dtype": dtype, "rotary": rotary, "interleaved": interleaved}
+            "kv_heads": kv_heads, "dim": dim, "page": page, "source": source, "dtype": dtype, "rotary": rotary,
+            "interleaved": interleaved}
 
 
 def _plan(name, requests, chunk, chunks, lo, hi, page):
@@ -110,8 +111,8 @@ def draw(rng: random.Random):
             rotary = rng.choice([0, 32, dim // 16 * 16, dim // 16 * 16])
             tokens = _log(rng, 1, 8192)
             case = _append(None, tokens, rng.choice([1, tokens, min(tokens, 7)]), kv_heads * rng.choice([1, 3, 4]),
-                           kv_heads, dim, rng.choice([8, 16, 64]), rng.choice(["bf16", "f16", "f32"]), rng.choice(["bf16", "f16"]),
-                           rotary, rng.random() < 0.3)
+                           kv_heads, dim, rng.choice([8, 16, 64]), rng.choice(["bf16", "f16", "f32"]),
+                           rng.choice(["bf16", "f16"]), rotary, rng.random() < 0.3)
             if work(case)["bytes"] > 256 << 20:
                 continue
             if case["source"] != "f32":
