@@ -375,6 +375,144 @@ dfc_status dfc_derived_tables_bytes(const dfc_info *info, uint64_t *bytes);
 dfc_status dfc_derive_tables(const void *blob_dev, const dfc_info *info, uint32_t threads, void *dst_dev,
                              uint64_t cap, void *stream);
 
+/* ------------------------------------------------------------------------
+ * The paged key/value cache of a serving program, whose products run on
+ * compressed weights (dfc_decode_gemm): the memory that the coding frees
+ * holds more tokens.  A step of such a program brings new tokens of several
+ * requests; dfc_paged_plan finds their pages and slots, and for every layer
+ * dfc_paged_append stores their keys and values and dfc_paged_attention
+ * attends over everything stored.  All three are asynchronous on stream,
+ * read every length on the device (nothing is copied back to the host) and
+ * give the same bits on every run.  Structures are read before the call
+ * returns.  Device lengths, tables and slots that make no sense never lead
+ * an access out of the buffers described; they set *status_dev (NULL, or one
+ * device uint32 the caller clears) to DFC_ECORRUPT or DFC_ESIZE (their
+ * two's-complement bit patterns, ORed together) and leave the outputs they
+ * concern unspecified. */
+typedef enum { DFC_BF16 = 0, DFC_F16 = 1, DFC_F32 = 2 } dfc_dtype;
+
+/* Token slot s of a cache (page s / page_size, place s mod page_size) holds
+ * kv_heads rows of head_dim values of each of K and V at
+ * k_dev[page k_stride[0] + place k_stride[1] + head k_stride[2] + i] (element
+ * strides, multiples of 8, not negative; V likewise), 16-byte aligned, so any
+ * order of (page, place, head) fits.  page_size: a power of two.  head_dim: a
+ * multiple of 8, at most 256.  dtype: DFC_BF16 or DFC_F16. */
+typedef struct {
+    void *k_dev, *v_dev;
+    int64_t k_stride[3], v_stride[3];
+    uint32_t n_pages, page_size, kv_heads, head_dim, dtype;
+} dfc_paged_cache;
+
+/* Device pointers unless said otherwise. */
+typedef struct {
+    uint32_t n_requests, max_pages; /* rows of block_table, entries of a row */
+    uint32_t page_size;             /* tokens per page, a power of two */
+    uint32_t n_ring;                /* entries of free_pages */
+    uint64_t tokens;                /* capacity of slots and positions */
+    const int32_t *context_lens;    /* tokens each request holds (n_requests) */
+    const int32_t *new_lens;        /* tokens it brings */
+    int32_t *block_table;           /* request r's pages, in order, at block_table[r table_stride] */
+    int64_t table_stride;
+    const int32_t *free_pages;      /* ring of page numbers */
+    const int64_t *cursor;          /* {head, tail}: free are the ring's entries head .. tail - 1, mod n_ring */
+    int32_t *seq_lens;              /* out: context_lens + new_lens */
+    int32_t *cu_q;                  /* out: n_requests + 1 prefix sums of new_lens */
+    int64_t *slots;                 /* out: cache slot of every new token, -1 where it has none */
+    int32_t *positions;             /* out: its position in its request */
+    int64_t *cursor_out;            /* out: the cursor after the step */
+    uint32_t *status_dev;
+} dfc_plan_args;
+
+/* Pages, slots and positions of a step from its request lengths.  A request
+ * of c tokens holds the pages block_table[r][0 .. ceil(c / P)), which are
+ * read; the pages its n new tokens need beyond those are taken off the ring
+ * in request order and written after them (other entries stay).  New tokens
+ * are numbered request by request; token t of request r gets position
+ * c + t - cu_q[r] and that position's slot.  Entries of slots and positions
+ * past the last new token become -1 and 0.  Pages that the ring cannot give
+ * become -1 in the table and so do their tokens' slots (DFC_ESIZE in the
+ * status, as for requests past max_pages and steps past `tokens`); negative
+ * lengths count as 0 and a cursor that does not fit the ring as an empty one
+ * (DFC_ECORRUPT).  Integers only: the result is exact.  Several workgroups
+ * read the inputs while the outputs are written: cursor_out, seq_lens and
+ * cu_q may not be the inputs themselves.  One launch.  Errors: DFC_EINVAL
+ * (null pointers, page_size not a power of two, table_stride < max_pages, an
+ * output that is an input, an empty ring), DFC_EHIP. */
+dfc_status dfc_paged_plan(const dfc_plan_args *args, void *stream);
+
+typedef struct {
+    dfc_paged_cache cache;
+    uint64_t tokens;
+    const void *k_dev, *v_dev;  /* tokens x kv_heads x head_dim of source_dtype, 16-byte aligned, */
+    int64_t k_src_stride[2], v_src_stride[2]; /* element strides of (token, head), in whole 16 bytes */
+    const int64_t *slots;       /* slot of every token; -1: not stored */
+    uint32_t source_dtype;      /* DFC_F32, or the cache's */
+    uint32_t q_heads;           /* 0: no q */
+    const void *q_dev;          /* tokens x q_heads x head_dim of source_dtype */
+    void *q_out_dev;            /* the same in the cache's type, rotated */
+    int64_t q_stride[2], q_out_stride[2];
+    uint32_t rot_dim;           /* values of each head that are rotated: a multiple of 16, 0 = none */
+    uint32_t interleaved;       /* pairs (2i, 2i + 1) instead of (i, i + rot_dim / 2) */
+    uint32_t max_positions;
+    const int32_t *positions;   /* position of every token (rot_dim > 0) */
+    const float *rotary_dev;    /* max_positions x rot_dim: rot_dim / 2 cosines, then as many sines; 16-byte aligned */
+    uint32_t *status_dev;
+} dfc_append_args;
+
+/* A step's keys and values into the cache, rounded to nearest even, with the
+ * rotary embedding of k (and of q, which goes to q_out): each pair (a, b) of
+ * a head's first rot_dim values becomes (a cos - b sin, b cos + a sin) by the
+ * angles of the token's position, in fp32.  Tokens whose slot is -1 are not
+ * stored (their q is still rotated); a slot past the cache is not stored
+ * either, and a position past the table takes the first row's angles
+ * (DFC_ECORRUPT in the status).  Slots are distinct.  The source may be the
+ * fp32 output of dfc_decode_gemm.  q_out may be q only without rotation.
+ * Errors: DFC_EINVAL (null or misaligned pointers, strides or sizes as
+ * above), DFC_EUNSUPPORTED (types, head_dim over 256), DFC_EHIP. */
+dfc_status dfc_paged_append(const dfc_append_args *args, void *stream);
+
+typedef struct {
+    dfc_paged_cache cache;
+    uint32_t heads;             /* query heads, a multiple of cache.kv_heads: head h reads cache head h / (heads / kv_heads) */
+    uint32_t n_requests, max_pages;
+    uint32_t max_q_len;         /* a hint: the most new tokens a request has, 0 = unknown.  A wrong one costs time only */
+    uint64_t tokens;            /* rows of q */
+    const void *q_dev;          /* tokens x heads x head_dim in the cache's type, 16-byte aligned */
+    void *out_dev;              /* the same shape and type */
+    int64_t q_stride[2], out_stride[2]; /* element strides of (token, head), multiples of 8 */
+    float *lse_dev;             /* NULL, or tokens x heads: ln of each row's sum of exp(scaled score) */
+    const int32_t *block_table; /* as in dfc_plan_args */
+    int64_t table_stride;
+    const int32_t *cu_q;        /* request r's rows of q: cu_q[r] .. cu_q[r + 1] - 1 */
+    const int32_t *seq_lens;    /* tokens each request has in the cache, its new ones included */
+    float scale;                /* of the scores, above 0 */
+    uint32_t causal;            /* 0: every row sees all of its request */
+    uint32_t window;            /* keys a row sees, counted back from its own position; 0 = all */
+    void *workspace_dev;        /* dfc_paged_attention_workspace bytes, 256-byte aligned, that nothing */
+    uint64_t workspace_bytes;   /* else touches until this call's work has run */
+    uint32_t *status_dev;
+} dfc_attention_args;
+
+/* Attention of a step's new tokens over the paged cache: one token a request
+ * (decoding), a chunk (a prompt's part) or both in one call.  Row i of a
+ * request with n rows and s tokens stands at position p = s - n + i and sees
+ * the keys j < s with j <= p (causal) and j > p - window (window > 0):
+ * out = sum_j exp(z_j) v_j / sum_j exp(z_j), z_j = scale q . k_j.  Products of
+ * 16-bit values accumulate in fp32, maxima, sums and rescaling are fp32, and
+ * the weights are rounded to the cache's type for the second product.  A row
+ * that sees no key gives 0 and an lse of -inf.  What a key or value that a
+ * row does not see holds (inf and NaN included), and what lies in a page past
+ * its request's tokens, has no influence on the row.  Pages outside the cache
+ * count as zeros (DFC_ECORRUPT in the status).  Rows past cu_q[n_requests]
+ * are not written.  Errors: DFC_EINVAL, DFC_ESIZE (workspace),
+ * DFC_EUNSUPPORTED (types, head_dim over 256, tokens x heads / kv_heads past
+ * 2^31), DFC_EHIP. */
+dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream);
+
+/* Bytes of the workspace for those arguments (host; reads sizes only, no
+ * pointers but the cache's are needed). */
+dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_t *bytes);
+
 /* Human-readable name of a status code. */
 const char *dfc_status_str(dfc_status s);
 

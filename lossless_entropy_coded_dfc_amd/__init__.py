@@ -23,6 +23,7 @@ __all__ = [
     "encode_bound", "encode", "blob_info", "decode", "decode_batch", "set_launch",
     "STORES_AUTO", "STORES_DEFERRED", "STORES_IMMEDIATE",
     "status_str", "MAX_BATCH", "derived_tables_bytes", "derive_tables",
+    "PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace",
 ]
 
 MAX_BATCH = 32
@@ -88,6 +89,16 @@ class Info(ctypes.Structure):
 class BatchItem(ctypes.Structure):
     _fields_ = [("blob_dev", ctypes.c_void_p), ("info", ctypes.POINTER(Info)),
                 ("dst_dev", ctypes.c_void_p), ("n", ctypes.c_uint64), ("tables_dev", ctypes.c_void_p)]
+
+
+def __getattr__(name):
+    # the paged cache's entry points need torch, which the codec does not
+    if name in ("PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace"):
+        from . import paged
+        for entry in paged.__all__:
+            globals()[entry] = getattr(paged, entry)
+        return globals()[name]
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
 
 
 def library_path() -> str:

@@ -1,0 +1,862 @@
+// dfc_attention.hip - attention of a step's new tokens over the paged cache.
+//
+// Token i of request r (n_r new tokens, s_r tokens in all) stands at position
+// p = s_r - n_r + i and sees the keys j < s_r with j <= p (causal) and
+// j > p - window.  For each of its heads, which share the keys and values of
+// one cache head in groups of G = heads / kv_heads,
+//     o = sum_j exp(z_j - m) v_j / sum_j exp(z_j - m),  z_j = scale q . k_j,
+// in one pass over the keys: m is a running reference no smaller than the
+// running maximum less a slack, and the sums are rescaled when it moves.
+//
+// Rows.  The n_r G (token, head of the group) pairs of a request and cache
+// head are its rows; a tile is 32 RW of them, 32 per wavefront.  A workgroup
+// of four wavefronts takes one tile and one piece of its keys: RW wavefronts
+// along the rows times 4 / RW groups along the keys, whose results it joins
+// at the end.
+//
+// Layout.  Scores are computed transposed, S^T = K Q^T, with 32x32x16
+// MFMA: lane l then holds, for the row l mod 32, the keys 8 (r / 4) +
+// 4 (l / 32) + r mod 4 of each block of 32 (r = 0..15), so a row's maximum
+// and sum are in-lane sums and one exchange with lane l ^ 32, and the
+// rounded probabilities are, as they stand, the B operand of O^T = V^T P^T
+// (the order of the keys within a step of 16 is free as long as V^T follows
+// it: the transposing LDS read gives each lane those four keys at its
+// column).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+#include <cstring>
+
+#include "dfc.h"
+#include "dfc_decode_core.h"
+#include "dfc_paged.h"
+
+namespace {
+
+using f32x16 = __attribute__((ext_vector_type(16))) float;
+using s16x4 = __attribute__((ext_vector_type(4))) short;
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kSchedThreads = 1024;
+constexpr uint32_t kWaves = 4;
+
+// One piece of work: a tile of rows of one request and a range of keys; every
+// cache head has it.
+struct alignas(64) Piece {
+    int32_t req, row0;     // request; first row of the tile
+    int32_t q_start, q_len, kv_len;
+    int32_t lo, hi;        // keys
+    int32_t split, splits; // which piece of the tile, of how many
+    int32_t slot;          // first partial result of the tile (splits > 1)
+    int32_t pad[6];
+};
+
+struct AttnArgs {
+    const void *q, *k, *v;
+    void *out;
+    float *lse;
+    const int32_t *table, *cu_q, *seq_lens;
+    int64_t q_stride[2], out_stride[2], k_stride[3], v_stride[3], table_stride;
+    uint32_t n_pages, page_shift, kv_heads, group, heads, dim;
+    uint32_t n_requests, tokens, max_pages, window;
+    int32_t causal;
+    float scale, scale_log2;   // scores by exp2: scale log2(e)
+    // schedule
+    uint32_t rows_per_tile, key_tile, min_piece, targets;  // targets: pieces aimed at over all cache heads
+    uint32_t piece_cap, slot_cap;                          // capacities of pieces[] and of partial results per head
+    uint32_t *count;       // pieces made
+    Piece *pieces;
+    float *part_o, *part_ml;
+    uint32_t *status;
+};
+
+// -------------------------------------------------------------- schedule
+
+__device__ __forceinline__ uint32_t block_scan(uint32_t &x, uint32_t *part) {
+    constexpr uint32_t W = kSchedThreads / kWave;
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint32_t ix = x;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint32_t u = __shfl_up(ix, d);
+        if (lane >= uint32_t(d)) ix += u;
+    }
+    __syncthreads();
+    if (lane == kWave - 1) part[wave] = ix;
+    __syncthreads();
+    uint32_t before = 0, sum = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < W; ++w) {
+        const uint32_t v = part[w];
+        if (w < wave) before += v;
+        sum += v;
+    }
+    x = before + ix - x;
+    return sum;
+}
+
+struct Req {
+    int32_t q_start, q_len, kv_len;
+};
+
+// A request's ranges, held inside the buffers whatever the lengths say.
+__device__ __forceinline__ Req request(const AttnArgs &a, uint32_t r, uint32_t &bad) {
+    Req q;
+    const int32_t c0 = a.cu_q[r], c1 = a.cu_q[r + 1];
+    q.q_start = min(max(c0, 0), int32_t(a.tokens));
+    q.q_len = min(max(c1, q.q_start), int32_t(a.tokens)) - q.q_start;
+    const int64_t room = int64_t(a.max_pages) << a.page_shift;
+    const int32_t s = a.seq_lens[r];
+    const int32_t most = int32_t(min(room, int64_t(0x7fffff00)));  // a key tile past it is still an int
+    q.kv_len = min(max(s, 0), most);
+    if (c0 < 0 || c1 < c0 || c1 > int32_t(a.tokens) || q.kv_len != s) bad |= kStatusCorrupt;
+    return q;
+}
+
+// Keys [lo, hi) that the rows row0 .. of a tile see between them, lo at a
+// multiple of the key tile.
+__device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint32_t row0, int32_t &lo, int32_t &hi) {
+    const int32_t t0 = int32_t(row0 / a.group);
+    const int32_t rows = int32_t(min(uint64_t(a.rows_per_tile), uint64_t(q.q_len) * a.group - row0));
+    const int32_t t1 = int32_t((row0 + uint32_t(rows) - 1) / a.group);
+    const int64_t base = int64_t(q.kv_len) - q.q_len;
+    const int64_t end = a.causal ? min(int64_t(q.kv_len), base + t1 + 1) : int64_t(q.kv_len);
+    int64_t begin = a.window ? max(int64_t(0), base + t0 + 1 - int64_t(a.window)) : 0;
+    begin = begin / a.key_tile * a.key_tile;
+    hi = int32_t(max(end, int64_t(0)));
+    lo = int32_t(min(begin, int64_t(hi)));
+}
+
+// One workgroup cuts the step into pieces: a first pass adds up the key tiles
+// of every tile of rows, which sets the largest piece, a second one writes
+// the pieces.  A tile's later rows see more keys, so a request's tiles are
+// listed from the last.
+__global__ __launch_bounds__(kSchedThreads) void schedule_kernel(AttnArgs a) {
+    __shared__ uint32_t part[kSchedThreads / kWave];
+    __shared__ uint32_t first[kSchedThreads], tiles_of[kSchedThreads];
+    __shared__ Req req_of[kSchedThreads];
+    const uint32_t tid = threadIdx.x;
+    uint32_t bad = 0;
+    uint64_t cost = 0;          // key tiles, over all tiles (this thread's share)
+    uint32_t piece = 1u << 30;  // key tiles per piece
+    uint32_t n_pieces = 0, n_slots = 0;
+    for (int pass = 0; pass < 2; ++pass) {
+        for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kSchedThreads) {
+            const uint32_t r = r0 + tid, here = min(kSchedThreads, a.n_requests - r0);
+            Req q{0, 0, 0};
+            if (r < a.n_requests) q = request(a, r, bad);
+            uint32_t n = uint32_t((uint64_t(q.q_len) * a.group + a.rows_per_tile - 1) / a.rows_per_tile);
+            uint32_t f = n;
+            const uint32_t total = block_scan(f, part);
+            __syncthreads();
+            first[tid] = f;
+            tiles_of[tid] = n;
+            req_of[tid] = q;
+            __syncthreads();
+            for (uint32_t t0 = 0; t0 < total; t0 += kSchedThreads) {
+                const uint32_t t = t0 + tid;
+                uint32_t splits = 0, row0 = 0, k = 0;
+                int32_t lo = 0, hi = 0;
+                if (t < total) {
+                    uint32_t h = here;
+                    while (h - k > 1) {
+                        const uint32_t mid = (k + h) / 2;
+                        if (first[mid] <= t)
+                            k = mid;
+                        else
+                            h = mid;
+                    }
+                    row0 = (tiles_of[k] - 1u - (t - first[k])) * a.rows_per_tile;
+                    tile_keys(a, req_of[k], row0, lo, hi);
+                    const uint32_t c = uint32_t(hi - lo + int32_t(a.key_tile) - 1) / a.key_tile;
+                    cost += c;
+                    splits = max(1u, (c + piece - 1) / piece);
+                }
+                if (pass == 0) continue;
+                uint32_t at = splits, slot = splits > 1 ? splits : 0u;
+                const uint32_t s_all = block_scan(at, part), p_all = block_scan(slot, part);
+                at += n_pieces;
+                slot += n_slots;
+                n_pieces += s_all;
+                n_slots += p_all;
+                if (t < total) {
+                    const uint32_t c = uint32_t(hi - lo + int32_t(a.key_tile) - 1) / a.key_tile;
+                    const Req q2 = req_of[k];
+                    for (uint32_t s = 0; s < splits; ++s) {
+                        // even shares of the key tiles
+                        const uint32_t c0 = uint32_t(uint64_t(c) * s / splits), c1 = uint32_t(uint64_t(c) * (s + 1) / splits);
+                        Piece w;
+                        w.req = int32_t(r0 + k);
+                        w.row0 = int32_t(row0);
+                        w.q_start = q2.q_start;
+                        w.q_len = q2.q_len;
+                        w.kv_len = q2.kv_len;
+                        w.lo = lo + int32_t(c0 * a.key_tile);
+                        w.hi = min(hi, lo + int32_t(c1 * a.key_tile));
+                        w.split = int32_t(s);
+                        w.splits = int32_t(splits);
+                        w.slot = int32_t(slot);
+                        // the capacities hold every step whose lengths are what they should be
+                        if (splits > 1 && slot + splits > a.slot_cap) {
+                            w.q_len = 0;
+                            bad |= kStatusCorrupt;
+                        }
+                        if (at + s < a.piece_cap) a.pieces[at + s] = w;
+                    }
+                }
+            }
+            __syncthreads();  // the requests have been read
+        }
+        if (pass == 0) {
+            // the workgroup's key tiles over all cache heads, shared out
+            __shared__ unsigned long long sum;
+            if (tid == 0) sum = 0;
+            __syncthreads();
+            atomicAdd(&sum, cost);
+            __syncthreads();
+            const uint64_t all = sum * a.kv_heads;
+            piece = uint32_t(min(uint64_t(1) << 30, max(uint64_t(a.min_piece), (all + a.targets - 1) / a.targets)));
+        }
+    }
+    if (n_pieces > a.piece_cap) bad |= kStatusCorrupt;
+    if (tid == 0) *a.count = min(n_pieces, a.piece_cap);
+    if (bad && a.status) atomicOr(a.status, bad);
+}
+
+// ------------------------------------------------------------- attention
+
+// A piece, in scalar registers.
+__device__ __forceinline__ Piece get_piece(const AttnArgs &a, uint32_t index) {
+    Piece w = a.pieces[index];
+    int32_t *x = &w.req;
+#pragma unroll
+    for (int i = 0; i < 10; ++i) x[i] = __builtin_amdgcn_readfirstlane(x[i]);
+    return w;
+}
+
+template <typename E>
+struct Type;
+template <>
+struct Type<__bf16> {
+    using V8 = __attribute__((ext_vector_type(8))) __bf16;
+    // probabilities up to 2^kSlack: bf16 has the range of fp32
+    static constexpr float kSlack = 8.0f, kBias = 0.0f;
+    static constexpr uint32_t kExp = 0x7f80u, kOne = 0x0080u;
+    static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+    }
+};
+template <>
+struct Type<_Float16> {
+    using V8 = __attribute__((ext_vector_type(8))) _Float16;
+    // fp16 ends at 65504 and loses bits below 2^-14: probabilities are held
+    // 2^8 above their value, so that the largest are in [2^8, 2^14] and a
+    // weight keeps its bits down to 2^-22 of the largest
+    static constexpr float kSlack = 6.0f, kBias = 8.0f;
+    static constexpr uint32_t kExp = 0x7c00u, kOne = 0x0400u;
+    static __device__ __forceinline__ f32x16 mfma(V8 a, V8 b, f32x16 c) {
+        return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
+    }
+};
+
+// 16-byte pieces of K and V rows in LDS are permuted within the row so that
+// the reads below spread over the banks.  K: a read takes the same piece of
+// 32 rows.  V: a transposing read takes 64 bytes of each of 4 rows.
+template <int DP>
+__device__ __forceinline__ uint32_t k_place(uint32_t row, uint32_t c) {
+    return row * (DP / 8) + (c ^ (row & (DP >= 128 ? 15u : 7u)));
+}
+template <int DP>
+__device__ __forceinline__ uint32_t v_place(uint32_t row, uint32_t c) {
+    const uint32_t turn = DP >= 128 ? (row & 3u) : ((row ^ (row >> 1)) & 1u);
+    return row * (DP / 8) + (c ^ (turn << 2));
+}
+
+__device__ __forceinline__ float other_half(float x) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+    return __uint_as_float((threadIdx.x & 32u) ? r[0] : r[1]);
+}
+
+template <typename E, int DP, int RW, int KT>
+struct Shape {
+    static constexpr int KW = kWaves / RW;             // groups along the keys
+    static constexpr int kBuffers = RW == 1 ? 1 : 2;   // a wavefront alone needs no second one
+    static constexpr uint32_t kTileBytes = KT * DP * 2;          // of K or of V
+    static constexpr uint32_t kGroupBytes = 2 * kTileBytes * kBuffers;
+    static constexpr uint32_t kOutBytes = 32 * DP * 4;           // a wavefront's rows in fp32
+    static constexpr uint32_t kLoop = KW * kGroupBytes;
+    static constexpr uint32_t kEnd = kWaves * kOutBytes;
+    static constexpr uint32_t kMl = kLoop > kEnd ? kLoop : kEnd;  // offset of the joined maxima and sums
+    static constexpr uint32_t kLds = kMl + kWaves * 32 * 8;
+};
+
+// The same sums for 32 rows of a wavefront, a row at a time and without
+// matrix instructions, so that a key that a row does not see takes no part at
+// all: for tiles in which such a key's value is not finite.  Lanes take keys
+// for the scores and columns for the sums.  The wavefront's keys are the
+// tiles of `kt` keys every `stride` from w.lo + first.
+template <typename E, int DP>
+__device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t row_base,
+                                                uint32_t first, uint32_t stride, int kt, float *own, float *ml) {
+    using V8 = __attribute__((ext_vector_type(8))) E;
+    const uint32_t lane = threadIdx.x % kWave;
+    const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
+    const E *kbase = static_cast<const E *>(a.k) + int64_t(kvh) * a.k_stride[2];
+    const E *vbase = static_cast<const E *>(a.v) + int64_t(kvh) * a.v_stride[2];
+    const int32_t page_mask = (1 << a.page_shift) - 1;
+    constexpr int NO = DP / 64;
+#pragma unroll 1
+    for (uint32_t r = 0; r < 32u; ++r) {
+        const int32_t row = w.row0 + int32_t(row_base + r);
+        if (row >= w.q_len * int32_t(a.group)) break;
+        const int32_t tok = row / int32_t(a.group), g = row - tok * int32_t(a.group);
+        const int32_t pos = w.kv_len - w.q_len + tok;
+        const int32_t see_hi = a.causal ? min(pos + 1, w.hi) : w.hi;
+        const int32_t see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
+        const E *qp = static_cast<const E *>(a.q) + int64_t(w.q_start + tok) * a.q_stride[0] +
+                      int64_t(kvh * a.group + uint32_t(g)) * a.q_stride[1];
+        float m = -INFINITY, l = 0.0f, o[NO] = {};
+#pragma unroll 1
+        for (int32_t start = w.lo + int32_t(first); start < w.hi; start += int32_t(stride)) {
+            const int32_t key = start + int32_t(lane);
+            int32_t page = -1;
+            if (int32_t(lane) < kt && key >= see_lo && key < see_hi) page = table[key >> a.page_shift];
+            const bool seen = int32_t(lane) < kt && key >= see_lo && key < see_hi;
+            if (uint32_t(page) >= a.n_pages) page = -1;  // counts as zeros
+            const int64_t in_page = key & page_mask;
+            float z = 0.0f;
+            if (page >= 0) {
+                const E *kp = kbase + page * a.k_stride[0] + in_page * a.k_stride[1];
+                for (uint32_t d = 0; d < a.dim; d += 8u) {
+                    const V8 x = *reinterpret_cast<const V8 *>(kp + d), y = *reinterpret_cast<const V8 *>(qp + d);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) z = __builtin_fmaf(float(x[j]), float(y[j]), z);
+                }
+            }
+            if (!seen) z = -INFINITY;
+            float top = z;
+#pragma unroll
+            for (int d = 32; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+            const float m2 = fmaxf(m, top);
+            const float f = m2 == m ? 1.0f : __builtin_amdgcn_exp2f((m - m2) * a.scale_log2);
+            m = m2;
+            const float off = Type<E>::kBias - (m == -INFINITY ? 0.0f : m * a.scale_log2);
+            const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(z, a.scale_log2, off));
+            float sum = e;
+#pragma unroll
+            for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+            l = l * f + sum;
+#pragma unroll
+            for (int j = 0; j < NO; ++j) o[j] *= f;
+            const uint64_t seen_mask = __ballot(seen), page_in = __ballot(page >= 0);
+#pragma unroll 1
+            for (int k = 0; k < kt; ++k) {
+                if (!((seen_mask & page_in) >> k & 1u)) continue;
+                const float p = __shfl(e, k);
+                const int32_t pg = __shfl(page, k);
+                const E *vp = vbase + pg * a.v_stride[0] + int64_t((start + k) & page_mask) * a.v_stride[1];
+#pragma unroll
+                for (int j = 0; j < NO; ++j)
+                    if (lane + 64u * uint32_t(j) < a.dim) o[j] += p * float(vp[lane + 64u * uint32_t(j)]);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NO; ++j) {
+            const uint32_t d = lane + 64u * uint32_t(j);
+            own[4u * (r * (DP / 4) + ((d / 4u) ^ (r & 7u))) + d % 4u] = o[j];
+        }
+        if (lane == 0) *reinterpret_cast<float2 *>(ml + 2u * r) = float2{m, l};
+    }
+}
+
+template <typename E, int DP, int RW, int KT>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a) {
+    using T = Type<E>;
+    using V8 = typename T::V8;
+    using Sh = Shape<E, DP, RW, KT>;
+    constexpr int KW = Sh::KW;
+    constexpr int CPR = DP / 8;                       // 16-byte pieces per row
+    constexpr int GT = 64 * RW;                       // threads that load a tile together
+    constexpr int NL = KT * CPR / GT;                 // pieces of K (and of V) per thread
+    constexpr int NB = KT / 32, NS = KT / 16, ND = DP / 32, NQ = DP / 16;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+
+    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
+    if (index >= *a.count) return;
+    const Piece w = get_piece(a, index);
+    if (w.q_len <= 0) return;
+    const uint32_t lane = threadIdx.x % kWave;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t rw = wave % RW, kw = wave / RW;
+    const uint32_t c = lane & 31u, h = lane >> 5;
+    const int32_t n_rows = w.q_len * int32_t(a.group);
+    const int32_t lo = w.lo, hi = w.hi;
+
+    // this lane's row
+    const int32_t row = w.row0 + int32_t(32u * rw + c);
+    const bool row_in = row < n_rows;
+    const int32_t row_c = min(row, n_rows - 1);
+    const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
+    const int32_t pos = w.kv_len - w.q_len + tok;
+    const int32_t see_hi = a.causal ? min(pos + 1, hi) : hi;
+    const int32_t see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
+    // over the wavefront's rows (positions ascend with the row)
+    const int32_t hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
+    const int32_t hi_max = __builtin_amdgcn_readlane(see_hi, 31), lo_max = __builtin_amdgcn_readlane(see_lo, 31);
+    const bool idle = w.row0 + int32_t(32u * rw) >= n_rows;
+
+    V8 qf[NQ];
+    {
+        const E *qp = static_cast<const E *>(a.q) + int64_t(w.q_start + tok) * a.q_stride[0] +
+                      int64_t(kvh * a.group + uint32_t(g)) * a.q_stride[1];
+#pragma unroll
+        for (int s = 0; s < NQ; ++s) {
+            V8 x = {};
+            const uint32_t d = 16u * uint32_t(s) + 8u * h;
+            if (row_in && d < a.dim) x = *reinterpret_cast<const V8 *>(qp + d);
+            qf[s] = x;
+        }
+    }
+
+    f32x16 acc[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) acc[d] = f32x16{};
+    float m = -INFINITY, l = 0.0f;  // reference (raw scores); this lane's share of the sum
+    const float slack = fminf(T::kSlack / a.scale_log2, 1e30f);
+
+    uint8_t *group = lds + kw * Sh::kGroupBytes;
+    const uint32_t gtid = rw * 64u + lane;  // thread among those of the key group
+    const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
+    const E *kbase = static_cast<const E *>(a.k) + int64_t(kvh) * a.k_stride[2];
+    const E *vbase = static_cast<const E *>(a.v) + int64_t(kvh) * a.v_stride[2];
+    const int32_t page_mask = (1 << a.page_shift) - 1;
+    const int32_t n_tiles = (hi - lo + KT - 1) / KT;
+    const int32_t n_steps = (n_tiles + KW - 1) / KW;  // the same for every group: they meet at barriers
+    bool missing = false;
+    uint32_t odd = 0;  // a tile with masked keys held a value that is not finite
+
+    // The page of key start + lane of a tile, -1 where there is none.
+    auto pages_of = [&](int32_t start) -> int32_t {
+        const int32_t key = start + int32_t(lane % KT);
+        int32_t page = -1;
+        if (key < hi) {
+            page = table[key >> a.page_shift];
+            if (uint32_t(page) >= a.n_pages) {
+                page = -1;
+                missing = true;
+            }
+        }
+        return page;
+    };
+    uint4 kr[NL], vr[NL];
+    auto load = [&](int32_t start, int32_t pages) {
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const uint32_t i = gtid + uint32_t(n) * GT;
+            const uint32_t r = i / CPR, ch = i % CPR;
+            const int32_t page = __shfl(pages, int(r));
+            kr[n] = vr[n] = uint4{0, 0, 0, 0};
+            if (page >= 0 && ch * 8u < a.dim) {
+                const int64_t in_page = (start + int32_t(r)) & page_mask;
+                kr[n] = *reinterpret_cast<const uint4 *>(kbase + page * a.k_stride[0] + in_page * a.k_stride[1] + ch * 8u);
+                vr[n] = *reinterpret_cast<const uint4 *>(vbase + page * a.v_stride[0] + in_page * a.v_stride[1] + ch * 8u);
+            }
+        }
+    };
+    auto tile_start = [&](int32_t step) { return lo + (step * KW + int32_t(kw)) * KT; };
+
+    int32_t pages = pages_of(tile_start(0));
+    load(tile_start(0), pages);
+    pages = pages_of(tile_start(1));
+
+    for (int32_t step = 0; step < n_steps; ++step) {
+        const int32_t start = tile_start(step);
+        uint8_t *buf = group + (Sh::kBuffers == 2 ? uint32_t(step & 1) : 0u) * 2u * Sh::kTileBytes;
+        uint4 *kl = reinterpret_cast<uint4 *>(buf);
+        uint4 *vl = reinterpret_cast<uint4 *>(buf + Sh::kTileBytes);
+        if constexpr (RW == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const uint32_t i = gtid + uint32_t(n) * GT;
+            kl[k_place<DP>(i / CPR, i % CPR)] = kr[n];
+            vl[v_place<DP>(i / CPR, i % CPR)] = vr[n];
+        }
+        // one barrier a step: a buffer is written again two steps later, when
+        // every wavefront has passed the next step's barrier
+        if constexpr (RW == 1)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        else
+            __syncthreads();
+        if (step + 1 < n_steps) {
+            load(tile_start(step + 1), pages);
+            pages = pages_of(tile_start(step + 2));
+        }
+        if (idle || start >= hi_max || start + KT <= lo_min) continue;
+
+        // S^T = K Q^T
+        f32x16 s[NB];
+#pragma unroll
+        for (int b = 0; b < NB; ++b) s[b] = f32x16{};
+#pragma unroll
+        for (int k = 0; k < NQ; ++k)
+#pragma unroll
+            for (int b = 0; b < NB; ++b) {
+                const V8 kf = __builtin_bit_cast(V8, kl[k_place<DP>(32u * uint32_t(b) + c, 2u * uint32_t(k) + h)]);
+                s[b] = T::mfma(kf, qf[k], s[b]);
+            }
+        const bool masked = start + KT > hi_min || start < lo_max;
+        if (masked) {
+#pragma unroll
+            for (int b = 0; b < NB; ++b)
+#pragma unroll
+                for (int r = 0; r < 16; ++r) {
+                    const int32_t key = start + 32 * b + 8 * (r / 4) + 4 * int32_t(h) + r % 4;
+                    if (key >= see_hi || key < see_lo) s[b][r] = -INFINITY;
+                }
+        }
+        // the running reference
+        float top = s[0][0];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) top = fmaxf(top, s[b][r]);
+        top = fmaxf(top, other_half(top));
+        if (__any(top > m + slack)) {
+            const float m2 = fmaxf(m, top);
+            const float f = m2 == m ? 1.0f : __builtin_amdgcn_exp2f((m - m2) * a.scale_log2);
+            m = m2;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d] *= f;
+        }
+        const float off = T::kBias - (m == -INFINITY ? 0.0f : m * a.scale_log2);
+        V8 p[NS];
+#pragma unroll
+        for (int b = 0; b < NB; ++b)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(s[b][r], a.scale_log2, off));
+                l += e;
+                p[2 * b + r / 8][r % 8] = E(e);
+            }
+
+        // O^T += V^T P^T
+        const uint32_t i16 = lane % 16u;
+        auto v_frag = [&](int st, int d) -> V8 {
+            const uint32_t key = 16u * uint32_t(st) + 4u * h + i16 / 4u;
+            const uint32_t ch = 4u * uint32_t(d) + 2u * ((lane >> 4) & 1u) + (i16 % 4u) / 2u;
+            using L4 = __attribute__((address_space(3))) s16x4;
+            struct Two {
+                s16x4 a, b;
+            } t;
+            const uint8_t *at = reinterpret_cast<const uint8_t *>(vl);
+            t.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 16u * v_place<DP>(key, ch) + 8u * (i16 & 1u)));
+            t.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 16u * v_place<DP>(key + 8u, ch) + 8u * (i16 & 1u)));
+            return __builtin_bit_cast(V8, t);
+        };
+        if (masked) {
+            // a masked key adds nothing, whatever its value holds, but 0 x inf
+            // in the product below is not nothing: note it, and see the end
+            constexpr uint32_t kE = T::kExp * 0x10001u, kO = T::kOne * 0x10001u;
+            uint32_t bits = 0;
+#pragma unroll 2
+            for (uint32_t i = lane; i < uint32_t(KT * CPR); i += 64u) {
+                const uint4 x = vl[i];
+                bits |= ((x.x & kE) + kO) | ((x.y & kE) + kO) | ((x.z & kE) + kO) | ((x.w & kE) + kO);
+            }
+            odd |= bits & 0x80008000u;
+        }
+#pragma unroll
+        for (int st = 0; st < NS; ++st)
+#pragma unroll
+            for (int d = 0; d < ND; ++d) acc[d] = T::mfma(v_frag(st, d), p[st], acc[d]);
+    }
+    if (missing && a.status) atomicOr(a.status, kStatusCorrupt);
+
+    // Join the key groups and write.  A wavefront's rows go to LDS; the
+    // wavefronts of a row group then each take a share of its rows, so that
+    // stores run along the rows.
+    l += other_half(l);
+    float *ml = reinterpret_cast<float *>(lds + Sh::kMl) + 64u * wave;
+    auto place = [&](uint32_t r, uint32_t q4) { return r * (DP / 4) + (q4 ^ (r & 7u)); };
+    float4 *own = reinterpret_cast<float4 *>(lds + wave * Sh::kOutBytes);
+    __syncthreads();
+    if (!__any(odd != 0)) {
+        if (h == 0) *reinterpret_cast<float2 *>(ml + 2u * c) = float2{m, l};
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int q4 = 0; q4 < 4; ++q4)
+                own[place(c, 8u * uint32_t(d) + 2u * uint32_t(q4) + h)] =
+                    float4{acc[d][4 * q4], acc[d][4 * q4 + 1], acc[d][4 * q4 + 2], acc[d][4 * q4 + 3]};
+    } else {
+        rows_one_by_one<E, DP>(a, w, kvh, 32u * rw, kw * KT, uint32_t(KW * KT), KT, reinterpret_cast<float *>(own), ml);
+    }
+    __syncthreads();
+    auto weight = [&](float mk, float top) {
+        return mk == top ? 1.0f : __builtin_amdgcn_exp2f((mk - top) * a.scale_log2);
+    };
+    ml = reinterpret_cast<float *>(lds + Sh::kMl);
+    const bool whole = w.splits == 1;
+    const uint64_t slot = (uint64_t(uint32_t(w.slot + w.split)) * a.kv_heads + kvh) * a.rows_per_tile;
+#pragma unroll 2
+    for (uint32_t i = lane; i < 32u / KW * CPR; i += 64u) {
+        const uint32_t r = kw * (32u / KW) + i / CPR, ch = i % CPR;
+        const int32_t at = w.row0 + int32_t(32u * rw + r);
+        if (at >= n_rows || ch * 8u >= a.dim) continue;
+        float top = -INFINITY, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < KW; ++k) top = fmaxf(top, ml[2u * (32u * (uint32_t(k) * RW + rw) + r)]);
+        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+        for (int k = 0; k < KW; ++k) {
+            const uint32_t src = uint32_t(k) * RW + rw;
+            const float2 v = *reinterpret_cast<const float2 *>(ml + 2u * (32u * src + r));
+            const float f = KW == 1 ? 1.0f : weight(v.x, top);
+            sum += v.y * f;
+            const float4 *o = reinterpret_cast<const float4 *>(lds + src * Sh::kOutBytes);
+            const float4 x0 = o[place(r, 2u * ch)], x1 = o[place(r, 2u * ch + 1u)];
+            x[0] += x0.x * f, x[1] += x0.y * f, x[2] += x0.z * f, x[3] += x0.w * f;
+            x[4] += x1.x * f, x[5] += x1.y * f, x[6] += x1.z * f, x[7] += x1.w * f;
+        }
+        if (whole) {
+            const int32_t t = at / int32_t(a.group), hg = at - t * int32_t(a.group);
+            const uint32_t head = kvh * a.group + uint32_t(hg);
+            const int64_t token = w.q_start + t;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees no key gives 0
+            V8 y;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) y[j] = E(x[j] * inv);
+            *reinterpret_cast<V8 *>(static_cast<E *>(a.out) + token * a.out_stride[0] + int64_t(head) * a.out_stride[1] +
+                                    ch * 8u) = y;
+            if (a.lse && ch == 0)
+                a.lse[token * a.heads + head] =
+                    sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
+        } else {
+            const uint64_t pr = slot + uint32_t(at - w.row0);
+            float4 *o = reinterpret_cast<float4 *>(a.part_o + pr * DP + ch * 8u);
+            o[0] = float4{x[0], x[1], x[2], x[3]};
+            o[1] = float4{x[4], x[5], x[6], x[7]};
+            if (ch == 0) *reinterpret_cast<float2 *>(a.part_ml + 2u * pr) = float2{top, sum};
+        }
+    }
+}
+
+// The pieces of a split tile joined: a wavefront per row, 16-byte pieces of
+// the row along the lanes and several pieces of work at a time.
+template <typename E, int DP>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
+    using T = Type<E>;
+    constexpr uint32_t CPR = DP / 4;                   // float4 pieces per row
+    constexpr uint32_t SL = CPR >= 64 ? 1 : 64 / CPR;  // pieces of work side by side
+    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
+    if (index >= *a.count) return;
+    const Piece w = get_piece(a, index);
+    if (w.split != 0 || w.splits == 1 || w.q_len <= 0) return;
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    const uint32_t ch = lane % CPR, sl = lane / CPR;
+    const uint32_t splits = uint32_t(w.splits);
+    const uint32_t rows = uint32_t(min(int64_t(a.rows_per_tile), int64_t(w.q_len) * a.group - w.row0));
+    for (uint32_t r = blockIdx.y * 32u + wave; r < min(rows, blockIdx.y * 32u + 32u); r += kWaves) {
+        auto at = [&](uint32_t s) {
+            return (uint64_t(uint32_t(w.slot) + s) * a.kv_heads + kvh) * a.rows_per_tile + r;
+        };
+        float top = -INFINITY;
+        for (uint32_t s = lane; s < splits; s += kWave) top = fmaxf(top, a.part_ml[2u * at(s)]);
+#pragma unroll
+        for (int d = 32; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+        float sum = 0.0f;
+        float4 x{0, 0, 0, 0};
+#pragma unroll 4
+        for (uint32_t s = sl; s < splits; s += SL) {
+            const uint64_t pr = at(s);
+            const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2u * pr);
+            const float4 o = *reinterpret_cast<const float4 *>(a.part_o + pr * DP + 4u * ch);
+            const float f = v.x == top ? 1.0f : __builtin_amdgcn_exp2f((v.x - top) * a.scale_log2);
+            sum += v.y * f;
+            x.x += o.x * f, x.y += o.y * f, x.z += o.z * f, x.w += o.w * f;
+        }
+#pragma unroll
+        for (uint32_t d = CPR; d < 64u; d *= 2) {
+            sum += __shfl_xor(sum, int(d));
+            x.x += __shfl_xor(x.x, int(d));
+            x.y += __shfl_xor(x.y, int(d));
+            x.z += __shfl_xor(x.z, int(d));
+            x.w += __shfl_xor(x.w, int(d));
+        }
+        if (sl != 0 || ch * 4u >= a.dim) continue;
+        const uint32_t gr = uint32_t(w.row0) + r;
+        const uint32_t t = gr / a.group, head = kvh * a.group + gr % a.group;
+        const int64_t token = int64_t(w.q_start) + t;
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        using E4 = __attribute__((ext_vector_type(4))) E;
+        const E4 y = {E(x.x * inv), E(x.y * inv), E(x.z * inv), E(x.w * inv)};
+        *reinterpret_cast<E4 *>(static_cast<E *>(a.out) + token * a.out_stride[0] + int64_t(head) * a.out_stride[1] +
+                                4u * ch) = y;
+        if (a.lse && ch == 0)
+            a.lse[token * a.heads + head] =
+                sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
+    }
+}
+
+// ------------------------------------------------------------------ launch
+
+// The launch's shape, from what the host knows: sizes only.
+struct LaunchPlan {
+    int rw, kt, dp;
+    uint32_t rows_per_tile, min_piece, targets, piece_cap, slot_cap;
+    uint64_t off_pieces, off_ml, off_o, bytes;
+};
+
+LaunchPlan launch_plan(const dfc_attention_args &a) {
+    LaunchPlan p;
+    const uint32_t group = a.heads / a.cache.kv_heads;
+    p.dp = a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256;
+    // most rows a request has per cache head
+    const uint64_t most = std::min<uint64_t>(a.max_q_len ? a.max_q_len : a.tokens, a.tokens) * group;
+    // one wavefront holds a whole key tile of K and V on its way to LDS: too
+    // many registers at 256 columns
+    p.rw = most <= 32 && p.dp <= 128 ? 1 : most <= 64 ? 2 : 4;
+    p.kt = p.rw == 4 && p.dp <= 128 ? 64 : 32;
+    p.rows_per_tile = 32u * uint32_t(p.rw);
+    const uint32_t kw = kWaves / uint32_t(p.rw);
+    // a piece has at least 256 keys (512 where tiles are large: their partial
+    // results cost more), and there are up to four pieces a resident
+    // workgroup (two)
+    p.min_piece = (p.rw == 4 ? 512u : 256u) / uint32_t(p.kt);
+    p.min_piece = std::max(p.min_piece, kw);
+    p.targets = 512u * (p.rw == 4 ? 2u : 4u);
+    const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
+                                              uint64_t(a.tokens) * group);
+    const uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt));
+    // a tile of c key tiles has ceil(c / piece) pieces, and the c add up to
+    // at most targets / kv_heads pieces
+    const uint64_t extra = std::min<uint64_t>(p.targets / a.cache.kv_heads + 1u, tiles * (longest / p.min_piece + 1u));
+    p.piece_cap = uint32_t(std::min<uint64_t>(tiles + extra, 0x7fffffffu));
+    p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, p.piece_cap));
+    p.off_pieces = 256;
+    p.off_ml = p.off_pieces + uint64_t(p.piece_cap) * sizeof(Piece);
+    const uint64_t rows = uint64_t(p.slot_cap) * a.cache.kv_heads * p.rows_per_tile;
+    p.off_o = (p.off_ml + rows * 8u + 255u) & ~uint64_t(255);
+    p.bytes = p.off_o + rows * uint64_t(p.dp) * 4u;
+    return p;
+}
+
+dfc_status check_attention(const dfc_attention_args &a) {
+    const dfc_status cs = dfc::check_cache(a.cache);
+    if (cs != DFC_OK) return cs;
+    if (!a.heads || a.heads % a.cache.kv_heads || a.heads > 65536u) return DFC_EINVAL;
+    if (a.tokens > 0x7fffffffull || a.n_requests > 0x7fffffffu) return DFC_EINVAL;
+    // rows (tokens x heads of a group) are counted in 32 bits
+    if (a.tokens * (a.heads / a.cache.kv_heads) > 0x7fffff00ull) return DFC_EUNSUPPORTED;
+    if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return DFC_EINVAL;
+    if (a.window > 0x7fffffffu) return DFC_EINVAL;
+    return DFC_OK;
+}
+
+template <typename E, int DP, int RW, int KT>
+dfc_status launch(const AttnArgs &a, hipStream_t st) {
+    using Sh = Shape<E, DP, RW, KT>;
+    const void *fn = reinterpret_cast<const void *>(&attention_kernel<E, DP, RW, KT>);
+    if (!allow_full_lds(fn)) return DFC_EHIP;
+    const uint64_t grid = uint64_t(a.piece_cap) * a.kv_heads;
+    if (grid > 0x7fffffffull) return DFC_EUNSUPPORTED;
+    hipLaunchKernelGGL(schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, a);
+    hipLaunchKernelGGL((attention_kernel<E, DP, RW, KT>), dim3(uint32_t(grid)), dim3(kThreads), Sh::kLds, st, a);
+    if (a.slot_cap)
+        hipLaunchKernelGGL((join_kernel<E, DP>), dim3(uint32_t(grid), uint32_t(RW)), dim3(kThreads), 0, st, a);
+    return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
+}
+
+template <typename E>
+dfc_status launch_type(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
+    switch (p.dp * 8 + p.rw) {
+        case 64 * 8 + 1: return launch<E, 64, 1, 32>(a, st);
+        case 64 * 8 + 2: return launch<E, 64, 2, 32>(a, st);
+        case 64 * 8 + 4: return launch<E, 64, 4, 64>(a, st);
+        case 128 * 8 + 1: return launch<E, 128, 1, 32>(a, st);
+        case 128 * 8 + 2: return launch<E, 128, 2, 32>(a, st);
+        case 128 * 8 + 4: return launch<E, 128, 4, 64>(a, st);
+        case 256 * 8 + 2: return launch<E, 256, 2, 32>(a, st);
+        default: return launch<E, 256, 4, 32>(a, st);
+    }
+}
+
+}  // namespace
+
+extern "C" {
+
+dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_t *bytes) {
+    if (!args || !bytes) return DFC_EINVAL;
+    const dfc_status s = check_attention(*args);
+    if (s != DFC_OK) return s;
+    *bytes = args->tokens && args->n_requests ? launch_plan(*args).bytes : 0;
+    return DFC_OK;
+}
+
+dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_attention_args &in = *args;
+    const dfc_status s = check_attention(in);
+    if (s != DFC_OK) return s;
+    if (!in.tokens || !in.n_requests) return DFC_OK;
+    if (!in.q_dev || !in.out_dev || !in.cu_q || !in.seq_lens || !in.workspace_dev) return DFC_EINVAL;
+    if (in.max_pages && !in.block_table) return DFC_EINVAL;
+    if (in.table_stride < int64_t(in.max_pages)) return DFC_EINVAL;
+    if ((reinterpret_cast<uintptr_t>(in.q_dev) | reinterpret_cast<uintptr_t>(in.out_dev)) & 15u) return DFC_EINVAL;
+    if (reinterpret_cast<uintptr_t>(in.workspace_dev) & 255u) return DFC_EINVAL;
+    for (int i = 0; i < 2; ++i)
+        if (in.q_stride[i] % 8 || in.out_stride[i] % 8) return DFC_EINVAL;
+    const LaunchPlan p = launch_plan(in);
+    if (in.workspace_bytes < p.bytes) return DFC_ESIZE;
+    AttnArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = in.q_dev;
+    a.k = in.cache.k_dev;
+    a.v = in.cache.v_dev;
+    a.out = in.out_dev;
+    a.lse = in.lse_dev;
+    a.table = in.block_table;
+    a.cu_q = in.cu_q;
+    a.seq_lens = in.seq_lens;
+    for (int i = 0; i < 2; ++i) {
+        a.q_stride[i] = in.q_stride[i];
+        a.out_stride[i] = in.out_stride[i];
+    }
+    for (int i = 0; i < 3; ++i) {
+        a.k_stride[i] = in.cache.k_stride[i];
+        a.v_stride[i] = in.cache.v_stride[i];
+    }
+    a.table_stride = in.table_stride;
+    a.n_pages = in.cache.n_pages;
+    a.page_shift = dfc::log2_of(in.cache.page_size);
+    a.kv_heads = in.cache.kv_heads;
+    a.heads = in.heads;
+    a.group = in.heads / in.cache.kv_heads;
+    a.dim = in.cache.head_dim;
+    a.n_requests = in.n_requests;
+    a.tokens = uint32_t(in.tokens);
+    a.max_pages = in.max_pages;
+    a.window = in.window;
+    a.causal = in.causal ? 1 : 0;
+    a.scale = in.scale;
+    a.scale_log2 = in.scale * 1.44269504088896340736f;
+    a.rows_per_tile = p.rows_per_tile;
+    a.key_tile = uint32_t(p.kt);
+    a.min_piece = p.min_piece;
+    a.targets = p.targets;
+    a.piece_cap = p.piece_cap;
+    a.slot_cap = p.slot_cap;
+    uint8_t *ws = static_cast<uint8_t *>(in.workspace_dev);
+    a.count = reinterpret_cast<uint32_t *>(ws);
+    a.pieces = reinterpret_cast<Piece *>(ws + p.off_pieces);
+    a.part_ml = reinterpret_cast<float *>(ws + p.off_ml);
+    a.part_o = reinterpret_cast<float *>(ws + p.off_o);
+    a.status = in.status_dev;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    return in.cache.dtype == DFC_BF16 ? launch_type<__bf16>(a, p, st) : launch_type<_Float16>(a, p, st);
+}
+
+}  // extern "C"

@@ -1,0 +1,359 @@
+// dfc_paged.hip - the paged key/value cache of a serving program: the plan of
+// a step (pages, slots and positions from request lengths) and the append of
+// a step's keys and values (with the rotary embedding).
+//
+// dfc_paged_plan.  Request r holds c_r tokens and brings n_r: with pages of P
+// tokens it has ceil(c_r / P) pages and needs ceil((c_r + n_r) / P).  The
+// missing ones come off the ring of free pages in request order, so request
+// r's first new page is the exclusive sum of the missing pages before it, and
+// its first new token is the exclusive sum of the new tokens before it.
+//
+// dfc_paged_append.  Token t's keys and values go to row slots[t] of the
+// cache, rounded to its type; q and k are first rotated by the angles of
+// their position: (a, b) -> (a cos - b sin, b cos + a sin) over the pairs
+// (i, i + half) or (2i, 2i + 1).
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+
+#include "dfc.h"
+#include "dfc_decode_core.h"
+#include "dfc_paged.h"
+
+namespace {
+
+// ------------------------------------------------------------------- plan
+
+constexpr uint32_t kPlanThreads = 1024;
+constexpr uint32_t kPlanWaves = kPlanThreads / kWave;
+
+struct PlanArgs {
+    dfc_plan_args a;
+    uint32_t page_shift;
+};
+
+// Exclusive prefix sums of (x, y) over the workgroup; the totals come back in
+// sum_x and sum_y.  `part` is 2 * kPlanWaves values of LDS.
+__device__ __forceinline__ void scan2(uint64_t &x, uint64_t &y, uint64_t &sum_x, uint64_t &sum_y, uint64_t *part) {
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
+    uint64_t ix = x, iy = y;
+#pragma unroll
+    for (int d = 1; d < kWave; d *= 2) {
+        const uint64_t ux = __shfl_up(ix, d), uy = __shfl_up(iy, d);
+        if (lane >= uint32_t(d)) {
+            ix += ux;
+            iy += uy;
+        }
+    }
+    __syncthreads();  // the previous scan's part has been read
+    if (lane == kWave - 1) {
+        part[wave] = ix;
+        part[kPlanWaves + wave] = iy;
+    }
+    __syncthreads();
+    uint64_t bx = 0, by = 0;
+    sum_x = sum_y = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kPlanWaves; ++w) {
+        const uint64_t px = part[w], py = part[kPlanWaves + w];
+        if (w < wave) {
+            bx += px;
+            by += py;
+        }
+        sum_x += px;
+        sum_y += py;
+    }
+    x = bx + ix - x;
+    y = by + iy - y;
+}
+
+// The last j in [0, n) with key[j] <= t (key ascending, key[0] <= t).
+__device__ __forceinline__ uint32_t last_at_most(const uint64_t *key, uint32_t n, uint64_t t) {
+    uint32_t lo = 0, hi = n;
+    while (hi - lo > 1) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (key[mid] <= t)
+            lo = mid;
+        else
+            hi = mid;
+    }
+    return lo;
+}
+
+// Every workgroup scans all requests (1,024 at a time) and then writes its
+// share of the step's tokens and new pages, in groups of 1,024 dealt out in
+// turn: no workgroup waits for another, and one launch does it all.  Tokens
+// and pages find their request by binary search in the scanned starts.
+__global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
+    __shared__ uint64_t part[2 * kPlanWaves];
+    __shared__ uint64_t tok_start[kPlanThreads], page_start[kPlanThreads];
+    __shared__ uint32_t ctx_of[kPlanThreads], have_of[kPlanThreads], need_of[kPlanThreads];
+    const dfc_plan_args &a = p.a;
+    const uint32_t tid = threadIdx.x, b = blockIdx.x, nb = gridDim.x;
+    const uint32_t P = a.page_size, shift = p.page_shift;
+    uint32_t bad = 0;
+    const int64_t head0 = a.cursor[0], tail0 = a.cursor[1];
+    const bool ring_ok = head0 >= 0 && tail0 >= head0 && uint64_t(tail0 - head0) <= a.n_ring;
+    const uint64_t avail = ring_ok ? uint64_t(tail0 - head0) : 0;
+    const uint64_t head = ring_ok ? uint64_t(head0) : 0;
+    if (!ring_ok) bad |= kStatusCorrupt;
+    // the page a ring rank stands for, or -1
+    auto ring_page = [&](uint64_t rank) -> int32_t {
+        if (rank >= avail) return -1;
+        const int32_t page = a.free_pages[(head + rank) % a.n_ring];
+        return page < 0 ? -1 : page;
+    };
+    uint64_t tok_base = 0, page_base = 0;
+    for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kPlanThreads) {
+        const uint32_t r = r0 + tid, n_here = min(kPlanThreads, a.n_requests - r0);
+        int32_t ctx = 0, n_new = 0;
+        if (r < a.n_requests) {
+            ctx = a.context_lens[r];
+            n_new = a.new_lens[r];
+            if (ctx < 0 || n_new < 0 || int64_t(ctx) + n_new > INT32_MAX) {
+                bad |= kStatusCorrupt;
+                ctx = max(ctx, 0);
+                n_new = min(max(n_new, 0), INT32_MAX - ctx);
+            }
+        }
+        const uint32_t total = uint32_t(ctx) + uint32_t(n_new);
+        const uint32_t have0 = (uint32_t(ctx) + P - 1) >> shift, need0 = (total + P - 1) >> shift;
+        if (need0 > a.max_pages) bad |= uint32_t(DFC_ESIZE);
+        const uint32_t have = min(have0, a.max_pages), need = min(need0, a.max_pages);
+        uint64_t ts = uint32_t(n_new), ps = need - have, t_sum, p_sum;
+        scan2(ts, ps, t_sum, p_sum, part);
+        ts += tok_base;
+        ps += page_base;
+        tok_start[tid] = ts;
+        page_start[tid] = ps;
+        ctx_of[tid] = uint32_t(ctx);
+        have_of[tid] = have;
+        need_of[tid] = need;
+        if (b == 0 && r < a.n_requests) {
+            a.seq_lens[r] = int32_t(total);
+            a.cu_q[r] = int32_t(min(ts, a.tokens));
+        }
+        __syncthreads();
+        // new pages of these requests
+        for (uint64_t g = page_base / kPlanThreads; g * kPlanThreads < page_base + p_sum; ++g) {
+            if (g % nb != b) continue;
+            const uint64_t j = g * kPlanThreads + tid;
+            if (j < page_base || j >= page_base + p_sum) continue;
+            const uint32_t k = last_at_most(page_start, n_here, j);
+            const int32_t page = ring_page(j);
+            if (page < 0) bad |= uint32_t(DFC_ESIZE);
+            a.block_table[int64_t(r0 + k) * a.table_stride + have_of[k] + (j - page_start[k])] = page;
+        }
+        // new tokens of these requests
+        const uint64_t t_end = min(tok_base + t_sum, a.tokens);
+        for (uint64_t g = tok_base / kPlanThreads; g * kPlanThreads < t_end; ++g) {
+            if (g % nb != b) continue;
+            const uint64_t t = g * kPlanThreads + tid;
+            if (t < tok_base || t >= t_end) continue;
+            const uint32_t k = last_at_most(tok_start, n_here, t);
+            const uint32_t pos = ctx_of[k] + uint32_t(t - tok_start[k]);
+            const uint32_t pi = pos >> shift;
+            int32_t page = -1;
+            if (pi < have_of[k]) {
+                page = a.block_table[int64_t(r0 + k) * a.table_stride + pi];
+                if (page < 0) bad |= kStatusCorrupt;
+            } else if (pi < need_of[k]) {
+                page = ring_page(page_start[k] + (pi - have_of[k]));
+            }
+            a.slots[t] = page < 0 ? -1 : (int64_t(page) << shift) + (pos & (P - 1));
+            a.positions[t] = int32_t(pos);
+        }
+        tok_base += t_sum;
+        page_base += p_sum;
+        __syncthreads();  // the starts have been read
+    }
+    if (tok_base > a.tokens) bad |= uint32_t(DFC_ESIZE);
+    // what is left of the capacity is padding
+    for (uint64_t t = tok_base + uint64_t(b) * kPlanThreads + tid; t < a.tokens; t += uint64_t(nb) * kPlanThreads) {
+        a.slots[t] = -1;
+        a.positions[t] = 0;
+    }
+    if (b == 0 && tid == 0) {
+        a.cu_q[a.n_requests] = int32_t(min(tok_base, a.tokens));
+        a.cursor_out[0] = head0 + int64_t(min(page_base, avail));
+        a.cursor_out[1] = tail0;
+    }
+    if (bad && a.status_dev) atomicOr(a.status_dev, bad);
+}
+
+// ----------------------------------------------------------------- append
+
+struct AppendArgs {
+    dfc_append_args a;
+    uint32_t page_shift;
+    uint32_t per_head, per_token;  // 8-value chunks of a head, of a token's q, k and v
+    uint64_t chunks;
+};
+
+__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
+    const float4 lo = *reinterpret_cast<const float4 *>(p), hi = *reinterpret_cast<const float4 *>(p + 4);
+    x[0] = lo.x, x[1] = lo.y, x[2] = lo.z, x[3] = lo.w;
+    x[4] = hi.x, x[5] = hi.y, x[6] = hi.z, x[7] = hi.w;
+}
+
+template <typename S>
+__device__ __forceinline__ void load8(const S *p, float (&x)[8]) {
+    using S8 = __attribute__((ext_vector_type(8))) S;
+    const S8 v = *reinterpret_cast<const S8 *>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = float(v[i]);
+}
+
+// One thread handles 8 values of one head of one token: it reads them (and
+// the 8 they pair with when the pairs lie half a rotation apart), rotates,
+// rounds to nearest even and writes 16 bytes.
+template <typename S, typename E>
+__global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
+    using E8 = __attribute__((ext_vector_type(8))) E;
+    const dfc_append_args &a = p.a;
+    const uint64_t base = uint64_t(blockIdx.x) * 256u;
+    if (base + threadIdx.x >= p.chunks) return;
+    // the block's first token by one uniform division, the rest in 32 bits
+    const uint64_t t_base = base / p.per_token;
+    const uint32_t rest = uint32_t(base - t_base * p.per_token) + threadIdx.x;
+    const uint64_t t = t_base + rest / p.per_token;
+    const uint32_t in_token = rest % p.per_token;
+    const uint32_t row = in_token / p.per_head, d = 8u * (in_token % p.per_head);
+    const uint32_t nk = a.cache.kv_heads;
+    // rows of a token: k heads, v heads, q heads
+    const uint32_t which = row < nk ? 0u : row < 2u * nk ? 1u : 2u;
+    const uint32_t h = row - (which == 0u ? 0u : which == 1u ? nk : 2u * nk);
+    const S *src;
+    E *dst;
+    if (which == 2u) {
+        src = static_cast<const S *>(a.q_dev) + int64_t(t) * a.q_stride[0] + int64_t(h) * a.q_stride[1];
+        dst = static_cast<E *>(a.q_out_dev) + int64_t(t) * a.q_out_stride[0] + int64_t(h) * a.q_out_stride[1];
+    } else {
+        const int64_t slot = a.slots[t];
+        const uint64_t page = uint64_t(slot) >> p.page_shift;
+        if (slot < 0) return;
+        if (page >= a.cache.n_pages) {
+            if (a.status_dev) atomicOr(a.status_dev, kStatusCorrupt);
+            return;
+        }
+        const int64_t in_page = slot & int64_t(a.cache.page_size - 1u);
+        const int64_t *st = which == 0u ? a.cache.k_stride : a.cache.v_stride;
+        dst = static_cast<E *>(which == 0u ? a.cache.k_dev : a.cache.v_dev) + int64_t(page) * st[0] + in_page * st[1] +
+              int64_t(h) * st[2];
+        src = which == 0u ? static_cast<const S *>(a.k_dev) + int64_t(t) * a.k_src_stride[0] + int64_t(h) * a.k_src_stride[1]
+                          : static_cast<const S *>(a.v_dev) + int64_t(t) * a.v_src_stride[0] + int64_t(h) * a.v_src_stride[1];
+    }
+    float x[8];
+    load8(src + d, x);
+    if (which != 1u && d < a.rot_dim) {
+        const uint32_t half = a.rot_dim / 2u;
+        int32_t pos = a.positions[t];
+        if (pos < 0 || uint32_t(pos) >= a.max_positions) {
+            if (a.status_dev) atomicOr(a.status_dev, kStatusCorrupt);
+            pos = 0;
+        }
+        const float *cs = a.rotary_dev + int64_t(pos) * a.rot_dim;
+        if (a.interleaved) {
+            const float4 co = *reinterpret_cast<const float4 *>(cs + d / 2u);
+            const float4 si = *reinterpret_cast<const float4 *>(cs + half + d / 2u);
+            const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float u = x[2 * i], w = x[2 * i + 1];
+                x[2 * i] = u * c[i] - w * s[i];
+                x[2 * i + 1] = w * c[i] + u * s[i];
+            }
+        } else {
+            const bool second = d >= half;
+            float y[8], c[8], s[8];
+            load8(src + (second ? d - half : d + half), y);
+            load8(cs + (second ? d - half : d), c);
+            load8(cs + (second ? d : d + half), s);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + (second ? y[i] : -y[i]) * s[i];
+        }
+    }
+    E8 out;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = E(x[i]);
+    *reinterpret_cast<E8 *>(dst + d) = out;
+}
+
+template <typename S, typename E>
+void launch_append(const AppendArgs &p, uint32_t blocks, hipStream_t stream) {
+    hipLaunchKernelGGL((append_kernel<S, E>), dim3(blocks), dim3(256), 0, stream, p);
+}
+
+bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+
+}  // namespace
+
+extern "C" {
+
+dfc_status dfc_paged_plan(const dfc_plan_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_plan_args &a = *args;
+    if (!dfc::is_pow2(a.page_size) || a.tokens > 0x7fffffffull || a.n_requests > 0x7fffffffu) return DFC_EINVAL;
+    if (!a.cursor || !a.cursor_out || a.cursor == a.cursor_out || !a.cu_q) return DFC_EINVAL;
+    if (a.n_requests && (!a.context_lens || !a.new_lens || !a.seq_lens || !a.block_table || !a.max_pages ||
+                         a.table_stride < int64_t(a.max_pages)))
+        return DFC_EINVAL;
+    // every workgroup reads the lengths while one writes seq_lens and cu_q
+    if (a.n_requests && (a.seq_lens == a.context_lens || a.seq_lens == a.new_lens || a.cu_q == a.context_lens ||
+                         a.cu_q == a.new_lens))
+        return DFC_EINVAL;
+    if (a.tokens && (!a.slots || !a.positions)) return DFC_EINVAL;
+    if (!a.n_ring || !a.free_pages) return DFC_EINVAL;
+    PlanArgs p{a, dfc::log2_of(a.page_size)};
+    const uint32_t groups = uint32_t(dfc::ceil_div(a.tokens, uint64_t(kPlanThreads)));
+    const uint32_t blocks = std::min(std::max(groups, 1u), 256u);
+    hipLaunchKernelGGL(plan_kernel, dim3(blocks), dim3(kPlanThreads), 0, static_cast<hipStream_t>(stream), p);
+    return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
+}
+
+dfc_status dfc_paged_append(const dfc_append_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_append_args &a = *args;
+    const dfc_status cs = dfc::check_cache(a.cache);
+    if (cs != DFC_OK) return cs;
+    if (a.tokens > 0x7fffffffull) return DFC_EINVAL;
+    if (a.source_dtype != DFC_BF16 && a.source_dtype != DFC_F16 && a.source_dtype != DFC_F32) return DFC_EUNSUPPORTED;
+    if (a.source_dtype != DFC_F32 && a.source_dtype != a.cache.dtype) return DFC_EUNSUPPORTED;
+    if (a.rot_dim % 16u || a.rot_dim > a.cache.head_dim) return DFC_EINVAL;
+    if (a.rot_dim && (!a.rotary_dev || !a.max_positions || !aligned16(a.rotary_dev))) return DFC_EINVAL;
+    if (a.q_heads > 65536u) return DFC_EINVAL;
+    if (!a.tokens) return DFC_OK;
+    if (!a.k_dev || !a.v_dev || !a.slots || (a.rot_dim && !a.positions)) return DFC_EINVAL;
+    if (a.q_heads && (!a.q_dev || !a.q_out_dev)) return DFC_EINVAL;
+    if (!aligned16(a.k_dev) || !aligned16(a.v_dev)) return DFC_EINVAL;
+    // strides in whole 16-byte pieces
+    const int64_t unit = a.source_dtype == DFC_F32 ? 4 : 8;
+    for (int i = 0; i < 2; ++i)
+        if (a.k_src_stride[i] % unit || a.v_src_stride[i] % unit) return DFC_EINVAL;
+    if (a.q_heads) {
+        if (!aligned16(a.q_dev) || !aligned16(a.q_out_dev)) return DFC_EINVAL;
+        for (int i = 0; i < 2; ++i)
+            if (a.q_stride[i] % unit || a.q_out_stride[i] % 8) return DFC_EINVAL;
+        // a chunk is read again by the thread of the chunk it pairs with
+        if (a.rot_dim && a.q_dev == a.q_out_dev) return DFC_EINVAL;
+    }
+    AppendArgs p;
+    p.a = a;
+    p.page_shift = dfc::log2_of(a.cache.page_size);
+    p.per_head = a.cache.head_dim / 8u;
+    p.per_token = p.per_head * (a.q_heads + 2u * a.cache.kv_heads);
+    p.chunks = uint64_t(p.per_token) * a.tokens;
+    const uint64_t blocks = dfc::ceil_div(p.chunks, uint64_t(256));
+    if (blocks > 0x7fffffffull) return DFC_EUNSUPPORTED;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const bool bf = a.cache.dtype == DFC_BF16;
+    if (a.source_dtype == DFC_F32)
+        bf ? launch_append<float, __bf16>(p, uint32_t(blocks), st) : launch_append<float, _Float16>(p, uint32_t(blocks), st);
+    else
+        bf ? launch_append<__bf16, __bf16>(p, uint32_t(blocks), st)
+           : launch_append<_Float16, _Float16>(p, uint32_t(blocks), st);
+    return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
+}
+
+}  // extern "C"

@@ -1,0 +1,622 @@
+"""GPU: the paged key/value cache (dfc_paged_plan, dfc_paged_append,
+dfc_paged_attention) against the oracle's definitions in 64 bits.
+
+Every cache starts as NaN, so a value that an operator should not have read
+shows.  Bounds on the attention's error come from the formula: weights are
+rounded to the cache's type once (relative u = 2^-8 for bfloat16, 2^-11 for
+float16) and so is the output, scores accumulate dim products in fp32 and go
+through one multiply-add and one exponential; the sums over N keys are in
+fp32.  With A the largest sum of |scale q_i k_i| and Z the largest |score| of
+a row, a weight and a sum are off by a factor of at most 1 + e,
+e = 2^-23 (dim A + 2 Z + N + 16), and
+|out - ref| <= (u + 2 e) sum_j w_j |v_j| + u |ref|; float16 weights below
+2^-24 of their scaled range lose all bits, N 2^-32 max |v| at most."""
+import sys
+
+import numpy as np
+import pytest
+
+import lossless_entropy_coded_dfc_amd as dfc
+from oracle import paged as op
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}
+
+
+def say(*a):
+    print(*a, file=sys.stderr, flush=True)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def as64(t):
+    return t.detach().cpu().double().numpy()
+
+
+class Step:
+    """Requests with `total` tokens of which `new` are the step's, their keys
+    and values scattered over the pages of a cache that is NaN elsewhere."""
+
+    def __init__(self, total, new, heads, kv_heads, dim, page, dtype, seed=0, extra_pages=0, order="phd"):
+        g = torch.Generator().manual_seed(seed)
+        self.total, self.new, self.page = total, new, page
+        need = [-(-t // page) for t in total]
+        width = max(need + [1]) + extra_pages
+        n_pages = sum(need) + 2
+        perm = torch.randperm(n_pages, generator=g)
+        self.table = torch.full((len(total), width), -1, dtype=torch.int32)
+        shape = (n_pages, page, kv_heads, dim)
+        self.k, self.v = (torch.full(shape, float("nan"), dtype=dtype) for _ in range(2))
+        at = 0
+        for r, t in enumerate(total):
+            self.table[r, : need[r]] = perm[at: at + need[r]].int()
+            at += need[r]
+            for c in (self.k, self.v):
+                rows = torch.randn(t, kv_heads, dim, generator=g).to(dtype)
+                for j in range(t):
+                    c[self.table[r, j // page], j % page] = rows[j]
+        self.q = (1.5 * torch.randn(sum(new), heads, dim, generator=g)).to(dtype)
+        self.cu = torch.tensor([0] + list(np.cumsum(new)), dtype=torch.int32)
+        self.lens = torch.tensor(total, dtype=torch.int32)
+        self.order = order
+
+    def cache(self, c):
+        """On the device; order "hpd": heads outside the tokens of a page."""
+        if self.order == "hpd":
+            return c.permute(0, 2, 1, 3).contiguous().cuda().permute(0, 2, 1, 3)
+        return c.cuda()
+
+    def run(self, scale=None, **kw):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out = torch.full(self.q.shape, float("nan"), dtype=self.q.dtype, device="cuda")
+        lse = torch.full(self.q.shape[:2], float("nan"), dtype=torch.float32, device="cuda")
+        dfc.paged_attention(self.q.cuda(), self.cache(self.k), self.cache(self.v), self.table.cuda(), self.cu.cuda(),
+                            self.lens.cuda(), scale=scale, out=out, lse=lse, status=status, **kw)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        return out, lse
+
+    def check(self, out, lse, scale=None, causal=True, window=0, rows=None):
+        """Every row against the definition, or the first `rows` rows of the
+        first request."""
+        dim = self.q.shape[2]
+        scale = dim ** -0.5 if scale is None else scale
+        u = U[self.q.dtype]
+        got, got_lse, q = as64(out), as64(lse), as64(self.q)
+        for r in range(len(self.total) if rows is None else 1):
+            a, b = int(self.cu[r]), int(self.cu[r + 1])
+            n = self.total[r]
+            if a == b:
+                continue
+            if rows is not None:
+                n -= b - rows
+                b = rows
+            k, v = (op.gather(as64(c), self.table[r].numpy(), self.page, n) for c in (self.k, self.v))
+            ref, ref_lse, spread, top, mass = op.attention(q[a:b], k, v, scale, causal, window)
+            e = 2.0 ** -23 * (dim * mass + 2 * top + n + 16)[..., None]
+            lost = 2.0 ** -32 * n * np.abs(v).max(initial=0.0)
+            bound = (u + 2 * e) * spread + u * np.abs(ref) + lost + 1e-30
+            assert np.isfinite(got[a:b]).all(), r
+            assert (np.abs(got[a:b] - ref) <= bound).all(), (r, np.abs(got[a:b] - ref).max())
+            empty = np.isneginf(ref_lse)
+            assert np.isneginf(got_lse[a:b][empty]).all() and (got[a:b][empty] == 0).all()
+            diff = np.where(empty, 0, got_lse[a:b]) - np.where(empty, 0, ref_lse)
+            assert (np.abs(diff) <= 4 * e[..., 0] + 2.0 ** -21 * (1 + np.abs(np.where(empty, 0, ref_lse)))).all(), r
+
+
+CASES = [
+    # total, new, heads, kv_heads, dim, page
+    ([1], [1], 1, 1, 64, 16),
+    ([700], [1], 32, 8, 128, 16),
+    ([1, 2, 31, 32, 33, 64, 65, 127, 300], [1] * 9, 8, 2, 128, 16),
+    ([515, 64, 40], [5, 5, 5], 16, 4, 128, 32),
+    ([130, 77], [130, 77], 8, 2, 128, 16),
+    ([333], [129], 4, 4, 64, 16),
+    ([190, 65, 300, 1], [67, 1, 1, 1], 6, 2, 80, 8),
+    ([97, 200], [33, 1], 3, 1, 256, 64),
+    ([260], [2], 64, 1, 256, 16),
+    ([50, 129], [3, 40], 5, 5, 24, 4),
+    ([70, 33], [70, 2], 4, 2, 128, 1),
+    ([140], [1], 7, 1, 200, 256),
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention_against_the_definition(case, dtype):
+    total, new, heads, kv_heads, dim, page = CASES[case]
+    s = Step(total, new, heads, kv_heads, dim, page, dtype, seed=case)
+    for hint in (0, max(new)):
+        say("attention", case, dtype, "hint", hint)
+        s.check(*s.run(max_q_len=hint))
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 100, 2 ** 31 - 1])
+def test_attention_window(window):
+    s = Step([300, 90, 64], [70, 1, 64], 8, 2, 128, 16, torch.bfloat16, seed=window % 1000)
+    say("window", window)
+    s.check(*s.run(window=window), window=window)
+    say("window, not causal", window)
+    s.check(*s.run(window=window, causal=False), window=window, causal=False)
+
+
+def test_attention_without_the_causal_mask():
+    s = Step([300, 90, 64], [70, 1, 64], 8, 2, 64, 16, torch.float16, seed=3)
+    say("not causal")
+    s.check(*s.run(causal=False), causal=False)
+
+
+def test_rows_that_see_nothing():
+    # no tokens at all, more rows than tokens, a request without rows
+    s = Step([0, 3, 40, 17], [1, 5, 0, 1], 4, 2, 128, 16, torch.bfloat16, seed=4)
+    for hint in (0, 5, 1):
+        say("rows that see nothing, hint", hint)
+        s.check(*s.run(max_q_len=hint))
+
+
+def test_attention_splits_and_joins_long_keys():
+    # enough keys for several pieces of a tile, in each tile height
+    for new, heads, kv_heads in ((1, 4, 2), (9, 8, 2), (40, 4, 1)):
+        s = Step([9000], [new], heads, kv_heads, 64, 64, torch.float16, seed=new)
+        say("split", new)
+        s.check(*s.run(max_q_len=new))
+
+
+def test_extreme_scores():
+    # scores of tens of thousands: one key has all the weight; and a constant
+    # score, where every key has the same
+    s = Step([200, 70], [20, 1], 4, 2, 128, 16, torch.bfloat16, seed=6)
+    say("scale 300")
+    s.check(*s.run(scale=300.0), scale=300.0)
+    say("scale 1e-30")
+    s.check(*s.run(scale=1e-30), scale=1e-30)
+
+
+def test_float16_small_weights_add_up():
+    # one key far above 60,000 equal ones, whose weights are 2^-20 of its own
+    n = 60000
+    s = Step([8], [1], 1, 1, 64, 8, torch.float16, seed=7)
+    pages = n // 8
+    s.k, s.v = torch.zeros(pages, 8, 1, 64, dtype=torch.float16), torch.ones(pages, 8, 1, 64, dtype=torch.float16)
+    s.table = torch.arange(pages, dtype=torch.int32)[None]
+    s.total, s.lens = [n], torch.tensor([n], dtype=torch.int32)
+    s.q.zero_()
+    s.q[0, 0, 0] = 16.0
+    s.k[3, 5, 0, 0] = 20 * np.log(2.0) / 2   # its score: 0.125 x 16 x this
+    s.v[3, 5] = 0.0
+    scale = 0.125
+    say("float16 small weights")
+    out, lse = s.run(scale=scale)
+    z = scale * 16.0 * float(s.k[3, 5, 0, 0])
+    share = (n - 1) / (n - 1 + np.exp(z))
+    # a weight of 2^-20 is held above 2^-14, with all its bits: one rounding
+    # of the weights, one of the output, and sums of n fp32 terms
+    assert np.abs(as64(out) - share).max() <= share * (2 * 2.0 ** -11 + n * 2.0 ** -24)
+    assert abs(float(lse[0, 0]) - np.log(n - 1 + np.exp(z))) <= n * 2.0 ** -24
+
+
+@pytest.mark.parametrize("bad", [float("inf"), float("-inf"), float("nan")])
+def test_values_that_are_not_finite_in_masked_places(bad):
+    # tokens 60 and 100 of 130 new ones: rows before them must not notice
+    for dtype in (torch.bfloat16, torch.float16):
+        s = Step([150, 40], [130, 1], 4, 2, 128, 16, dtype, seed=8)
+        clean = s.run()
+        for tok in (80, 120):
+            p, j = s.table[0, tok // 16], tok % 16
+            s.v[p, j, 0, 5] = bad
+            s.k[p, j, 1, 7] = bad
+        say("not finite", bad, dtype)
+        out, lse = s.run()
+        # token i stands at 20 + i: those before 80 see neither key
+        i = 60
+        s.check(out, lse, rows=i)
+        assert torch.isfinite(out[130:].float()).all() and torch.equal(out[130:], clean[0][130:])
+        # those that see it: their weight is above 0, so the value is theirs
+        seen = out[i:130, :2, 5].float().cpu()
+        want = float("nan") if bad != bad else bad
+        first = seen[:40]  # rows 60..99 see one of the two
+        assert torch.isnan(first).all() if want != want else (first == want).all()
+        others = out[i:130, :2, :5].float()
+        assert torch.isfinite(others).all()
+        # head group 1 has the key: a score of inf or NaN makes NaN, -inf nothing
+        assert torch.isfinite(lse[:i]).all()
+
+
+def test_strides_and_streams():
+    s = Step([140, 33], [67, 33], 8, 2, 128, 16, torch.bfloat16, seed=9, order="hpd", extra_pages=3)
+    say("cache with heads outside the page")
+    s.check(*s.run())
+    # q and out inside wider rows, on a stream that is not the current one
+    wide = torch.zeros(s.q.shape[0], 3, 8, 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, 1] = s.q.cuda()
+    out = torch.full_like(wide, float("nan"))
+    lse = torch.full(s.q.shape[:2], float("nan"), device="cuda")
+    k, v, table, cu, lens = s.cache(s.k), s.cache(s.v), s.table.cuda(), s.cu.cuda(), s.lens.cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    say("strided rows, side stream")
+    dfc.paged_attention(wide[:, 1], k, v, table, cu, lens, out=out[:, 1], lse=lse, stream=side.cuda_stream)
+    side.synchronize()
+    s.check(out[:, 1], lse)
+    assert torch.isnan(out[:, 0]).all() and torch.isnan(out[:, 2]).all()
+
+
+def test_page_offsets_past_32_bits():
+    # 40,000 pages of 128 x 8 x 128: K is 10.5 GB, and the pages used lie at its end
+    n, page, kv_heads, dim = 40000, 128, 8, 128
+    s = Step([700, 129], [3, 129], 16, kv_heads, dim, page, torch.bfloat16, seed=10)
+    k, v = (torch.empty(n, page, kv_heads, dim, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    used = s.k.shape[0]
+    k[n - used:], v[n - used:] = s.k.cuda(), s.v.cuda()
+    table = torch.where(s.table >= 0, s.table + (n - used), s.table).cuda()
+    out, lse = torch.empty(s.q.shape, dtype=s.q.dtype, device="cuda"), torch.empty(s.q.shape[:2], device="cuda")
+    say("offsets past 32 bits")
+    dfc.paged_attention(s.q.cuda(), k, v, table, s.cu.cuda(), s.lens.cuda(), out=out, lse=lse)
+    torch.cuda.synchronize()
+    s.check(out, lse)
+    # and the append's
+    slots = torch.tensor([(n - 1) * page + 127, (n - 2) * page], device="cuda")
+    x = torch.randn(2, kv_heads, dim, device="cuda").bfloat16()
+    dfc.paged_append(x, -x, k, v, slots)
+    torch.cuda.synchronize()
+    assert torch.equal(k[n - 1, 127], x[0]) and torch.equal(v[n - 2, 0], -x[1])
+
+
+def test_same_bits_again_and_no_stale_workspace():
+    s = Step([2500, 800, 90], [5, 1, 90], 8, 2, 128, 16, torch.bfloat16, seed=11)
+    need = dfc.paged_attention_workspace(s.q.cuda(), s.cache(s.k), s.cache(s.v), s.table.cuda(), s.cu.cuda(),
+                                         s.lens.cuda())
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    first = None
+    for fill in (0xFF, 0x00, 0x5A):
+        ws.fill_(fill)
+        say("workspace fill", fill)
+        got = s.run(workspace=ws)
+        assert first is None or (torch.equal(got[0], first[0]) and torch.equal(got[1], first[1]))
+        first = got
+
+
+def test_lengths_and_pages_that_make_no_sense():
+    s = Step([300, 90], [2, 1], 4, 2, 128, 16, torch.bfloat16, seed=12)
+    args = [s.q.cuda(), s.k.cuda(), s.v.cuda()]
+    for name, table, cu, lens in (
+            ("page past the cache", s.table.clone().index_fill_(1, torch.tensor([2]), 10 ** 6), s.cu, s.lens),
+            ("missing page", s.table.clone().index_fill_(1, torch.tensor([1]), -1), s.cu, s.lens),
+            ("length past the table", s.table, s.cu, torch.tensor([10 ** 9, 90], dtype=torch.int32)),
+            ("negative length", s.table, s.cu, torch.tensor([-5, 90], dtype=torch.int32)),
+            ("rows past q", s.table, torch.tensor([0, 2, 900], dtype=torch.int32), s.lens),
+            ("descending rows", s.table, torch.tensor([0, 3, 1], dtype=torch.int32), s.lens),
+            ("negative rows", s.table, torch.tensor([-7, 2, 3], dtype=torch.int32), s.lens)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        say(name)
+        dfc.paged_attention(*args, table.cuda(), cu.cuda(), lens.cuda(), status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == dfc.ECORRUPT, name
+
+
+def test_attention_refusals():
+    s = Step([30], [2], 4, 2, 128, 16, torch.bfloat16, seed=13)
+    q, k, v, t, cu, lens = (s.q.cuda(), s.k.cuda(), s.v.cuda(), s.table.cuda(), s.cu.cuda(), s.lens.cuda())
+    go = dfc.paged_attention
+    with pytest.raises(TypeError):
+        go(q.half(), k, v, t, cu, lens)
+    with pytest.raises(TypeError):
+        go(q.float(), k.float(), v.float(), t, cu, lens)
+    with pytest.raises(TypeError):
+        go(q.cpu(), k, v, t, cu, lens)
+    with pytest.raises(TypeError):
+        go(q, k, v, t.long(), cu, lens)
+    with pytest.raises(TypeError):
+        go(q, k, v, t, cu.long(), lens)
+    with pytest.raises(ValueError):
+        go(q[:, :3].contiguous(), k, v, t, cu, lens)
+    with pytest.raises(ValueError):
+        go(q, k, v, t, cu[:1], lens)
+    with pytest.raises(ValueError):
+        go(q, k, v, t, cu, lens, window=-1)
+    with pytest.raises(ValueError):
+        go(q, k, v, t, cu, lens, out=torch.empty(1, 4, 128, dtype=q.dtype, device="cuda"))
+    for scale in (0.0, -1.0, float("nan"), float("inf")):
+        with pytest.raises(dfc.DfcError) as e:
+            go(q, k, v, t, cu, lens, scale=scale)
+        assert e.value.status == dfc.EINVAL
+    with pytest.raises(dfc.DfcError) as e:
+        go(q, k, v, t, cu, lens, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    assert e.value.status == dfc.ESIZE
+    with pytest.raises(dfc.DfcError) as e:   # pages of 15 tokens
+        go(q, k[:, :15], v[:, :15], t, cu, lens)
+    assert e.value.status == dfc.EINVAL
+    with pytest.raises(dfc.DfcError) as e:   # head dim not a multiple of 8
+        go(q[..., :60], k[..., :60], v[..., :60], t, cu, lens)
+    assert e.value.status == dfc.EINVAL
+    with pytest.raises(dfc.DfcError) as e:   # rows at odd addresses
+        go(q[..., 4:124], k[..., :120], v[..., :120], t, cu, lens)
+    assert e.value.status == dfc.EINVAL
+    # nothing to do
+    none = torch.empty(0, 4, 128, dtype=q.dtype, device="cuda")
+    assert go(none, k, v, t[:0], torch.zeros(1, dtype=torch.int32, device="cuda"), lens[:0]).shape == (0, 4, 128)
+
+
+# ------------------------------------------------------------------- append
+
+@pytest.mark.parametrize("interleaved", [False, True], ids=["halves", "pairs"])
+@pytest.mark.parametrize("source,dtype", [(torch.float32, torch.bfloat16), (torch.float32, torch.float16),
+                                          (torch.bfloat16, torch.bfloat16), (torch.float16, torch.float16)])
+@pytest.mark.parametrize("tokens,heads,kv_heads,dim,rot,page", [(1, 4, 1, 64, 64, 16), (13, 6, 3, 80, 32, 4),
+                                                              (70, 8, 2, 128, 128, 16), (5, 3, 1, 8, 0, 1),
+                                                              (9, 2, 2, 256, 256, 128)])
+def test_append(tokens, heads, kv_heads, dim, rot, page, source, dtype, interleaved):
+    g = torch.Generator().manual_seed(tokens + dim)
+    q, k, v = (torch.randn(tokens, n, dim, generator=g).to(source) for n in (heads, kv_heads, kv_heads))
+    pages = 2 * tokens // page + 2
+    slots = torch.randperm(pages * page, generator=g)[:tokens]
+    if tokens > 4:
+        slots[tokens // 2] = -1
+    pos = torch.randint(0, 400, (tokens,), generator=g).int()
+    angle = torch.arange(400)[:, None] * 10000.0 ** (-torch.arange(0, max(rot, 2), 2) / max(rot, 2))
+    table = torch.cat([angle.cos(), angle.sin()], 1).float()
+    kc, vc = (torch.full((pages, page, kv_heads, dim), float("nan"), dtype=dtype, device="cuda") for _ in range(2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    say("append", tokens, heads, dim, rot, source, dtype, interleaved)
+    got = dfc.paged_append(k.cuda(), v.cuda(), kc, vc, slots.cuda(), q=q.cuda(), positions=pos.cuda(),
+                           rotary=table.cuda() if rot else None, interleaved=interleaved, status=status)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    ref = [as64(x) for x in (q, k)]
+    if rot:
+        ref = [op.rotate(x, pos.tolist(), table.numpy(), interleaved) for x in ref]
+    size = [np.abs(as64(x)).max(-1, keepdims=True) for x in (q, k)]
+    # two products and a sum in fp32, then one rounding
+    u = U[dtype]
+    small = 2.0 ** -24 if dtype == torch.float16 else 0.0
+    stored = slots >= 0
+    assert (np.abs(as64(got) - ref[0]) <= u * np.abs(ref[0]) + 2.0 ** -21 * size[0] + small).all()
+    flat_k, flat_v = as64(kc).reshape(-1, kv_heads, dim), as64(vc).reshape(-1, kv_heads, dim)
+    at = slots[stored].numpy()
+    kept = stored.numpy()
+    assert (np.abs(flat_k[at] - ref[1][kept]) <= u * np.abs(ref[1][kept]) + 2.0 ** -21 * size[1][kept] + small).all()
+    assert np.array_equal(flat_v[at], as64(v.to(dtype))[kept])
+    rest = np.setdiff1d(np.arange(pages * page), at)
+    assert np.isnan(flat_k[rest]).all() and np.isnan(flat_v[rest]).all()
+
+
+def test_append_strides_and_a_quarter_turn():
+    # cos 0, sin 1: the pair (a, b) becomes (-b, a) exactly
+    x = torch.arange(2 * 6 * 32, dtype=torch.float32, device="cuda").view(2, 6, 32)   # k, v, q side by side
+    kc, vc = (torch.zeros(4, 2, 8, 32, dtype=torch.bfloat16, device="cuda").permute(0, 2, 1, 3)[:, :, :2]
+              for _ in range(2))
+    table = torch.cat([torch.zeros(1, 16), torch.ones(1, 16)], 1).cuda()
+    q_out = torch.zeros(2, 4, 64, dtype=torch.bfloat16, device="cuda")[:, 1:3, :32]
+    slots = torch.tensor([9, 30], device="cuda")
+    dfc.paged_append(x[:, :2], x[:, 2:4], kc, vc, slots, q=x[:, 4:], q_out=q_out,
+                     positions=torch.zeros(2, dtype=torch.int32, device="cuda"), rotary=table)
+    torch.cuda.synchronize()
+    turned = torch.cat([-x[..., 16:], x[..., :16]], -1).bfloat16()
+    for t, (p, j) in enumerate(((1, 1), (3, 6))):
+        assert torch.equal(kc[p, j], turned[t, :2]) and torch.equal(vc[p, j], x[t, 2:4].bfloat16())
+    assert torch.equal(q_out, turned[:, 4:])
+    assert int((kc != 0).any(-1).sum()) == 4
+
+
+def test_append_slots_and_positions_that_make_no_sense():
+    x = torch.ones(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    table = torch.ones(4, 64, device="cuda")
+    for slots, pos in (([0, 10 ** 12, 1], [0, 1, 2]), ([0, 32, 1], [0, 1, 2]), ([0, 2, 1], [0, 4, 2]),
+                       ([0, 2, 1], [0, -1, 2])):
+        kc, vc = (torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        say(slots, pos)
+        dfc.paged_append(x, x, kc, vc, torch.tensor(slots, device="cuda"),
+                         positions=torch.tensor(pos, dtype=torch.int32, device="cuda"), rotary=table, status=status)
+        torch.cuda.synchronize()
+        assert int(status.item()) == dfc.ECORRUPT
+        assert torch.equal(vc[0, 0], x[0]) and torch.equal(vc[0, 1], x[2])
+
+
+def test_append_refusals():
+    x = torch.ones(3, 2, 64, device="cuda")
+    kc, vc = (torch.zeros(2, 16, 2, 64, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    slots = torch.arange(3, device="cuda")
+    with pytest.raises(TypeError):
+        dfc.paged_append(x.half(), x.half(), kc, vc, slots)
+    with pytest.raises(TypeError):
+        dfc.paged_append(x, x, kc, vc, slots.int())
+    with pytest.raises(ValueError):
+        dfc.paged_append(x, x, kc, vc, slots[:2])
+    with pytest.raises(ValueError):
+        dfc.paged_append(x, x[:, :1], kc, vc, slots)
+    with pytest.raises(ValueError):
+        dfc.paged_append(x, x, kc, vc, slots, rotary=torch.ones(4, 64, device="cuda"))
+    pos = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for width in (24, 80):   # not a multiple of 16; more than a head
+        with pytest.raises(dfc.DfcError) as e:
+            dfc.paged_append(x, x, kc, vc, slots, positions=pos, rotary=torch.ones(4, width, device="cuda"))
+        assert e.value.status == dfc.EINVAL
+    b = x.bfloat16()
+    with pytest.raises(dfc.DfcError) as e:   # rotated in place
+        dfc.paged_append(b, b, kc, vc, slots, q=b, q_out=b, positions=pos, rotary=torch.ones(4, 64, device="cuda"))
+    assert e.value.status == dfc.EINVAL
+    dfc.paged_append(x[:0], x[:0], kc, vc, slots[:0])
+
+
+# --------------------------------------------------------------------- plan
+
+def run_plan(context, new, page, ring, head, tail, tokens=None, width=None, holes=0, seed=0):
+    rng = np.random.default_rng(seed)
+    have = [-(-c // page) for c in context]
+    need = [-(-(c + n) // page) for c, n in zip(context, new)]
+    width = max(need + [1]) + 2 if width is None else width
+    table = np.full((len(context), width), -7, np.int32)
+    used = rng.permutation(100000)
+    for r, h in enumerate(have):
+        table[r, :h] = used[:h]
+        used = used[h:]
+    free = used[:ring].astype(np.int32)
+    tokens = sum(new) + 5 if tokens is None else tokens
+    want = op.plan(context, new, table, free, (head, tail), page, tokens)
+    dev = torch.from_numpy(table).cuda()
+    cursor = torch.tensor([head, tail], device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = dfc.paged_plan(torch.tensor(context, dtype=torch.int32, device="cuda"),
+                         torch.tensor(new, dtype=torch.int32, device="cuda"), dev, torch.from_numpy(free).cuda(),
+                         cursor, page, tokens, status=status)
+    torch.cuda.synchronize()
+    assert torch.equal(cursor.cpu(), torch.tensor([head, tail]))
+    return want, (dev, got.seq_lens, got.cu_q, got.slots, got.positions, got.cursor), int(status.item())
+
+
+@pytest.mark.parametrize("page", [1, 16, 64])
+@pytest.mark.parametrize("requests,longest", [(1, 1), (3, 50), (64, 1), (1000, 7), (1024, 3), (1025, 2), (2600, 9)])
+def test_plan(requests, longest, page):
+    rng = np.random.default_rng(requests + page)
+    context = rng.integers(0, 60, requests).tolist()
+    new = rng.integers(0 if requests > 1 else 1, longest + 1, requests).tolist()
+    say("plan", requests, longest, page)
+    ring = sum(new) + 3
+    want, got, status = run_plan(context, new, page, ring, 10 * ring + 2, 10 * ring + 2 + ring)
+    assert status == 0
+    for w, x in zip(want, got):
+        assert np.array_equal(w, x.cpu().numpy())
+
+
+def test_plan_of_long_prompts():
+    want, got, status = run_plan([0, 5, 0, 4000], [9000, 1, 0, 5000], 16, 1000, 0, 900)
+    assert status == 0
+    for w, x in zip(want, got):
+        assert np.array_equal(w, x.cpu().numpy())
+
+
+def test_plan_runs_out_of_pages():
+    want, got, status = run_plan([3, 16, 0, 31], [14, 40, 20, 1], 16, 10, 7, 11)
+    assert status == dfc.ESIZE and (want[3] == -1).sum() > 5
+    for w, x in zip(want, got):
+        assert np.array_equal(w, x.cpu().numpy())
+
+
+def test_plan_without_requests():
+    e = torch.zeros(0, dtype=torch.int32, device="cuda")
+    free, cursor = torch.arange(4, dtype=torch.int32, device="cuda"), torch.tensor([1, 3], device="cuda")
+    p = dfc.paged_plan(e, e, torch.zeros(0, 3, dtype=torch.int32, device="cuda"), free, cursor, 16, 2)
+    assert p.cu_q.tolist() == [0] and p.slots.tolist() == [-1, -1] and p.cursor.tolist() == [1, 3]
+
+
+def test_plan_inputs_that_make_no_sense():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.full((2, 4), -7, **i32)
+    free = torch.arange(10, 30, **i32)
+
+    def go(context, new, cursor, tokens=40, t=table):
+        status = torch.zeros(1, **i32)
+        t = t.clone()
+        p = dfc.paged_plan(torch.tensor(context, **i32), torch.tensor(new, **i32), t, free,
+                           torch.tensor(cursor, device="cuda"), 16, tokens, status=status)
+        torch.cuda.synchronize()
+        return p, t, int(status.item())
+
+    p, t, status = go([0, -4], [3, -2], [0, 20])
+    assert status == dfc.ECORRUPT and p.cu_q.tolist() == [0, 3, 3] and p.slots.tolist() == [160, 161, 162] + [-1] * 37
+    p, t, status = go([0, 0], [3, 2], [5, 26])          # more free pages than the ring has
+    assert status & 0xFFFFFFFF == (dfc.ECORRUPT | dfc.ESIZE) & 0xFFFFFFFF and (p.slots == -1).all()
+    p, t, status = go([0, 0], [3, 90], [0, 20], tokens=100)   # more pages than a row holds
+    assert status == dfc.ESIZE and p.slots[3 + 64:93].eq(-1).all() and p.slots[3:67].ge(0).all()
+    p, t, status = go([0, 0], [3, 5], [0, 20], tokens=4)      # more tokens than fit
+    assert status == dfc.ESIZE and p.cu_q.tolist() == [0, 3, 4] and p.slots.tolist() == [160, 161, 162, 176]
+    p, t, status = go([17, 0], [3, 1], [0, 20])               # the page it holds is missing
+    assert status == dfc.ECORRUPT and p.slots.tolist()[:4] == [-1, -1, -1, 160]
+
+
+def test_plan_refusals():
+    i32 = dict(dtype=torch.int32, device="cuda")
+    c, n, t = torch.zeros(2, **i32), torch.ones(2, **i32), torch.zeros(2, 4, **i32)
+    free, cursor = torch.arange(10, **i32), torch.tensor([0, 10], device="cuda")
+    with pytest.raises(TypeError):
+        dfc.paged_plan(c.long(), n, t, free, cursor, 16, 2)
+    with pytest.raises(TypeError):
+        dfc.paged_plan(c, n, t, free, cursor.int(), 16, 2)
+    with pytest.raises(ValueError):
+        dfc.paged_plan(c, n[:1], t, free, cursor, 16, 2)
+    with pytest.raises(ValueError):
+        dfc.paged_plan(c, n, t[:1], free, cursor, 16, 2)
+    for kw in (dict(page_size=0), dict(page_size=24), dict(page_size=16, free=free[:0])):
+        with pytest.raises(dfc.DfcError) as e:
+            dfc.paged_plan(c, n, t, kw.get("free", free), cursor, kw["page_size"], 2)
+        assert e.value.status == dfc.EINVAL
+    p = dfc.paged_plan(c, n, t, free, cursor, 16, 2)
+    for out in (p._replace(cursor=cursor), p._replace(seq_lens=c)):
+        with pytest.raises(dfc.DfcError) as e:
+            dfc.paged_plan(c, n, t, free, cursor, 16, 2, out=out)
+        assert e.value.status == dfc.EINVAL
+
+
+# ---------------------------------------------------------------- one step
+
+def test_a_captured_step_follows_the_lengths():
+    """Plan, append and attention captured once; replays with other lengths
+    between them match the eager calls."""
+    H, K, D, P, R, T = 8, 2, 64, 16, 3, 6
+    i32 = dict(dtype=torch.int32, device="cuda")
+    ctx, new = torch.zeros(R, **i32), torch.zeros(R, **i32)
+    table = torch.full((R, 20), -1, **i32)
+    free = torch.randperm(60, device="cuda").int()
+    cursor = torch.tensor([0, 60], device="cuda")
+    kc, vc = (torch.zeros(60, P, K, D, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    q, k, v = (torch.zeros(T, n, D, device="cuda") for n in (H, K, K))
+    angle = torch.arange(320, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D)
+    rotary = torch.cat([angle.cos(), angle.sin()], 1).float()
+    plan = dfc.paged_plan(ctx, new, table, free, cursor, P, T)
+    q16 = torch.zeros(T, H, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros_like(q16)
+    ws = torch.empty(dfc.paged_attention_workspace(q16, kc, vc, table, plan.cu_q, plan.seq_lens), dtype=torch.uint8,
+                     device="cuda")
+
+    def step():
+        dfc.paged_plan(ctx, new, table, free, cursor, P, T, out=plan)
+        dfc.paged_append(k, v, kc, vc, plan.slots, q=q, q_out=q16, positions=plan.positions, rotary=rotary)
+        dfc.paged_attention(q16, kc, vc, table, plan.cu_q, plan.seq_lens, out=out, workspace=ws)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    held = [[], [], []]
+    for i, counts in enumerate(([2, 3, 1], [1, 1, 1], [1, 0, 4], [0, 5, 1], [1, 1, 1])):
+        new.copy_(torch.tensor(counts))
+        for t in (q, k, v):
+            t.normal_()
+        say("replay", i, counts)
+        graph.replay()
+        torch.cuda.synchronize()
+        replayed = out.clone()
+        kept = (table.clone(), kc.clone(), vc.clone())
+        step()
+        torch.cuda.synchronize()
+        n = sum(counts)
+        assert torch.equal(replayed[:n], out[:n])
+        assert all(torch.equal(a, b) for a, b in zip(kept, (table, kc, vc)))
+        # the whole history from scratch
+        at = 0
+        for r, c in enumerate(counts):
+            pos = plan.positions[at: at + c].tolist()
+            assert pos == list(range(len(held[r]), len(held[r]) + c))
+            kr = torch.from_numpy(op.rotate(as64(k[at: at + c]), pos, rotary.cpu().numpy(), False))
+            held[r] += [(kr[j], v[at + j].double().cpu()) for j in range(c)]
+            if c:
+                kk = torch.stack([x[0] for x in held[r]]).numpy()
+                vv = torch.stack([x[1] for x in held[r]]).numpy()
+                qq = op.rotate(as64(q[at: at + c]), pos, rotary.cpu().numpy(), False)
+                ref, _, spread, _, mass = op.attention(qq, kk, vv, D ** -0.5)
+                # q, k and v are rounded to 8 bits: a score moves by 2 u mass,
+                # a weight by e^(2 of that); then v, the weights, the output
+                u = 2.0 ** -8
+                bound = (np.expm1(2 * 2.02 * u * mass)[..., None] + 3 * u) * spread + u * np.abs(ref) + 1e-5
+                assert (np.abs(as64(out[at: at + c]) - ref) <= bound).all()
+            at += c
+        ctx.copy_(plan.seq_lens)
+        cursor.copy_(plan.cursor)
