@@ -39,18 +39,25 @@ using f32x16 = __attribute__((ext_vector_type(16))) float;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kSchedThreads = 1024;
 constexpr uint32_t kWaves = 4;
 
-// One piece of work: a tile of rows of one request and a range of keys; every
-// cache head has it.
-struct alignas(64) Piece {
-    int32_t req, row0;     // request; first row of the tile
+// One piece of work: a tile of rows of one request and a range of keys, for
+// one cache head.
+struct Piece {
+    uint32_t req, row0;     // request; first row of the tile
     int32_t q_start, q_len, kv_len;
-    int32_t lo, hi;        // keys
-    int32_t split, splits; // which piece of the tile, of how many
-    int32_t slot;          // first partial result of the tile (splits > 1)
-    int32_t pad[6];
+    int32_t lo, hi;         // keys
+    uint32_t split, splits; // which piece of the tile, of how many
+    uint32_t slot;          // first partial result of the tile (splits > 1)
+    uint32_t tile;          // number of the tile in the step
+};
+
+// A tile, for the joining of its pieces.
+struct alignas(16) Tile {
+    uint32_t splits, slot;
+    int32_t token0;         // row of q of the request's first token
+    uint32_t row0, rows;
+    uint32_t pad[3];
 };
 
 struct AttnArgs {
@@ -63,39 +70,25 @@ struct AttnArgs {
     uint32_t n_requests, tokens, max_pages, window;
     int32_t causal;
     float scale, scale_log2;   // scores by exp2: scale log2(e)
-    // schedule
-    uint32_t rows_per_tile, key_tile, min_piece, targets;  // targets: pieces aimed at over all cache heads
-    uint32_t piece_cap, slot_cap;                          // capacities of pieces[] and of partial results per head
-    uint32_t *count;       // pieces made
-    Piece *pieces;
+    uint32_t rows_per_tile, key_tile, min_piece;  // a piece has min_piece key tiles or more
+    uint32_t resident;         // workgroups that run at once
+    float piece_cost, join_cost;  // what a piece, and the joining, cost in key tiles
+    uint32_t extra;            // pieces there may be beyond one a tile
+    uint32_t tile_cap;
+    uint32_t *tile_count;
+    Tile *tiles;               // null: no tile can be split
     float *part_o, *part_ml;
     uint32_t *status;
 };
 
 // -------------------------------------------------------------- schedule
-
-__device__ __forceinline__ uint32_t block_scan(uint32_t &x, uint32_t *part) {
-    constexpr uint32_t W = kSchedThreads / kWave;
-    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    uint32_t ix = x;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint32_t u = __shfl_up(ix, d);
-        if (lane >= uint32_t(d)) ix += u;
-    }
-    __syncthreads();
-    if (lane == kWave - 1) part[wave] = ix;
-    __syncthreads();
-    uint32_t before = 0, sum = 0;
-#pragma unroll
-    for (uint32_t w = 0; w < W; ++w) {
-        const uint32_t v = part[w];
-        if (w < wave) before += v;
-        sum += v;
-    }
-    x = before + ix - x;
-    return sum;
-}
+//
+// Every workgroup finds its own piece from the step's lengths.  A request's
+// tiles (n of them, the longest of c key tiles) are cut into S = ceil(c / L)
+// pieces each, so the pieces before a request are a prefix sum of n S, and
+// what all workgroups have to agree on is L.  Reading the lengths costs each
+// workgroup about a microsecond; a kernel that lists the pieces first, and
+// its launch, cost the step more than ten.
 
 struct Req {
     int32_t q_start, q_len, kv_len;
@@ -129,112 +122,171 @@ __device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint3
     lo = int32_t(min(begin, int64_t(hi)));
 }
 
-// One workgroup cuts the step into pieces: a first pass adds up the key tiles
-// of every tile of rows, which sets the largest piece, a second one writes
-// the pieces.  A tile's later rows see more keys, so a request's tiles are
-// listed from the last.
-__global__ __launch_bounds__(kSchedThreads) void schedule_kernel(AttnArgs a) {
-    __shared__ uint32_t part[kSchedThreads / kWave];
-    __shared__ uint32_t first[kSchedThreads], tiles_of[kSchedThreads];
-    __shared__ Req req_of[kSchedThreads];
-    const uint32_t tid = threadIdx.x;
-    uint32_t bad = 0;
-    uint64_t cost = 0;          // key tiles, over all tiles (this thread's share)
-    uint32_t piece = 1u << 30;  // key tiles per piece
-    uint32_t n_pieces = 0, n_slots = 0;
-    for (int pass = 0; pass < 2; ++pass) {
-        for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kSchedThreads) {
-            const uint32_t r = r0 + tid, here = min(kSchedThreads, a.n_requests - r0);
-            Req q{0, 0, 0};
-            if (r < a.n_requests) q = request(a, r, bad);
-            uint32_t n = uint32_t((uint64_t(q.q_len) * a.group + a.rows_per_tile - 1) / a.rows_per_tile);
-            uint32_t f = n;
-            const uint32_t total = block_scan(f, part);
-            __syncthreads();
-            first[tid] = f;
-            tiles_of[tid] = n;
-            req_of[tid] = q;
-            __syncthreads();
-            for (uint32_t t0 = 0; t0 < total; t0 += kSchedThreads) {
-                const uint32_t t = t0 + tid;
-                uint32_t splits = 0, row0 = 0, k = 0;
-                int32_t lo = 0, hi = 0;
-                if (t < total) {
-                    uint32_t h = here;
-                    while (h - k > 1) {
-                        const uint32_t mid = (k + h) / 2;
-                        if (first[mid] <= t)
-                            k = mid;
-                        else
-                            h = mid;
-                    }
-                    row0 = (tiles_of[k] - 1u - (t - first[k])) * a.rows_per_tile;
-                    tile_keys(a, req_of[k], row0, lo, hi);
-                    const uint32_t c = uint32_t(hi - lo + int32_t(a.key_tile) - 1) / a.key_tile;
-                    cost += c;
-                    splits = max(1u, (c + piece - 1) / piece);
-                }
-                if (pass == 0) continue;
-                uint32_t at = splits, slot = splits > 1 ? splits : 0u;
-                const uint32_t s_all = block_scan(at, part), p_all = block_scan(slot, part);
-                at += n_pieces;
-                slot += n_slots;
-                n_pieces += s_all;
-                n_slots += p_all;
-                if (t < total) {
-                    const uint32_t c = uint32_t(hi - lo + int32_t(a.key_tile) - 1) / a.key_tile;
-                    const Req q2 = req_of[k];
-                    for (uint32_t s = 0; s < splits; ++s) {
-                        // even shares of the key tiles
-                        const uint32_t c0 = uint32_t(uint64_t(c) * s / splits), c1 = uint32_t(uint64_t(c) * (s + 1) / splits);
-                        Piece w;
-                        w.req = int32_t(r0 + k);
-                        w.row0 = int32_t(row0);
-                        w.q_start = q2.q_start;
-                        w.q_len = q2.q_len;
-                        w.kv_len = q2.kv_len;
-                        w.lo = lo + int32_t(c0 * a.key_tile);
-                        w.hi = min(hi, lo + int32_t(c1 * a.key_tile));
-                        w.split = int32_t(s);
-                        w.splits = int32_t(splits);
-                        w.slot = int32_t(slot);
-                        // the capacities hold every step whose lengths are what they should be
-                        if (splits > 1 && slot + splits > a.slot_cap) {
-                            w.q_len = 0;
-                            bad |= kStatusCorrupt;
-                        }
-                        if (at + s < a.piece_cap) a.pieces[at + s] = w;
-                    }
-                }
-            }
-            __syncthreads();  // the requests have been read
-        }
-        if (pass == 0) {
-            // the workgroup's key tiles over all cache heads, shared out
-            __shared__ unsigned long long sum;
-            if (tid == 0) sum = 0;
-            __syncthreads();
-            atomicAdd(&sum, cost);
-            __syncthreads();
-            const uint64_t all = sum * a.kv_heads;
-            piece = uint32_t(min(uint64_t(1) << 30, max(uint64_t(a.min_piece), (all + a.targets - 1) / a.targets)));
-        }
+__device__ __forceinline__ uint32_t key_tiles(const AttnArgs &a, int32_t lo, int32_t hi) {
+    return (uint32_t(hi - lo) + a.key_tile - 1u) / a.key_tile;
+}
+
+__device__ __forceinline__ uint32_t ceil_of(uint32_t x, uint32_t y) { return (x + y - 1u) / y; }
+
+// Tiles of rows of a request, and the key tiles of its last one (the longest
+// but for a window's edge).
+__device__ __forceinline__ void tiles_of(const AttnArgs &a, const Req &q, uint32_t &n, uint32_t &c) {
+    n = uint32_t((uint64_t(uint32_t(q.q_len)) * a.group + a.rows_per_tile - 1u) / a.rows_per_tile);
+    c = 0;
+    if (n) {
+        int32_t lo, hi;
+        tile_keys(a, q, (n - 1u) * a.rows_per_tile, lo, hi);
+        c = key_tiles(a, lo, hi);
     }
-    if (n_pieces > a.piece_cap) bad |= kStatusCorrupt;
-    if (tid == 0) *a.count = min(n_pieces, a.piece_cap);
-    if (bad && a.status) atomicOr(a.status, bad);
+}
+
+__device__ __forceinline__ float wave_max(float x) {
+#pragma unroll
+    for (int d = 32; d; d /= 2) x = fmaxf(x, __shfl_xor(x, d));
+    return x;
+}
+
+// L for up to 64 requests, one a lane: every lane tries one value, counts the
+// pieces p it makes and takes
+//     rounds (L + piece_cost), rounds = ceil(p heads / resident),
+// for its time; the least wins.  Cutting one long request into as many equal
+// pieces as run at once, cutting many ragged ones finer so that the last
+// round is full, and not cutting where it does not pay all come out of it.
+__device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, uint32_t c) {
+    const uint32_t lane = threadIdx.x % kWave;
+    const float longest = wave_max(float(c));
+    const float parts = lane < 32u ? float(lane + 1u) : 32.0f * __builtin_amdgcn_exp2f(float(lane - 31u) * 0.15625f);
+    const uint32_t piece = max(a.min_piece, uint32_t(ceilf(longest / parts)));
+    const float inv = 1.0f / float(piece);
+    uint64_t p = 0;
+    uint32_t tiles = 0;
+    for (uint32_t r = 0; r < a.n_requests; ++r) {
+        const uint32_t nr = __builtin_amdgcn_readlane(n, r), cr = __builtin_amdgcn_readlane(c, r);
+        uint32_t s = uint32_t(float(cr) * inv);  // never below ceil(c / piece) after this
+        s += s * piece < cr;
+        s += s * piece < cr;
+        tiles += nr;
+        p += uint64_t(nr) * max(s, 1u);
+    }
+    const float rounds = ceilf(float(p) * float(a.kv_heads) / float(a.resident));
+    float t = rounds * (float(piece) + a.piece_cost);
+    if (float(piece) < longest) t += a.join_cost;
+    if (p - tiles > a.extra) t = 3e38f;
+    const float best = -wave_max(-t);
+    const uint32_t who = __builtin_ctzll(__ballot(t == best));
+    return __builtin_amdgcn_readlane(piece, who);
+}
+
+// The piece `index` of the step (for every cache head), false if there is
+// none.  `scratch` is LDS that nothing else uses meanwhile.  Row ranges that
+// overlap could make more tiles than q has room for: then there are none.
+__device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bool first, uint32_t *scratch, Piece &w) {
+    const uint32_t tid = threadIdx.x, lane = tid % kWave;
+    uint32_t bad = 0;
+    uint32_t within = 0, parts = 1, n_tiles = 0, slot0 = 0, tile0 = 0, piece = 1;
+    if (a.n_requests <= 64) {
+        Req q{0, 0, 0};
+        if (lane < a.n_requests) q = request(a, lane, bad);
+        uint32_t n, c;
+        tiles_of(a, q, n, c);
+        piece = a.extra ? choose_piece(a, n, c) : 1u << 30;
+        const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u;
+        const uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), in = wave_inclusive_scan(n);
+        const bool fits = uint32_t(__builtin_amdgcn_readlane(in, 63)) <= a.tile_cap;
+        if (!fits) bad |= kStatusCorrupt;
+        if (first && tid == 63) *a.tile_count = fits ? in : 0u;
+        if (first && bad && a.status) atomicOr(a.status, bad);
+        if (!fits || index >= uint32_t(__builtin_amdgcn_readlane(ix, 63))) return false;
+        const uint32_t r = 63u - uint32_t(__builtin_clzll(__ballot(x > 0u && ix - x <= index)));
+        within = index - uint32_t(__builtin_amdgcn_readlane(ix - x, r));
+        parts = __builtin_amdgcn_readlane(s, r);
+        n_tiles = __builtin_amdgcn_readlane(n, r);
+        slot0 = __builtin_amdgcn_readlane(iy - y, r);
+        tile0 = __builtin_amdgcn_readlane(in - n, r);
+        w.req = r;
+        w.q_start = __builtin_amdgcn_readlane(q.q_start, r);
+        w.q_len = __builtin_amdgcn_readlane(q.q_len, r);
+        w.kv_len = __builtin_amdgcn_readlane(q.kv_len, r);
+    } else {
+        // more requests than lanes: L from the sum of their key tiles
+        const uint32_t wave = tid / kWave;
+        uint64_t *sums = reinterpret_cast<uint64_t *>(scratch);
+        uint64_t all = 0, tiles = 0;
+        for (uint32_t r = tid; r < a.n_requests; r += kThreads) {
+            uint32_t n, c;
+            tiles_of(a, request(a, r, bad), n, c);
+            all += uint64_t(n) * c;
+            tiles += n;
+        }
+#pragma unroll
+        for (int d = 32; d; d /= 2) {
+            all += __shfl_xor(all, d);
+            tiles += __shfl_xor(tiles, d);
+        }
+        if (lane == 0) sums[wave] = all, sums[kWaves + wave] = tiles;
+        __syncthreads();
+        all = (sums[0] + sums[1] + sums[2] + sums[3]) * a.kv_heads;
+        const bool fits = sums[4] + sums[5] + sums[6] + sums[7] <= a.tile_cap;
+        if (!fits) bad |= kStatusCorrupt;
+        const uint64_t target = uint64_t(a.extra) * a.kv_heads;
+        piece = a.extra ? uint32_t(min(uint64_t(1) << 30, max(uint64_t(a.min_piece), (all + target - 1u) / target)))
+                        : 1u << 30;
+        uint32_t px = 0, py = 0, pn = 0;  // before this chunk of requests
+        uint32_t *found = scratch + 16, *part = scratch + 32;
+        if (tid == 0) found[0] = 0;
+        for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kThreads) {
+            Req q{0, 0, 0};
+            uint32_t unused = 0, n, c;
+            if (r0 + tid < a.n_requests) q = request(a, r0 + tid, unused);
+            tiles_of(a, q, n, c);
+            const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u;
+            uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), in = wave_inclusive_scan(n);
+            __syncthreads();  // part has been read
+            if (lane == 63u) part[3u * wave] = ix, part[3u * wave + 1u] = iy, part[3u * wave + 2u] = in;
+            __syncthreads();
+            ix += px, iy += py, in += pn;
+            for (uint32_t k = 0; k < kWaves; ++k) {
+                const uint32_t tx = part[3u * k], ty = part[3u * k + 1u], tn = part[3u * k + 2u];
+                if (k < wave) ix += tx, iy += ty, in += tn;
+                px += tx, py += ty, pn += tn;
+            }
+            if (ix - x <= index && index < ix) {
+                found[0] = 1;
+                found[1] = r0 + tid, found[2] = uint32_t(q.q_start), found[3] = uint32_t(q.q_len);
+                found[4] = uint32_t(q.kv_len), found[5] = index - (ix - x), found[6] = s, found[7] = n;
+                found[8] = iy - y, found[9] = in - n;
+            }
+            if (!first && px > index) break;  // this chunk had it
+        }
+        __syncthreads();
+        if (first && tid == 0) *a.tile_count = fits ? pn : 0u;
+        if (first && bad && a.status) atomicOr(a.status, bad);
+        uint32_t f[10];
+#pragma unroll
+        for (int i = 0; i < 10; ++i) f[i] = __builtin_amdgcn_readfirstlane(found[i]);
+        __syncthreads();  // read by all before the scratch is used again
+        if (!f[0] || !fits) return false;
+        w.req = f[1];
+        w.q_start = int32_t(f[2]), w.q_len = int32_t(f[3]), w.kv_len = int32_t(f[4]);
+        within = f[5], parts = f[6], n_tiles = f[7], slot0 = f[8], tile0 = f[9];
+    }
+    // the later tiles of a request see more keys: they come first
+    const uint32_t tile = within / parts;
+    w.split = within - tile * parts;
+    w.row0 = (n_tiles - 1u - tile) * a.rows_per_tile;
+    int32_t lo, hi;
+    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi);
+    const uint32_t c = key_tiles(a, lo, hi);
+    w.splits = min(parts, max(1u, ceil_of(c, piece)));
+    w.slot = slot0 + tile * parts;
+    w.tile = tile0 + tile;
+    // even shares of the key tiles
+    w.lo = lo + int32_t(uint32_t(uint64_t(c) * w.split / w.splits) * a.key_tile);
+    w.hi = min(hi, lo + int32_t(uint32_t(uint64_t(c) * (w.split + 1u) / w.splits) * a.key_tile));
+    return w.split < w.splits;
 }
 
 // ------------------------------------------------------------- attention
-
-// A piece, in scalar registers.
-__device__ __forceinline__ Piece get_piece(const AttnArgs &a, uint32_t index) {
-    Piece w = a.pieces[index];
-    int32_t *x = &w.req;
-#pragma unroll
-    for (int i = 0; i < 10; ++i) x[i] = __builtin_amdgcn_readfirstlane(x[i]);
-    return w;
-}
 
 template <typename E>
 struct Type;
@@ -309,7 +361,7 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
     constexpr int NO = DP / 64;
 #pragma unroll 1
     for (uint32_t r = 0; r < 32u; ++r) {
-        const int32_t row = w.row0 + int32_t(row_base + r);
+        const int32_t row = int32_t(w.row0 + row_base + r);
         if (row >= w.q_len * int32_t(a.group)) break;
         const int32_t tok = row / int32_t(a.group), g = row - tok * int32_t(a.group);
         const int32_t pos = w.kv_len - w.q_len + tok;
@@ -384,9 +436,8 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
 
     const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
-    if (index >= *a.count) return;
-    const Piece w = get_piece(a, index);
-    if (w.q_len <= 0) return;
+    Piece w;
+    if (!find_piece(a, index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
     const uint32_t lane = threadIdx.x % kWave;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t rw = wave % RW, kw = wave / RW;
@@ -395,7 +446,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     const int32_t lo = w.lo, hi = w.hi;
 
     // this lane's row
-    const int32_t row = w.row0 + int32_t(32u * rw + c);
+    const int32_t row = int32_t(w.row0 + 32u * rw + c);
     const bool row_in = row < n_rows;
     const int32_t row_c = min(row, n_rows - 1);
     const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
@@ -405,7 +456,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     // over the wavefront's rows (positions ascend with the row)
     const int32_t hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
     const int32_t hi_max = __builtin_amdgcn_readlane(see_hi, 31), lo_max = __builtin_amdgcn_readlane(see_lo, 31);
-    const bool idle = w.row0 + int32_t(32u * rw) >= n_rows;
+    const bool idle = int32_t(w.row0 + 32u * rw) >= n_rows;
 
     V8 qf[NQ];
     {
@@ -600,11 +651,20 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     };
     ml = reinterpret_cast<float *>(lds + Sh::kMl);
     const bool whole = w.splits == 1;
-    const uint64_t slot = (uint64_t(uint32_t(w.slot + w.split)) * a.kv_heads + kvh) * a.rows_per_tile;
+    const uint64_t slot = (uint64_t(w.slot + w.split) * a.kv_heads + kvh) * a.rows_per_tile;
+    if (a.tiles && kvh == 0 && w.split == 0 && threadIdx.x == 0) {
+        Tile t;
+        t.splits = w.splits;
+        t.slot = w.slot;
+        t.token0 = w.q_start;
+        t.row0 = w.row0;
+        t.rows = uint32_t(min(int32_t(a.rows_per_tile), n_rows - int32_t(w.row0)));
+        a.tiles[w.tile] = t;
+    }
 #pragma unroll 2
     for (uint32_t i = lane; i < 32u / KW * CPR; i += 64u) {
         const uint32_t r = kw * (32u / KW) + i / CPR, ch = i % CPR;
-        const int32_t at = w.row0 + int32_t(32u * rw + r);
+        const int32_t at = int32_t(w.row0 + 32u * rw + r);
         if (at >= n_rows || ch * 8u >= a.dim) continue;
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
@@ -635,7 +695,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
                 a.lse[token * a.heads + head] =
                     sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
         } else {
-            const uint64_t pr = slot + uint32_t(at - w.row0);
+            const uint64_t pr = slot + (uint32_t(at) - w.row0);
             float4 *o = reinterpret_cast<float4 *>(a.part_o + pr * DP + ch * 8u);
             o[0] = float4{x[0], x[1], x[2], x[3]};
             o[1] = float4{x[4], x[5], x[6], x[7]};
@@ -644,52 +704,64 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     }
 }
 
-// The pieces of a split tile joined: a wavefront per row, 16-byte pieces of
-// the row along the lanes and several pieces of work at a time.
-template <typename E, int DP>
+// The pieces of a split tile joined.  A wavefront takes a row (WPR = 1, for
+// tiles of many rows and few pieces) or a quarter of its pieces (WPR = 4);
+// lanes run along the row in 16-byte steps and, where the row is shorter,
+// over several pieces.  Each lane keeps its own running maximum.
+template <typename E, int DP, int WPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     using T = Type<E>;
-    constexpr uint32_t CPR = DP / 4;                   // float4 pieces per row
-    constexpr uint32_t SL = CPR >= 64 ? 1 : 64 / CPR;  // pieces of work side by side
+    constexpr uint32_t CPR = DP / 4;                     // float4 pieces per row
+    constexpr uint32_t SL = 64 / CPR;                    // lanes side by side on one column
+    constexpr uint32_t kRows = kWaves / WPR;             // rows at a time
+    __shared__ float4 part_x[WPR == 4 ? 4 : 1][CPR];
+    __shared__ float2 part_ml[4];
     const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
-    if (index >= *a.count) return;
-    const Piece w = get_piece(a, index);
-    if (w.split != 0 || w.splits == 1 || w.q_len <= 0) return;
+    if (index >= *a.tile_count) return;
+    const Tile w = a.tiles[index];
+    const uint32_t splits = __builtin_amdgcn_readfirstlane(w.splits), slot = __builtin_amdgcn_readfirstlane(w.slot);
+    const uint32_t row0 = __builtin_amdgcn_readfirstlane(w.row0), rows = __builtin_amdgcn_readfirstlane(w.rows);
+    const int32_t token0 = __builtin_amdgcn_readfirstlane(w.token0);
+    if (splits == 1u) return;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const uint32_t ch = lane % CPR, sl = lane / CPR;
-    const uint32_t splits = uint32_t(w.splits);
-    const uint32_t rows = uint32_t(min(int64_t(a.rows_per_tile), int64_t(w.q_len) * a.group - w.row0));
-    for (uint32_t r = blockIdx.y * 32u + wave; r < min(rows, blockIdx.y * 32u + 32u); r += kWaves) {
-        auto at = [&](uint32_t s) {
-            return (uint64_t(uint32_t(w.slot) + s) * a.kv_heads + kvh) * a.rows_per_tile + r;
-        };
-        float top = -INFINITY;
-        for (uint32_t s = lane; s < splits; s += kWave) top = fmaxf(top, a.part_ml[2u * at(s)]);
-#pragma unroll
-        for (int d = 32; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
-        float sum = 0.0f;
+    auto weight = [&](float m, float top) { return m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * a.scale_log2); };
+    for (uint32_t r = blockIdx.y * kRows + (WPR == 4 ? 0u : wave); r < rows; r += gridDim.y * kRows) {
+        float top = -INFINITY, sum = 0.0f;
         float4 x{0, 0, 0, 0};
+        auto add = [&](float m, float l, const float4 &o) {
+            const float t2 = fmaxf(top, m), f = weight(top, t2), g = weight(m, t2);
+            top = t2;
+            sum = sum * f + l * g;
+            x.x = x.x * f + o.x * g, x.y = x.y * f + o.y * g, x.z = x.z * f + o.z * g, x.w = x.w * f + o.w * g;
+        };
 #pragma unroll 4
-        for (uint32_t s = sl; s < splits; s += SL) {
-            const uint64_t pr = at(s);
+        for (uint32_t s = (WPR == 4 ? wave * SL : 0u) + sl; s < splits; s += SL * WPR) {
+            const uint64_t pr = (uint64_t(slot + s) * a.kv_heads + kvh) * a.rows_per_tile + r;
             const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2u * pr);
-            const float4 o = *reinterpret_cast<const float4 *>(a.part_o + pr * DP + 4u * ch);
-            const float f = v.x == top ? 1.0f : __builtin_amdgcn_exp2f((v.x - top) * a.scale_log2);
-            sum += v.y * f;
-            x.x += o.x * f, x.y += o.y * f, x.z += o.z * f, x.w += o.w * f;
+            add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part_o + pr * DP + 4u * ch));
         }
 #pragma unroll
         for (uint32_t d = CPR; d < 64u; d *= 2) {
-            sum += __shfl_xor(sum, int(d));
-            x.x += __shfl_xor(x.x, int(d));
-            x.y += __shfl_xor(x.y, int(d));
-            x.z += __shfl_xor(x.z, int(d));
-            x.w += __shfl_xor(x.w, int(d));
+            const float m = __shfl_xor(top, int(d)), l = __shfl_xor(sum, int(d));
+            add(m, l, float4{__shfl_xor(x.x, int(d)), __shfl_xor(x.y, int(d)), __shfl_xor(x.z, int(d)),
+                             __shfl_xor(x.w, int(d))});
+        }
+        if constexpr (WPR == 4) {
+            __syncthreads();  // the row before has been read
+            if (sl == 0) part_x[wave][ch] = x;
+            if (lane == 0) part_ml[wave] = float2{top, sum};
+            __syncthreads();
+            if (wave == 0 && sl == 0) {
+#pragma unroll
+                for (int k = 1; k < 4; ++k) add(part_ml[k].x, part_ml[k].y, part_x[k][ch]);
+            }
+            if (wave != 0) continue;
         }
         if (sl != 0 || ch * 4u >= a.dim) continue;
-        const uint32_t gr = uint32_t(w.row0) + r;
+        const uint32_t gr = row0 + r;
         const uint32_t t = gr / a.group, head = kvh * a.group + gr % a.group;
-        const int64_t token = int64_t(w.q_start) + t;
+        const int64_t token = int64_t(token0) + t;
         const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
         using E4 = __attribute__((ext_vector_type(4))) E;
         const E4 y = {E(x.x * inv), E(x.y * inv), E(x.z * inv), E(x.w * inv)};
@@ -706,8 +778,9 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
 // The launch's shape, from what the host knows: sizes only.
 struct LaunchPlan {
     int rw, kt, dp;
-    uint32_t rows_per_tile, min_piece, targets, piece_cap, slot_cap;
-    uint64_t off_pieces, off_ml, off_o, bytes;
+    uint32_t rows_per_tile, min_piece, resident, extra, tile_cap, slot_cap, most_rows;
+    float piece_cost, join_cost;
+    uint64_t off_tiles, off_ml, off_o, bytes;
 };
 
 LaunchPlan launch_plan(const dfc_attention_args &a) {
@@ -721,23 +794,24 @@ LaunchPlan launch_plan(const dfc_attention_args &a) {
     p.rw = most <= 32 && p.dp <= 128 ? 1 : most <= 64 ? 2 : 4;
     p.kt = p.rw == 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
-    const uint32_t kw = kWaves / uint32_t(p.rw);
-    // a piece has at least 256 keys (512 where tiles are large: their partial
-    // results cost more), and there are up to four pieces a resident
-    // workgroup (two)
-    p.min_piece = (p.rw == 4 ? 512u : 256u) / uint32_t(p.kt);
-    p.min_piece = std::max(p.min_piece, kw);
-    p.targets = 512u * (p.rw == 4 ? 2u : 4u);
+    p.resident = p.dp > 128 ? 256u : 512u;
+    p.min_piece = p.rw == 4 ? 2u : kWaves / uint32_t(p.rw);
+    p.piece_cost = p.rw == 4 ? 1.0f : 4.0f;
+    p.join_cost = p.rw == 4 ? 2.0f : 8.0f;
     const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
                                               uint64_t(a.tokens) * group);
-    const uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt));
-    // a tile of c key tiles has ceil(c / piece) pieces, and the c add up to
-    // at most targets / kv_heads pieces
-    const uint64_t extra = std::min<uint64_t>(p.targets / a.cache.kv_heads + 1u, tiles * (longest / p.min_piece + 1u));
-    p.piece_cap = uint32_t(std::min<uint64_t>(tiles + extra, 0x7fffffffu));
-    p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, p.piece_cap));
-    p.off_pieces = 256;
-    p.off_ml = p.off_pieces + uint64_t(p.piece_cap) * sizeof(Piece);
+    // a tile of c key tiles has at most ceil(c / min_piece) pieces; there are
+    // up to four rounds of pieces beyond one a tile
+    const uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt)) + 1u;
+    const uint64_t each = longest > p.min_piece ? dfc::ceil_div(longest, uint64_t(p.min_piece)) - 1u : 0u;
+    const uint64_t extra = std::min<uint64_t>(4u * p.resident / a.cache.kv_heads + 1u, tiles * each);
+    p.extra = uint32_t(extra);
+    p.tile_cap = uint32_t(tiles);
+    // a tile's pieces are at most twice those beyond its first
+    p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, tiles + extra));
+    p.most_rows = uint32_t(std::min<uint64_t>(most, p.rows_per_tile));
+    p.off_tiles = 256;
+    p.off_ml = p.off_tiles + uint64_t(p.tile_cap) * sizeof(Tile);
     const uint64_t rows = uint64_t(p.slot_cap) * a.cache.kv_heads * p.rows_per_tile;
     p.off_o = (p.off_ml + rows * 8u + 255u) & ~uint64_t(255);
     p.bytes = p.off_o + rows * uint64_t(p.dp) * 4u;
@@ -749,38 +823,42 @@ dfc_status check_attention(const dfc_attention_args &a) {
     if (cs != DFC_OK) return cs;
     if (!a.heads || a.heads % a.cache.kv_heads || a.heads > 65536u) return DFC_EINVAL;
     if (a.tokens > 0x7fffffffull || a.n_requests > 0x7fffffffu) return DFC_EINVAL;
-    // rows (tokens x heads of a group) are counted in 32 bits
-    if (a.tokens * (a.heads / a.cache.kv_heads) > 0x7fffff00ull) return DFC_EUNSUPPORTED;
+    // rows (tokens x heads of a group), and the tiles of 64 requests, are
+    // counted in 32 bits
+    if (a.tokens * (a.heads / a.cache.kv_heads) > 0x3fffffffull) return DFC_EUNSUPPORTED;
     if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return DFC_EINVAL;
     if (a.window > 0x7fffffffu) return DFC_EINVAL;
     return DFC_OK;
 }
 
 template <typename E, int DP, int RW, int KT>
-dfc_status launch(const AttnArgs &a, hipStream_t st) {
+dfc_status launch(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
     using Sh = Shape<E, DP, RW, KT>;
     const void *fn = reinterpret_cast<const void *>(&attention_kernel<E, DP, RW, KT>);
     if (!allow_full_lds(fn)) return DFC_EHIP;
-    const uint64_t grid = uint64_t(a.piece_cap) * a.kv_heads;
+    const uint64_t grid = (uint64_t(p.tile_cap) + p.extra) * a.kv_heads;
     if (grid > 0x7fffffffull) return DFC_EUNSUPPORTED;
-    hipLaunchKernelGGL(schedule_kernel, dim3(1), dim3(kSchedThreads), 0, st, a);
     hipLaunchKernelGGL((attention_kernel<E, DP, RW, KT>), dim3(uint32_t(grid)), dim3(kThreads), Sh::kLds, st, a);
-    if (a.slot_cap)
-        hipLaunchKernelGGL((join_kernel<E, DP>), dim3(uint32_t(grid), uint32_t(RW)), dim3(kThreads), 0, st, a);
+    if (a.tiles) {
+        constexpr int WPR = RW == 4 ? 1 : 4;
+        hipLaunchKernelGGL((join_kernel<E, DP, WPR>),
+                           dim3(p.tile_cap * a.kv_heads, WPR == 4 ? p.most_rows : (p.most_rows + 7u) / 8u),
+                           dim3(kThreads), 0, st, a);
+    }
     return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
 }
 
 template <typename E>
 dfc_status launch_type(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
     switch (p.dp * 8 + p.rw) {
-        case 64 * 8 + 1: return launch<E, 64, 1, 32>(a, st);
-        case 64 * 8 + 2: return launch<E, 64, 2, 32>(a, st);
-        case 64 * 8 + 4: return launch<E, 64, 4, 64>(a, st);
-        case 128 * 8 + 1: return launch<E, 128, 1, 32>(a, st);
-        case 128 * 8 + 2: return launch<E, 128, 2, 32>(a, st);
-        case 128 * 8 + 4: return launch<E, 128, 4, 64>(a, st);
-        case 256 * 8 + 2: return launch<E, 256, 2, 32>(a, st);
-        default: return launch<E, 256, 4, 32>(a, st);
+        case 64 * 8 + 1: return launch<E, 64, 1, 32>(a, p, st);
+        case 64 * 8 + 2: return launch<E, 64, 2, 32>(a, p, st);
+        case 64 * 8 + 4: return launch<E, 64, 4, 64>(a, p, st);
+        case 128 * 8 + 1: return launch<E, 128, 1, 32>(a, p, st);
+        case 128 * 8 + 2: return launch<E, 128, 2, 32>(a, p, st);
+        case 128 * 8 + 4: return launch<E, 128, 4, 64>(a, p, st);
+        case 256 * 8 + 2: return launch<E, 256, 2, 32>(a, p, st);
+        default: return launch<E, 256, 4, 32>(a, p, st);
     }
 }
 
@@ -846,12 +924,14 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     a.rows_per_tile = p.rows_per_tile;
     a.key_tile = uint32_t(p.kt);
     a.min_piece = p.min_piece;
-    a.targets = p.targets;
-    a.piece_cap = p.piece_cap;
-    a.slot_cap = p.slot_cap;
+    a.resident = p.resident;
+    a.piece_cost = p.piece_cost;
+    a.join_cost = p.join_cost;
+    a.extra = p.extra;
+    a.tile_cap = p.tile_cap;
     uint8_t *ws = static_cast<uint8_t *>(in.workspace_dev);
-    a.count = reinterpret_cast<uint32_t *>(ws);
-    a.pieces = reinterpret_cast<Piece *>(ws + p.off_pieces);
+    a.tile_count = reinterpret_cast<uint32_t *>(ws);
+    a.tiles = p.extra ? reinterpret_cast<Tile *>(ws + p.off_tiles) : nullptr;
     a.part_ml = reinterpret_cast<float *>(ws + p.off_ml);
     a.part_o = reinterpret_cast<float *>(ws + p.off_o);
     a.status = in.status_dev;

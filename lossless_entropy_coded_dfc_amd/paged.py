@@ -13,47 +13,25 @@ for the C ABI (``include/dfc.h``).
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
 from typing import NamedTuple
 
 import torch
 
-from . import _check, _status_ptr, _stream, library
+from . import _check, library
 
 __all__ = ["PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace"]
 
-BF16, F16, F32 = 0, 1, 2
-_DTYPE = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+_DTYPE = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
-_i64x2, _i64x3 = ctypes.c_int64 * 2, ctypes.c_int64 * 3
-_ptr, _u32, _u64, _i64 = ctypes.c_void_p, ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int64
-
-
-class Cache(ctypes.Structure):
-    _fields_ = [("k_dev", _ptr), ("v_dev", _ptr), ("k_stride", _i64x3), ("v_stride", _i64x3), ("n_pages", _u32),
-                ("page_size", _u32), ("kv_heads", _u32), ("head_dim", _u32), ("dtype", _u32)]
-
-
-class PlanArgs(ctypes.Structure):
-    _fields_ = [("n_requests", _u32), ("max_pages", _u32), ("page_size", _u32), ("n_ring", _u32), ("tokens", _u64),
-                ("context_lens", _ptr), ("new_lens", _ptr), ("block_table", _ptr), ("table_stride", _i64),
-                ("free_pages", _ptr), ("cursor", _ptr), ("seq_lens", _ptr), ("cu_q", _ptr), ("slots", _ptr),
-                ("positions", _ptr), ("cursor_out", _ptr), ("status_dev", _ptr)]
-
-
-class AppendArgs(ctypes.Structure):
-    _fields_ = [("cache", Cache), ("tokens", _u64), ("k_dev", _ptr), ("v_dev", _ptr), ("k_src_stride", _i64x2),
-                ("v_src_stride", _i64x2), ("slots", _ptr), ("source_dtype", _u32), ("q_heads", _u32), ("q_dev", _ptr),
-                ("q_out_dev", _ptr), ("q_stride", _i64x2), ("q_out_stride", _i64x2), ("rot_dim", _u32),
-                ("interleaved", _u32), ("max_positions", _u32), ("positions", _ptr), ("rotary_dev", _ptr),
-                ("status_dev", _ptr)]
-
-
-class AttentionArgs(ctypes.Structure):
-    _fields_ = [("cache", Cache), ("heads", _u32), ("n_requests", _u32), ("max_pages", _u32), ("max_q_len", _u32),
-                ("tokens", _u64), ("q_dev", _ptr), ("out_dev", _ptr), ("q_stride", _i64x2), ("out_stride", _i64x2),
-                ("lse_dev", _ptr), ("block_table", _ptr), ("table_stride", _i64), ("cu_q", _ptr), ("seq_lens", _ptr),
-                ("scale", ctypes.c_float), ("causal", _u32), ("window", _u32), ("workspace_dev", _ptr),
-                ("workspace_bytes", _u64), ("status_dev", _ptr)]
+# The argument structures of include/dfc.h, packed in one go: filling a ctypes
+# structure field by field takes longer than the smaller kernels run.
+_CACHE = "QQ6q5I4x"
+CACHE = struct.Struct("=" + _CACHE)
+PLAN_ARGS = struct.Struct("=4I4Qq8Q")
+APPEND_ARGS = struct.Struct("=" + _CACHE + "QQQ4qQIIQQ4qIII4xQQQ")
+ATTENTION_ARGS = struct.Struct("=" + _CACHE + "4IQQQ4qQQqQQfII4xQQQ")
 
 
 class PagedPlan(NamedTuple):
@@ -72,66 +50,105 @@ def _lib():
     global _LIB
     if _LIB is None:
         lib = library()
-        for name, args in (("dfc_paged_plan", PlanArgs), ("dfc_paged_append", AppendArgs),
-                           ("dfc_paged_attention", AttentionArgs)):
+        for name in ("dfc_paged_plan", "dfc_paged_append", "dfc_paged_attention"):
             fn = getattr(lib, name)
-            fn.argtypes = [ctypes.POINTER(args), _ptr]
+            fn.argtypes = [ctypes.c_char_p, ctypes.c_void_p]
             fn.restype = ctypes.c_int
-        lib.dfc_paged_attention_workspace.argtypes = [ctypes.POINTER(AttentionArgs), ctypes.POINTER(_u64)]
+        lib.dfc_paged_attention_workspace.argtypes = [ctypes.c_char_p, ctypes.POINTER(ctypes.c_uint64)]
         lib.dfc_paged_attention_workspace.restype = ctypes.c_int
         _LIB = lib
     return _LIB
 
 
-def _vector(t, dtype, n, name):
-    """Device address of a contiguous vector of n elements (None: any number)."""
-    if t.dtype != dtype or t.dim() != 1 or not t.is_cuda or not t.is_contiguous():
-        raise TypeError(f"{name} must be a contiguous one-dimensional {dtype} device tensor")
-    if n is not None and t.shape[0] != n:
+def _device(t, name):
+    """The device of the call's main tensor, which must be the current one:
+    the launch goes to it."""
+    dev = t.get_device()
+    if dev < 0:
+        raise TypeError(f"{name} must be a device (cuda) tensor")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on device {dev}, not the current one")
+    return dev
+
+
+def _stream_of(stream, dev):
+    if stream is not None:
+        return int(stream)
+    return torch._C._cuda_getCurrentRawStream(dev)
+
+
+def _vector(t, dtype, n, dev, name):
+    """Device address of a contiguous vector of n elements."""
+    if t.dtype is not dtype or t.dim() != 1 or t.get_device() != dev or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous one-dimensional {dtype} tensor on the call's device")
+    if t.shape[0] != n:
         raise ValueError(f"{name} has {t.shape[0]} elements, not {n}")
     return t.data_ptr()
 
 
-def _rows(t, name, dtype, shape=None):
-    """Device address of (tokens, heads, head_dim) rows: any strides of the
-    first two dimensions, the last one contiguous."""
-    if t.dim() != 3 or not t.is_cuda or t.dtype != dtype:
-        raise TypeError(f"{name} must be a {dtype} device tensor of shape (tokens, heads, head_dim)")
-    if shape is not None and tuple(t.shape) != shape:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if t.stride(2) != 1 and t.shape[2] != 1:
+def _rows(t, name, dtype, shape, dev):
+    """Device address and strides of (tokens, heads, head_dim) rows: any
+    strides of the first two dimensions, the last one contiguous."""
+    if t.dtype is not dtype or t.get_device() != dev or t.dim() != 3:
+        raise TypeError(f"{name} must be a {dtype} tensor of shape (tokens, heads, head_dim) on the call's device")
+    if t.shape != shape:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 and shape[2] != 1:
         raise ValueError(f"the values of a head of {name} must be contiguous")
+    return t.data_ptr(), s0, s1
+
+
+def _cache(k, v, dev):
+    """The fields of dfc_paged_cache."""
+    dtype, shape = k.dtype, k.shape
+    if len(shape) != 4 or shape != v.shape or dtype is not v.dtype or k.get_device() != dev or v.get_device() != dev:
+        raise TypeError("k_cache and v_cache must be tensors of one shape (pages, page size, heads, head_dim) and one "
+                        "type on the call's device")
+    if dtype is not torch.bfloat16 and dtype is not torch.float16:
+        raise TypeError("the cache must be bfloat16 or float16")
+    k0, k1, k2, k3 = k.stride()
+    v0, v1, v2, v3 = v.stride()
+    if k3 != 1 or v3 != 1:
+        raise ValueError("the values of a head must be contiguous in the cache")
+    return (k.data_ptr(), v.data_ptr(), k0, k1, k2, v0, v1, v2, *shape, _DTYPE[dtype])
+
+
+def _table(t, n, dev):
+    """Device address, row stride and width of a block table of n rows."""
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise TypeError("block_table must be an int32 tensor of shape (requests, pages) on the call's device")
+    rows, width = t.shape
+    s0, s1 = t.stride()
+    if rows != n:
+        raise ValueError(f"block_table has {rows} rows for {n} requests")
+    if s1 != 1 and width > 1:
+        raise ValueError("the entries of a row of block_table must be contiguous")
+    # a single row's stride says nothing
+    return t.data_ptr(), s0 if n > 1 else width, width
+
+
+def _status(t, dev):
+    if t is None:
+        return 0
+    if t.get_device() != dev or t.element_size() != 4 or t.numel() < 1:
+        raise ValueError("status must be a device tensor of at least one 32-bit element")
     return t.data_ptr()
 
 
-def _cache(k, v):
-    if k.dim() != 4 or k.shape != v.shape or k.dtype != v.dtype or k.device != v.device or not k.is_cuda:
-        raise TypeError("k_cache and v_cache must be device tensors of one shape (pages, page size, heads, head_dim), "
-                        "one type and one device")
-    if k.dtype not in (torch.bfloat16, torch.float16):
-        raise TypeError("the cache must be bfloat16 or float16")
-    if k.stride(3) != 1 or v.stride(3) != 1:
-        raise ValueError("the values of a head must be contiguous in the cache")
-    pages, size, heads, dim = k.shape
-    return Cache(k.data_ptr(), v.data_ptr(), _i64x3(*k.stride()[:3]), _i64x3(*v.stride()[:3]), pages, size, heads, dim,
-                 _DTYPE[k.dtype])
+def _count(x, name):
+    """A size that the C structures hold in 32 bits."""
+    if not 0 <= x < 1 << 31:
+        raise ValueError(f"{name} must be between 0 and 2^31 - 1")
+    return x
 
 
-def _table(block_table, n_requests):
-    if block_table.dim() != 2 or block_table.dtype != torch.int32 or not block_table.is_cuda:
-        raise TypeError("block_table must be an int32 device tensor of shape (requests, pages)")
-    if block_table.shape[0] != n_requests:
-        raise ValueError(f"block_table has {block_table.shape[0]} rows for {n_requests} requests")
-    if block_table.shape[1] > 1 and block_table.stride(1) != 1:
-        raise ValueError("the entries of a row of block_table must be contiguous")
-    # a single row's stride says nothing
-    return max(block_table.stride(0), block_table.shape[1]) if n_requests <= 1 else block_table.stride(0)
-
-
-def _keep(tensor, stream):
-    """A tensor allocated here is used on the caller's stream."""
+def _keep(stream, dev, *tensors):
+    """Tensors allocated here are used on the caller's stream."""
     if stream is not None:
-        tensor.record_stream(torch.cuda.ExternalStream(int(stream), device=tensor.device))
+        ext = torch.cuda.ExternalStream(int(stream), device=dev)
+        for t in tensors:
+            t.record_stream(ext)
 
 
 def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_size: int, tokens: int, out=None,
@@ -147,23 +164,29 @@ def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_siz
     the length of the slots and positions, at least the step's new tokens (the
     rest become -1 and 0).  ``out``: a ``PagedPlan`` to write into (a captured
     step's buffers; its cursor may not be ``cursor``).  Asynchronous."""
+    dev = _device(block_table, "block_table")
     n = context_lens.shape[0] if context_lens.dim() == 1 else -1
-    table_stride = _table(block_table, n)
-    dev = block_table.device
+    table, table_stride, width = _table(block_table, n, dev)
+    _count(page_size, "page_size")
+    _count(tokens, "tokens")
+    i32, i64 = torch.int32, torch.int64
+    inputs = (_vector(context_lens, i32, n, dev, "context_lens"), _vector(new_lens, i32, n, dev, "new_lens"), table,
+              table_stride, _vector(free_pages, i32, free_pages.shape[0], dev, "free_pages"),
+              _vector(cursor, i64, 2, dev, "cursor"))
     if out is None:
-        whole = torch.empty(2 * n + 1 + tokens, dtype=torch.int32, device=dev)
-        wide = torch.empty(tokens + 2, dtype=torch.int64, device=dev)
-        out = PagedPlan(whole[:n], whole[n: 2 * n + 1], wide[:tokens], whole[2 * n + 1:], wide[tokens:])
-        _keep(whole, stream)
-        _keep(wide, stream)
-    args = PlanArgs(n, block_table.shape[1], page_size, free_pages.shape[0], tokens,
-                    _vector(context_lens, torch.int32, n, "context_lens"), _vector(new_lens, torch.int32, n, "new_lens"),
-                    block_table.data_ptr(), table_stride, _vector(free_pages, torch.int32, None, "free_pages"),
-                    _vector(cursor, torch.int64, 2, "cursor"), _vector(out.seq_lens, torch.int32, n, "seq_lens"),
-                    _vector(out.cu_q, torch.int32, n + 1, "cu_q"), _vector(out.slots, torch.int64, tokens, "slots"),
-                    _vector(out.positions, torch.int32, tokens, "positions"),
-                    _vector(out.cursor, torch.int64, 2, "the plan's cursor"), _status_ptr(status))
-    _check(_lib().dfc_paged_plan(ctypes.byref(args), _stream(stream)), "dfc_paged_plan")
+        out = PagedPlan(new_lens.new_empty(n), new_lens.new_empty(n + 1), cursor.new_empty(tokens),
+                        new_lens.new_empty(tokens), cursor.new_empty(2))
+        _keep(stream, dev, *out)
+        seq_lens, cu_q, slots, positions, cursor_out = (t.data_ptr() for t in out)
+    else:
+        seq_lens = _vector(out.seq_lens, i32, n, dev, "the plan's seq_lens")
+        cu_q = _vector(out.cu_q, i32, n + 1, dev, "the plan's cu_q")
+        slots = _vector(out.slots, i64, tokens, dev, "the plan's slots")
+        positions = _vector(out.positions, i32, tokens, dev, "the plan's positions")
+        cursor_out = _vector(out.cursor, i64, 2, dev, "the plan's cursor")
+    args = PLAN_ARGS.pack(n, width, page_size, free_pages.shape[0], tokens, *inputs, seq_lens, cu_q, slots, positions,
+                          cursor_out, _status(status, dev))
+    _check(_lib().dfc_paged_plan(args, _stream_of(stream, dev)), "dfc_paged_plan")
     return out
 
 
@@ -177,70 +200,59 @@ def paged_append(k, v, k_cache, v_cache, slots, q=None, q_out=None, positions=No
     by its token's ``positions`` (int32) first, and so is ``q`` (tokens,
     heads, head_dim); the rotated q, in the cache's type, is returned
     (``q_out``, or a new tensor).  Asynchronous."""
-    cache = _cache(k_cache, v_cache)
-    tokens = k.shape[0]
-    shape = (tokens, cache.kv_heads, cache.head_dim)
-    source = k.dtype
-    if source != torch.float32 and source != k_cache.dtype:
+    dev = _device(k_cache, "k_cache")
+    cache = _cache(k_cache, v_cache, dev)
+    tokens, source = k.shape[0], k.dtype
+    if source is not torch.float32 and source is not k_cache.dtype:
         raise TypeError("k and v must be float32 or of the cache's type")
-    args = AppendArgs(cache, tokens, _rows(k, "k", source, shape), _rows(v, "v", source, shape),
-                      _i64x2(*k.stride()[:2]), _i64x2(*v.stride()[:2]), _vector(slots, torch.int64, tokens, "slots"),
-                      _DTYPE[source], 0)
+    shape = (tokens, cache[10], cache[11])
+    k_ptr, k0, k1 = _rows(k, "k", source, shape, dev)
+    v_ptr, v0, v1 = _rows(v, "v", source, shape, dev)
+    q_heads = q_ptr = q0 = q1 = out_ptr = o0 = o1 = 0
     if q is not None:
-        args.q_dev = _rows(q, "q", source)
-        if q.shape[0] != tokens or q.shape[2] != cache.head_dim:
+        if q.dim() != 3 or q.shape[0] != tokens or q.shape[2] != cache[11]:
             raise ValueError("q must have k's tokens and head_dim")
+        q_heads = q.shape[1]
+        q_ptr, q0, q1 = _rows(q, "q", source, q.shape, dev)
         if q_out is None:
             q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
-            _keep(q_out, stream)
-        args.q_heads = q.shape[1]
-        args.q_out_dev = _rows(q_out, "q_out", k_cache.dtype, tuple(q.shape))
-        args.q_stride = _i64x2(*q.stride()[:2])
-        args.q_out_stride = _i64x2(*q_out.stride()[:2])
+            _keep(stream, dev, q_out)
+        out_ptr, o0, o1 = _rows(q_out, "q_out", k_cache.dtype, q.shape, dev)
+    rot = angles = max_pos = pos = 0
     if rotary is not None:
-        if rotary.dtype != torch.float32 or rotary.dim() != 2 or not rotary.is_cuda or not rotary.is_contiguous():
-            raise TypeError("rotary must be a contiguous float32 device tensor of shape (positions, rot_dim)")
+        if rotary.dtype is not torch.float32 or rotary.dim() != 2 or rotary.get_device() != dev or \
+                not rotary.is_contiguous():
+            raise TypeError("rotary must be a contiguous float32 tensor of shape (positions, rot_dim) on the call's "
+                            "device")
         if positions is None:
             raise ValueError("rotary needs positions")
-        args.rot_dim = rotary.shape[1]
-        args.interleaved = 1 if interleaved else 0
-        args.max_positions = rotary.shape[0]
-        args.positions = _vector(positions, torch.int32, tokens, "positions")
-        args.rotary_dev = rotary.data_ptr()
-    args.status_dev = _status_ptr(status)
-    _check(_lib().dfc_paged_append(ctypes.byref(args), _stream(stream)), "dfc_paged_append")
+        max_pos, rot = rotary.shape
+        pos = _vector(positions, torch.int32, tokens, dev, "positions")
+        angles = rotary.data_ptr()
+    args = APPEND_ARGS.pack(*cache, tokens, k_ptr, v_ptr, k0, k1, v0, v1, _vector(slots, torch.int64, tokens, dev, "slots"),
+                            _DTYPE[source], q_heads, q_ptr, out_ptr, q0, q1, o0, o1, rot, 1 if interleaved else 0,
+                            max_pos, pos, angles, _status(status, dev))
+    _check(_lib().dfc_paged_append(args, _stream_of(stream, dev)), "dfc_paged_append")
     return q_out
 
 
-def _attention_args(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window, max_q_len):
-    cache = _cache(k_cache, v_cache)
-    n = seq_lens.shape[0]
-    q_ptr = _rows(q, "q", k_cache.dtype)
-    tokens, heads, dim = q.shape
-    if dim != cache.head_dim or heads % cache.kv_heads or not heads:
-        raise ValueError("q must have the cache's head_dim and a multiple of its heads")
-    if window < 0 or max_q_len < 0:
-        raise ValueError("window and max_q_len may not be negative")
-    args = AttentionArgs(cache, heads, n, block_table.shape[1], max_q_len, tokens, q_ptr)
-    args.q_stride = _i64x2(*q.stride()[:2])
-    args.table_stride = _table(block_table, n)
-    args.block_table = block_table.data_ptr()
-    args.cu_q = _vector(cu_q, torch.int32, n + 1, "cu_q")
-    args.seq_lens = _vector(seq_lens, torch.int32, n, "seq_lens")
-    args.scale = dim ** -0.5 if scale is None else scale
-    args.causal = 1 if causal else 0
-    args.window = window
-    return args
+@functools.lru_cache(maxsize=1024)
+def _workspace_bytes(*sizes):
+    """dfc_paged_attention_workspace, a function of sizes alone."""
+    page_size, kv_heads, dim, dtype, heads, n, width, max_q_len, tokens = sizes
+    args = ATTENTION_ARGS.pack(16, 16, 0, 0, 0, 0, 0, 0, 1, page_size, kv_heads, dim, dtype, heads, n, width, max_q_len,
+                               tokens, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 0, 1.0, 0, 0, 0, 0, 0)
+    need = ctypes.c_uint64()
+    _check(_lib().dfc_paged_attention_workspace(args, ctypes.byref(need)), "dfc_paged_attention_workspace")
+    return need.value
 
 
 def paged_attention_workspace(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_q_len: int = 0) -> int:
     """Device bytes of the workspace ``paged_attention`` uses for these
     arguments (from their shapes alone)."""
-    args = _attention_args(q, k_cache, v_cache, block_table, cu_q, seq_lens, None, True, 0, max_q_len)
-    need = _u64()
-    _check(_lib().dfc_paged_attention_workspace(ctypes.byref(args), ctypes.byref(need)),
-           "dfc_paged_attention_workspace")
-    return need.value
+    _, page_size, kv_heads, dim = k_cache.shape
+    return _workspace_bytes(page_size, kv_heads, dim, _DTYPE[k_cache.dtype], q.shape[1], seq_lens.shape[0],
+                            block_table.shape[1], _count(max_q_len, "max_q_len"), q.shape[0])
 
 
 def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: float | None = None, causal: bool = True,
@@ -257,29 +269,45 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: flo
     a device uint8 tensor of at least ``paged_attention_workspace`` bytes that
     nothing else uses until the call's work has run (None: allocated here).
     Returns out, or (out, lse).  Asynchronous."""
-    args = _attention_args(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window, max_q_len)
+    dev = _device(q, "q")
+    cache = _cache(k_cache, v_cache, dev)
+    dtype = q.dtype
+    if dtype is not k_cache.dtype or q.dim() != 3:
+        raise TypeError("q must be a tensor of shape (tokens, heads, head_dim) of the cache's type")
+    n = seq_lens.shape[0]
+    shape = q.shape
+    tokens, heads, dim = shape
+    if dim != cache[11] or not heads or not cache[10] or heads % cache[10]:
+        raise ValueError("q must have the cache's head_dim and a multiple of its heads")
+    table, table_stride, width = _table(block_table, n, dev)
+    _count(window, "window")
+    _count(max_q_len, "max_q_len")
+    q_ptr, q0, q1 = _rows(q, "q", dtype, shape, dev)
     if out is None:
-        out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-        _keep(out, stream)
-    args.out_dev = _rows(out, "out", q.dtype, tuple(q.shape))
-    args.out_stride = _i64x2(*out.stride()[:2])
+        out = torch.empty(shape, dtype=dtype, device=q.device)
+        _keep(stream, dev, out)
+    out_ptr, o0, o1 = _rows(out, "out", dtype, shape, dev)
+    lse_ptr = 0
     if lse is True:
-        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
-        _keep(lse, stream)
-    if lse is not None:
-        if lse.dtype != torch.float32 or lse.shape != q.shape[:2] or not lse.is_cuda or not lse.is_contiguous():
-            raise TypeError("lse must be a contiguous float32 device tensor of shape (tokens, heads)")
-        args.lse_dev = lse.data_ptr()
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+        _keep(stream, dev, lse)
+        lse_ptr = lse.data_ptr()
+    elif lse is not None:
+        if lse.dtype is not torch.float32 or lse.shape != shape[:2] or lse.get_device() != dev or \
+                not lse.is_contiguous():
+            raise TypeError("lse must be a contiguous float32 tensor of shape (tokens, heads) on the call's device")
+        lse_ptr = lse.data_ptr()
     if workspace is None:
-        need = _u64()
-        _check(_lib().dfc_paged_attention_workspace(ctypes.byref(args), ctypes.byref(need)),
-               "dfc_paged_attention_workspace")
-        workspace = torch.empty(need.value, dtype=torch.uint8, device=q.device)
-        _keep(workspace, stream)
-    elif not workspace.is_cuda or not workspace.is_contiguous():
-        raise TypeError("workspace must be a contiguous device tensor")
-    args.workspace_dev = workspace.data_ptr()
-    args.workspace_bytes = workspace.numel() * workspace.element_size()
-    args.status_dev = _status_ptr(status)
-    _check(_lib().dfc_paged_attention(ctypes.byref(args), _stream(stream)), "dfc_paged_attention")
+        workspace = torch.empty(_workspace_bytes(*cache[9:], heads, n, width, max_q_len, tokens), dtype=torch.uint8,
+                                device=q.device)
+        _keep(stream, dev, workspace)
+    elif workspace.get_device() != dev or not workspace.is_contiguous():
+        raise TypeError("workspace must be a contiguous tensor on the call's device")
+    args = ATTENTION_ARGS.pack(*cache, heads, n, width, max_q_len, tokens, q_ptr, out_ptr, q0, q1, o0, o1, lse_ptr,
+                               table, table_stride, _vector(cu_q, torch.int32, n + 1, dev, "cu_q"),
+                               _vector(seq_lens, torch.int32, n, dev, "seq_lens"),
+                               dim ** -0.5 if scale is None else scale, 1 if causal else 0, window,
+                               workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                               _status(status, dev))
+    _check(_lib().dfc_paged_attention(args, _stream_of(stream, dev)), "dfc_paged_attention")
     return out if lse is None else (out, lse)
