@@ -69,6 +69,8 @@ struct AttnArgs {
     uint32_t n_pages, page_shift, kv_heads, group, heads, dim;
     uint32_t n_requests, tokens, max_pages, window;
     int32_t causal;
+    int32_t simple_rows;       // K and V have one layout, and a load's rows lie in one page
+    uint32_t page_units, slot_units;  // its strides in 16-byte pieces (simple_rows)
     float scale, scale_log2;   // scores by exp2: scale log2(e)
     uint32_t rows_per_tile, key_tile, min_piece;  // a piece has min_piece key tiles or more
     uint32_t resident;         // workgroups that run at once
@@ -488,26 +490,49 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     bool missing = false;
     uint32_t odd = 0;  // a tile with masked keys held a value that is not finite
 
-    // The page of key start + lane of a tile, -1 where there is none.
+    // The entry of the block table for key start + lane of a tile (-1 past the
+    // piece), as it was read: it is looked at a step later.
     auto pages_of = [&](int32_t start) -> int32_t {
         const int32_t key = start + int32_t(lane % KT);
-        int32_t page = -1;
-        if (key < hi) {
-            page = table[key >> a.page_shift];
-            if (uint32_t(page) >= a.n_pages) {
-                page = -1;
-                missing = true;
-            }
-        }
-        return page;
+        return key < hi ? table[key >> a.page_shift] : -1;
     };
+    // A load instruction of a wavefront covers kRpi rows, whole ones.  Where a
+    // tile lies wholly inside the piece and such rows inside a page, their
+    // address is one scalar and a constant per lane; other tiles find every
+    // lane's row by itself and leave zeros where there is none.
+    constexpr int kRpi = 64 / CPR;
+    const bool in_dim = lane % CPR * 8u < a.dim;
+    const uint32_t lane_off = uint32_t((int64_t(lane / CPR) * a.k_stride[1] + (in_dim ? lane % CPR * 8u : 0u)) * 2);
     uint4 kr[NL], vr[NL];
     auto load = [&](int32_t start, int32_t pages) {
+        const bool none = uint32_t(pages) >= a.n_pages;
+        if (a.simple_rows && start + KT <= hi && !__any(none)) {
+#pragma unroll
+            for (int n = 0; n < NL; ++n) {
+                const uint32_t r0 = (rw + uint32_t(n) * RW) * kRpi;
+                const uint32_t page = __builtin_amdgcn_readlane(pages, r0);
+                const uint32_t in_page = (uint32_t(start) + r0) & uint32_t(page_mask);
+                const uint64_t off = (uint64_t(page) * a.page_units + uint64_t(in_page) * a.slot_units) * 16u;
+                kr[n] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(kbase) + off + lane_off);
+                vr[n] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(vbase) + off + lane_off);
+            }
+            if (a.dim != DP) {
+                // lanes past the head have read its first piece
+                const uint32_t keep = in_dim ? ~0u : 0u;
+#pragma unroll
+                for (int n = 0; n < NL; ++n) {
+                    kr[n].x &= keep, kr[n].y &= keep, kr[n].z &= keep, kr[n].w &= keep;
+                    vr[n].x &= keep, vr[n].y &= keep, vr[n].z &= keep, vr[n].w &= keep;
+                }
+            }
+            return;
+        }
+        if (none && start + int32_t(lane % KT) < hi) missing = true;
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const uint32_t i = gtid + uint32_t(n) * GT;
             const uint32_t r = i / CPR, ch = i % CPR;
-            const int32_t page = __shfl(pages, int(r));
+            const int32_t page = __shfl(none ? -1 : pages, int(r));
             kr[n] = vr[n] = uint4{0, 0, 0, 0};
             if (page >= 0 && ch * 8u < a.dim) {
                 const int64_t in_page = (start + int32_t(r)) & page_mask;
@@ -521,6 +546,17 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     int32_t pages = pages_of(tile_start(0));
     load(tile_start(0), pages);
     pages = pages_of(tile_start(1));
+
+    // Where this lane reads its operands in a tile's K and V.  A later piece of
+    // a K row is an exclusive or away, later rows an immediate offset.
+    const uint32_t k_at = k_place<DP>(c, h) * 16u;
+    uint32_t v_at[ND];
+#pragma unroll
+    for (int d = 0; d < ND; ++d) {
+        const uint32_t i16 = lane % 16u;
+        v_at[d] = Sh::kTileBytes + 8u * (i16 & 1u) +
+                  16u * v_place<DP>(4u * h + i16 / 4u, 4u * uint32_t(d) + 2u * ((lane >> 4) & 1u) + (i16 % 4u) / 2u);
+    }
 
     for (int32_t step = 0; step < n_steps; ++step) {
         const int32_t start = tile_start(step);
@@ -554,7 +590,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         for (int k = 0; k < NQ; ++k)
 #pragma unroll
             for (int b = 0; b < NB; ++b) {
-                const V8 kf = __builtin_bit_cast(V8, kl[k_place<DP>(32u * uint32_t(b) + c, 2u * uint32_t(k) + h)]);
+                const V8 kf = *reinterpret_cast<const V8 *>(buf + (k_at ^ (uint32_t(k) << 5)) + b * 32 * DP * 2);
                 s[b] = T::mfma(kf, qf[k], s[b]);
             }
         const bool masked = start + KT > hi_min || start < lo_max;
@@ -594,17 +630,14 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             }
 
         // O^T += V^T P^T
-        const uint32_t i16 = lane % 16u;
         auto v_frag = [&](int st, int d) -> V8 {
-            const uint32_t key = 16u * uint32_t(st) + 4u * h + i16 / 4u;
-            const uint32_t ch = 4u * uint32_t(d) + 2u * ((lane >> 4) & 1u) + (i16 % 4u) / 2u;
             using L4 = __attribute__((address_space(3))) s16x4;
             struct Two {
                 s16x4 a, b;
             } t;
-            const uint8_t *at = reinterpret_cast<const uint8_t *>(vl);
-            t.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 16u * v_place<DP>(key, ch) + 8u * (i16 & 1u)));
-            t.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 16u * v_place<DP>(key + 8u, ch) + 8u * (i16 & 1u)));
+            const uint8_t *at = buf + v_at[d] + st * 16 * DP * 2;
+            t.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)at);
+            t.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 8 * DP * 2));
             return __builtin_bit_cast(V8, t);
         };
         if (masked) {
@@ -907,6 +940,13 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
         a.k_stride[i] = in.cache.k_stride[i];
         a.v_stride[i] = in.cache.v_stride[i];
     }
+    bool simple = in.cache.page_size >= 512u / uint32_t(p.dp);
+    for (int i = 0; i < 3; ++i) simple = simple && a.k_stride[i] == a.v_stride[i] && a.k_stride[i] / 8 < (int64_t(1) << 31);
+    // a lane's offset within its instruction's rows is 32 bits
+    simple = simple && a.k_stride[1] < (int64_t(1) << 27);
+    a.simple_rows = simple ? 1 : 0;
+    a.page_units = simple ? uint32_t(a.k_stride[0] / 8) : 0u;
+    a.slot_units = simple ? uint32_t(a.k_stride[1] / 8) : 0u;
     a.table_stride = in.table_stride;
     a.n_pages = in.cache.n_pages;
     a.page_shift = dfc::log2_of(in.cache.page_size);
