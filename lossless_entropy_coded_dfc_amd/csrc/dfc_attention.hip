@@ -582,17 +582,36 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         }
         if (idle || start >= hi_max || start + KT <= lo_min) continue;
 
-        // S^T = K Q^T
+        // S^T = K Q^T.  Operands are read a group of four ahead of the
+        // products that use them; left to itself the compiler reads each one
+        // just before its product and waits for it.
         f32x16 s[NB];
 #pragma unroll
         for (int b = 0; b < NB; ++b) s[b] = f32x16{};
+        {
+            constexpr int KG = 4 / NB;       // 16-column steps per group
+            constexpr int NG = NQ / KG;
+            V8 kf[2][KG][NB];
+            auto read = [&](int g) {
 #pragma unroll
-        for (int k = 0; k < NQ; ++k)
+                for (int k = 0; k < KG; ++k)
 #pragma unroll
-            for (int b = 0; b < NB; ++b) {
-                const V8 kf = *reinterpret_cast<const V8 *>(buf + (k_at ^ (uint32_t(k) << 5)) + b * 32 * DP * 2);
-                s[b] = T::mfma(kf, qf[k], s[b]);
+                    for (int b = 0; b < NB; ++b)
+                        kf[g & 1][k][b] = *reinterpret_cast<const V8 *>(
+                            buf + (k_at ^ (uint32_t(g * KG + k) << 5)) + b * 32 * DP * 2);
+            };
+            read(0);
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                if (g + 1 < NG) read(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int k = 0; k < KG; ++k)
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) s[b] = T::mfma(kf[g & 1][k][b], qf[g * KG + k], s[b]);
+                __builtin_amdgcn_sched_barrier(0);
             }
+        }
         const bool masked = start + KT > hi_min || start < lo_max;
         if (masked) {
 #pragma unroll
@@ -652,10 +671,28 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             }
             odd |= bits & 0x80008000u;
         }
+        {
+            // groups of up to four operands, as above
+            constexpr int VG = ND < 4 ? ND : 4;
+            constexpr int NG = NS * ND / VG;
+            V8 vf[2][VG];
+            auto read = [&](int g) {
 #pragma unroll
-        for (int st = 0; st < NS; ++st)
+                for (int j = 0; j < VG; ++j) vf[g & 1][j] = v_frag((g * VG + j) / ND, (g * VG + j) % ND);
+            };
+            read(0);
 #pragma unroll
-            for (int d = 0; d < ND; ++d) acc[d] = T::mfma(v_frag(st, d), p[st], acc[d]);
+            for (int g = 0; g < NG; ++g) {
+                if (g + 1 < NG) read(g + 1);
+                __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+                for (int j = 0; j < VG; ++j) {
+                    const int d = (g * VG + j) % ND;
+                    acc[d] = T::mfma(vf[g & 1][j], p[(g * VG + j) / ND], acc[d]);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
     }
     if (missing && a.status) atomicOr(a.status, kStatusCorrupt);
 
