@@ -506,7 +506,7 @@ typedef struct {
  * count as zeros (DFC_ECORRUPT in the status).  Rows past cu_q[n_requests]
  * are not written.  Errors: DFC_EINVAL, DFC_ESIZE (workspace),
  * DFC_EUNSUPPORTED (types, head_dim over 256, tokens x heads / kv_heads past
- * 2^30), DFC_EHIP. */
+ * 2^30, strides of the cache past 2^34), DFC_EHIP. */
 dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream);
 
 /* Bytes of the workspace for those arguments (host; reads sizes only, no

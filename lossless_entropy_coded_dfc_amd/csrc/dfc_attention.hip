@@ -30,263 +30,15 @@
 #include <cstring>
 
 #include "dfc.h"
+#include "dfc_attention_schedule.h"
 #include "dfc_decode_core.h"
+#include "dfc_format.h"
 #include "dfc_paged.h"
 
 namespace {
 
 using f32x16 = __attribute__((ext_vector_type(16))) float;
 using s16x4 = __attribute__((ext_vector_type(4))) short;
-
-constexpr uint32_t kThreads = 256;
-constexpr uint32_t kWaves = 4;
-
-// One piece of work: a tile of rows of one request and a range of keys, for
-// one cache head.
-struct Piece {
-    uint32_t req, row0;     // request; first row of the tile
-    int32_t q_start, q_len, kv_len;
-    int32_t lo, hi;         // keys
-    uint32_t split, splits; // which piece of the tile, of how many
-    uint32_t slot;          // first partial result of the tile (splits > 1)
-    uint32_t tile;          // number of the tile in the step
-};
-
-// A tile, for the joining of its pieces.
-struct alignas(16) Tile {
-    uint32_t splits, slot;
-    int32_t token0;         // row of q of the request's first token
-    uint32_t row0, rows;
-    uint32_t pad[3];
-};
-
-struct AttnArgs {
-    const void *q, *k, *v;
-    void *out;
-    float *lse;
-    const int32_t *table, *cu_q, *seq_lens;
-    int64_t q_stride[2], out_stride[2], k_stride[3], v_stride[3], table_stride;
-    uint32_t n_pages, page_shift, kv_heads, group, heads, dim;
-    uint32_t n_requests, tokens, max_pages, window;
-    int32_t causal;
-    int32_t simple_rows;       // K and V have one layout, and a load's rows lie in one page
-    uint32_t page_units, slot_units;  // its strides in 16-byte pieces (simple_rows)
-    float scale, scale_log2;   // scores by exp2: scale log2(e)
-    uint32_t rows_per_tile, key_tile, min_piece;  // a piece has min_piece key tiles or more
-    uint32_t resident;         // workgroups that run at once
-    float piece_cost, join_cost;  // what a piece, and the joining, cost in key tiles
-    uint32_t extra;            // pieces there may be beyond one a tile
-    uint32_t tile_cap;
-    uint32_t *tile_count;
-    Tile *tiles;               // null: no tile can be split
-    float *part_o, *part_ml;
-    uint32_t *status;
-};
-
-// -------------------------------------------------------------- schedule
-//
-// Every workgroup finds its own piece from the step's lengths.  A request's
-// tiles (n of them, the longest of c key tiles) are cut into S = ceil(c / L)
-// pieces each, so the pieces before a request are a prefix sum of n S, and
-// what all workgroups have to agree on is L.  Reading the lengths costs each
-// workgroup about a microsecond; a kernel that lists the pieces first, and
-// its launch, cost the step more than ten.
-
-struct Req {
-    int32_t q_start, q_len, kv_len;
-};
-
-// A request's ranges, held inside the buffers whatever the lengths say.
-__device__ __forceinline__ Req request(const AttnArgs &a, uint32_t r, uint32_t &bad) {
-    Req q;
-    const int32_t c0 = a.cu_q[r], c1 = a.cu_q[r + 1];
-    q.q_start = min(max(c0, 0), int32_t(a.tokens));
-    q.q_len = min(max(c1, q.q_start), int32_t(a.tokens)) - q.q_start;
-    const int64_t room = int64_t(a.max_pages) << a.page_shift;
-    const int32_t s = a.seq_lens[r];
-    const int32_t most = int32_t(min(room, int64_t(0x7fffff00)));  // a key tile past it is still an int
-    q.kv_len = min(max(s, 0), most);
-    if (c0 < 0 || c1 < c0 || c1 > int32_t(a.tokens) || q.kv_len != s) bad |= kStatusCorrupt;
-    return q;
-}
-
-// Keys [lo, hi) that the rows row0 .. of a tile see between them, lo at a
-// multiple of the key tile.
-__device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint32_t row0, int32_t &lo, int32_t &hi) {
-    const int32_t t0 = int32_t(row0 / a.group);
-    const int32_t rows = int32_t(min(uint64_t(a.rows_per_tile), uint64_t(q.q_len) * a.group - row0));
-    const int32_t t1 = int32_t((row0 + uint32_t(rows) - 1) / a.group);
-    const int64_t base = int64_t(q.kv_len) - q.q_len;
-    const int64_t end = a.causal ? min(int64_t(q.kv_len), base + t1 + 1) : int64_t(q.kv_len);
-    int64_t begin = a.window ? max(int64_t(0), base + t0 + 1 - int64_t(a.window)) : 0;
-    begin = begin / a.key_tile * a.key_tile;
-    hi = int32_t(max(end, int64_t(0)));
-    lo = int32_t(min(begin, int64_t(hi)));
-}
-
-__device__ __forceinline__ uint32_t key_tiles(const AttnArgs &a, int32_t lo, int32_t hi) {
-    return (uint32_t(hi - lo) + a.key_tile - 1u) / a.key_tile;
-}
-
-__device__ __forceinline__ uint32_t ceil_of(uint32_t x, uint32_t y) { return (x + y - 1u) / y; }
-
-// Tiles of rows of a request, and the key tiles of its last one (the longest
-// but for a window's edge).
-__device__ __forceinline__ void tiles_of(const AttnArgs &a, const Req &q, uint32_t &n, uint32_t &c) {
-    n = uint32_t((uint64_t(uint32_t(q.q_len)) * a.group + a.rows_per_tile - 1u) / a.rows_per_tile);
-    c = 0;
-    if (n) {
-        int32_t lo, hi;
-        tile_keys(a, q, (n - 1u) * a.rows_per_tile, lo, hi);
-        c = key_tiles(a, lo, hi);
-    }
-}
-
-__device__ __forceinline__ float wave_max(float x) {
-#pragma unroll
-    for (int d = 32; d; d /= 2) x = fmaxf(x, __shfl_xor(x, d));
-    return x;
-}
-
-// L for up to 64 requests, one a lane: every lane tries one value, counts the
-// pieces p it makes and takes
-//     rounds (L + piece_cost), rounds = ceil(p heads / resident),
-// for its time; the least wins.  Cutting one long request into as many equal
-// pieces as run at once, cutting many ragged ones finer so that the last
-// round is full, and not cutting where it does not pay all come out of it.
-__device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, uint32_t c) {
-    const uint32_t lane = threadIdx.x % kWave;
-    const float longest = wave_max(float(c));
-    const float parts = lane < 32u ? float(lane + 1u) : 32.0f * __builtin_amdgcn_exp2f(float(lane - 31u) * 0.15625f);
-    const uint32_t piece = max(a.min_piece, uint32_t(ceilf(longest / parts)));
-    const float inv = 1.0f / float(piece);
-    uint64_t p = 0;
-    uint32_t tiles = 0;
-    for (uint32_t r = 0; r < a.n_requests; ++r) {
-        const uint32_t nr = __builtin_amdgcn_readlane(n, r), cr = __builtin_amdgcn_readlane(c, r);
-        uint32_t s = uint32_t(float(cr) * inv);  // never below ceil(c / piece) after this
-        s += s * piece < cr;
-        s += s * piece < cr;
-        tiles += nr;
-        p += uint64_t(nr) * max(s, 1u);
-    }
-    const float rounds = ceilf(float(p) * float(a.kv_heads) / float(a.resident));
-    float t = rounds * (float(piece) + a.piece_cost);
-    if (float(piece) < longest) t += a.join_cost;
-    if (p - tiles > a.extra) t = 3e38f;
-    const float best = -wave_max(-t);
-    const uint32_t who = __builtin_ctzll(__ballot(t == best));
-    return __builtin_amdgcn_readlane(piece, who);
-}
-
-// The piece `index` of the step (for every cache head), false if there is
-// none.  `scratch` is LDS that nothing else uses meanwhile.  Row ranges that
-// overlap could make more tiles than q has room for: then there are none.
-__device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bool first, uint32_t *scratch, Piece &w) {
-    const uint32_t tid = threadIdx.x, lane = tid % kWave;
-    uint32_t bad = 0;
-    uint32_t within = 0, parts = 1, n_tiles = 0, slot0 = 0, tile0 = 0, piece = 1;
-    if (a.n_requests <= 64) {
-        Req q{0, 0, 0};
-        if (lane < a.n_requests) q = request(a, lane, bad);
-        uint32_t n, c;
-        tiles_of(a, q, n, c);
-        piece = a.extra ? choose_piece(a, n, c) : 1u << 30;
-        const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u;
-        const uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), in = wave_inclusive_scan(n);
-        const bool fits = uint32_t(__builtin_amdgcn_readlane(in, 63)) <= a.tile_cap;
-        if (!fits) bad |= kStatusCorrupt;
-        if (first && tid == 63) *a.tile_count = fits ? in : 0u;
-        if (first && bad && a.status) atomicOr(a.status, bad);
-        if (!fits || index >= uint32_t(__builtin_amdgcn_readlane(ix, 63))) return false;
-        const uint32_t r = 63u - uint32_t(__builtin_clzll(__ballot(x > 0u && ix - x <= index)));
-        within = index - uint32_t(__builtin_amdgcn_readlane(ix - x, r));
-        parts = __builtin_amdgcn_readlane(s, r);
-        n_tiles = __builtin_amdgcn_readlane(n, r);
-        slot0 = __builtin_amdgcn_readlane(iy - y, r);
-        tile0 = __builtin_amdgcn_readlane(in - n, r);
-        w.req = r;
-        w.q_start = __builtin_amdgcn_readlane(q.q_start, r);
-        w.q_len = __builtin_amdgcn_readlane(q.q_len, r);
-        w.kv_len = __builtin_amdgcn_readlane(q.kv_len, r);
-    } else {
-        // more requests than lanes: L from the sum of their key tiles
-        const uint32_t wave = tid / kWave;
-        uint64_t *sums = reinterpret_cast<uint64_t *>(scratch);
-        uint64_t all = 0, tiles = 0;
-        for (uint32_t r = tid; r < a.n_requests; r += kThreads) {
-            uint32_t n, c;
-            tiles_of(a, request(a, r, bad), n, c);
-            all += uint64_t(n) * c;
-            tiles += n;
-        }
-#pragma unroll
-        for (int d = 32; d; d /= 2) {
-            all += __shfl_xor(all, d);
-            tiles += __shfl_xor(tiles, d);
-        }
-        if (lane == 0) sums[wave] = all, sums[kWaves + wave] = tiles;
-        __syncthreads();
-        all = (sums[0] + sums[1] + sums[2] + sums[3]) * a.kv_heads;
-        const bool fits = sums[4] + sums[5] + sums[6] + sums[7] <= a.tile_cap;
-        if (!fits) bad |= kStatusCorrupt;
-        const uint64_t target = uint64_t(a.extra) * a.kv_heads;
-        piece = a.extra ? uint32_t(min(uint64_t(1) << 30, max(uint64_t(a.min_piece), (all + target - 1u) / target)))
-                        : 1u << 30;
-        uint32_t px = 0, py = 0, pn = 0;  // before this chunk of requests
-        uint32_t *found = scratch + 16, *part = scratch + 32;
-        if (tid == 0) found[0] = 0;
-        for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kThreads) {
-            Req q{0, 0, 0};
-            uint32_t unused = 0, n, c;
-            if (r0 + tid < a.n_requests) q = request(a, r0 + tid, unused);
-            tiles_of(a, q, n, c);
-            const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u;
-            uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), in = wave_inclusive_scan(n);
-            __syncthreads();  // part has been read
-            if (lane == 63u) part[3u * wave] = ix, part[3u * wave + 1u] = iy, part[3u * wave + 2u] = in;
-            __syncthreads();
-            ix += px, iy += py, in += pn;
-            for (uint32_t k = 0; k < kWaves; ++k) {
-                const uint32_t tx = part[3u * k], ty = part[3u * k + 1u], tn = part[3u * k + 2u];
-                if (k < wave) ix += tx, iy += ty, in += tn;
-                px += tx, py += ty, pn += tn;
-            }
-            if (ix - x <= index && index < ix) {
-                found[0] = 1;
-                found[1] = r0 + tid, found[2] = uint32_t(q.q_start), found[3] = uint32_t(q.q_len);
-                found[4] = uint32_t(q.kv_len), found[5] = index - (ix - x), found[6] = s, found[7] = n;
-                found[8] = iy - y, found[9] = in - n;
-            }
-            if (!first && px > index) break;  // this chunk had it
-        }
-        __syncthreads();
-        if (first && tid == 0) *a.tile_count = fits ? pn : 0u;
-        if (first && bad && a.status) atomicOr(a.status, bad);
-        uint32_t f[10];
-#pragma unroll
-        for (int i = 0; i < 10; ++i) f[i] = __builtin_amdgcn_readfirstlane(found[i]);
-        __syncthreads();  // read by all before the scratch is used again
-        if (!f[0] || !fits) return false;
-        w.req = f[1];
-        w.q_start = int32_t(f[2]), w.q_len = int32_t(f[3]), w.kv_len = int32_t(f[4]);
-        within = f[5], parts = f[6], n_tiles = f[7], slot0 = f[8], tile0 = f[9];
-    }
-    // the later tiles of a request see more keys: they come first
-    const uint32_t tile = within / parts;
-    w.split = within - tile * parts;
-    w.row0 = (n_tiles - 1u - tile) * a.rows_per_tile;
-    int32_t lo, hi;
-    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi);
-    const uint32_t c = key_tiles(a, lo, hi);
-    w.splits = min(parts, max(1u, ceil_of(c, piece)));
-    w.slot = slot0 + tile * parts;
-    w.tile = tile0 + tile;
-    // even shares of the key tiles
-    w.lo = lo + int32_t(uint32_t(uint64_t(c) * w.split / w.splits) * a.key_tile);
-    w.hi = min(hi, lo + int32_t(uint32_t(uint64_t(c) * (w.split + 1u) / w.splits) * a.key_tile));
-    return w.split < w.splits;
-}
 
 // ------------------------------------------------------------- attention
 
@@ -333,19 +85,6 @@ __device__ __forceinline__ float other_half(float x) {
     return __uint_as_float((threadIdx.x & 32u) ? r[0] : r[1]);
 }
 
-template <typename E, int DP, int RW, int KT>
-struct Shape {
-    static constexpr int KW = kWaves / RW;             // groups along the keys
-    static constexpr int kBuffers = RW == 1 ? 1 : 2;   // a wavefront alone needs no second one
-    static constexpr uint32_t kTileBytes = KT * DP * 2;          // of K or of V
-    static constexpr uint32_t kGroupBytes = 2 * kTileBytes * kBuffers;
-    static constexpr uint32_t kOutBytes = 32 * DP * 4;           // a wavefront's rows in fp32
-    static constexpr uint32_t kLoop = KW * kGroupBytes;
-    static constexpr uint32_t kEnd = kWaves * kOutBytes;
-    static constexpr uint32_t kMl = kLoop > kEnd ? kLoop : kEnd;  // offset of the joined maxima and sums
-    static constexpr uint32_t kLds = kMl + kWaves * 32 * 8;
-};
-
 // The same sums for 32 rows of a wavefront, a row at a time and without
 // matrix instructions, so that a key that a row does not see takes no part at
 // all: for tiles in which such a key's value is not finite.  Lanes take keys
@@ -357,8 +96,8 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
     using V8 = __attribute__((ext_vector_type(8))) E;
     const uint32_t lane = threadIdx.x % kWave;
     const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
-    const E *kbase = static_cast<const E *>(a.k) + int64_t(kvh) * a.k_stride[2];
-    const E *vbase = static_cast<const E *>(a.v) + int64_t(kvh) * a.v_stride[2];
+    const E *kbase = static_cast<const E *>(a.k) + uint64_t(kvh) * a.k_units[2] * 8u;
+    const E *vbase = static_cast<const E *>(a.v) + uint64_t(kvh) * a.v_units[2] * 8u;
     const int32_t page_mask = (1 << a.page_shift) - 1;
     constexpr int NO = DP / 64;
 #pragma unroll 1
@@ -379,10 +118,10 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
             if (int32_t(lane) < kt && key >= see_lo && key < see_hi) page = table[key >> a.page_shift];
             const bool seen = int32_t(lane) < kt && key >= see_lo && key < see_hi;
             if (uint32_t(page) >= a.n_pages) page = -1;  // counts as zeros
-            const int64_t in_page = key & page_mask;
+            const uint32_t in_page = uint32_t(key & page_mask);
             float z = 0.0f;
             if (page >= 0) {
-                const E *kp = kbase + page * a.k_stride[0] + in_page * a.k_stride[1];
+                const E *kp = kbase + (uint64_t(uint32_t(page)) * a.k_units[0] + uint64_t(in_page) * a.k_units[1]) * 8u;
                 for (uint32_t d = 0; d < a.dim; d += 8u) {
                     const V8 x = *reinterpret_cast<const V8 *>(kp + d), y = *reinterpret_cast<const V8 *>(qp + d);
 #pragma unroll
@@ -410,7 +149,8 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
                 if (!((seen_mask & page_in) >> k & 1u)) continue;
                 const float p = __shfl(e, k);
                 const int32_t pg = __shfl(page, k);
-                const E *vp = vbase + pg * a.v_stride[0] + int64_t((start + k) & page_mask) * a.v_stride[1];
+                const E *vp = vbase + (uint64_t(uint32_t(pg)) * a.v_units[0] +
+                                       uint64_t(uint32_t((start + k) & page_mask)) * a.v_units[1]) * 8u;
 #pragma unroll
                 for (int j = 0; j < NO; ++j)
                     if (lane + 64u * uint32_t(j) < a.dim) o[j] += p * float(vp[lane + 64u * uint32_t(j)]);
@@ -425,204 +165,166 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
     }
 }
 
-template <typename E, int DP, int RW, int KT>
-__global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a) {
+// The kernel's arguments, read again from here on: what only the end needs
+// would otherwise sit in scalar registers through the loop, which has none to
+// spare.
+__device__ __forceinline__ const AttnArgs &again(const AttnArgs &a) {
+#ifdef __HIP_DEVICE_COMPILE__
+    uint64_t p = reinterpret_cast<uint64_t>(__builtin_amdgcn_kernarg_segment_ptr());
+    asm volatile("" : "+s"(p));
+    return *reinterpret_cast<const __attribute__((address_space(4))) AttnArgs *>(p);
+#else
+    return a;
+#endif
+}
+
+constexpr auto nothing = [](int) {};
+
+// A wavefront's 32 rows: their queries, limits and running sums.  Lane l has
+// row l mod 32 (half l / 32 of its keys and columns).
+template <typename E, int DP, int KT>
+struct Rows {
     using T = Type<E>;
     using V8 = typename T::V8;
-    using Sh = Shape<E, DP, RW, KT>;
-    constexpr int KW = Sh::KW;
-    constexpr int CPR = DP / 8;                       // 16-byte pieces per row
-    constexpr int GT = 64 * RW;                       // threads that load a tile together
-    constexpr int NL = KT * CPR / GT;                 // pieces of K (and of V) per thread
-    constexpr int NB = KT / 32, NS = KT / 16, ND = DP / 32, NQ = DP / 16;
-    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
-
-    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
-    Piece w;
-    if (!find_piece(a, index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
-    const uint32_t lane = threadIdx.x % kWave;
-    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const uint32_t rw = wave % RW, kw = wave / RW;
-    const uint32_t c = lane & 31u, h = lane >> 5;
-    const int32_t n_rows = w.q_len * int32_t(a.group);
-    const int32_t lo = w.lo, hi = w.hi;
-
-    // this lane's row
-    const int32_t row = int32_t(w.row0 + 32u * rw + c);
-    const bool row_in = row < n_rows;
-    const int32_t row_c = min(row, n_rows - 1);
-    const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
-    const int32_t pos = w.kv_len - w.q_len + tok;
-    const int32_t see_hi = a.causal ? min(pos + 1, hi) : hi;
-    const int32_t see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
-    // over the wavefront's rows (positions ascend with the row)
-    const int32_t hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
-    const int32_t hi_max = __builtin_amdgcn_readlane(see_hi, 31), lo_max = __builtin_amdgcn_readlane(see_lo, 31);
-    const bool idle = int32_t(w.row0 + 32u * rw) >= n_rows;
+    static constexpr int NB = KT / 32, NS = KT / 16, ND = DP / 32, NQ = DP / 16;
 
     V8 qf[NQ];
-    {
+    f32x16 acc[ND];
+    float m, l, slack;              // reference (raw scores); this lane's share of the sum
+    int32_t see_lo, see_hi;         // the keys of the row
+    int32_t hi_min, hi_max, lo_min, lo_max;  // over the wavefront's rows
+    bool idle;                      // no rows
+    uint32_t odd;                   // a tile with masked keys held a value that is not finite
+    uint32_t k_at, v_at[ND];        // where the lane reads its operands in a tile of K and of V
+
+    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t row_base) {
+        const uint32_t lane = threadIdx.x % kWave, c = lane & 31u, h = lane >> 5;
+        const int32_t n_rows = w.q_len * int32_t(a.group);
+        const int32_t row = int32_t(w.row0 + row_base + c);
+        const int32_t row_c = min(row, n_rows - 1);
+        const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
+        const int32_t pos = w.kv_len - w.q_len + tok;
+        see_hi = a.causal ? min(pos + 1, w.hi) : w.hi;
+        see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
+        // positions ascend with the row
+        hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
+        hi_max = __builtin_amdgcn_readlane(see_hi, 31), lo_max = __builtin_amdgcn_readlane(see_lo, 31);
+        idle = int32_t(w.row0 + row_base) >= n_rows;
         const E *qp = static_cast<const E *>(a.q) + int64_t(w.q_start + tok) * a.q_stride[0] +
                       int64_t(kvh * a.group + uint32_t(g)) * a.q_stride[1];
 #pragma unroll
         for (int s = 0; s < NQ; ++s) {
             V8 x = {};
             const uint32_t d = 16u * uint32_t(s) + 8u * h;
-            if (row_in && d < a.dim) x = *reinterpret_cast<const V8 *>(qp + d);
+            if (row < n_rows && d < a.dim) x = *reinterpret_cast<const V8 *>(qp + d);
             qf[s] = x;
         }
-    }
-
-    f32x16 acc[ND];
 #pragma unroll
-    for (int d = 0; d < ND; ++d) acc[d] = f32x16{};
-    float m = -INFINITY, l = 0.0f;  // reference (raw scores); this lane's share of the sum
-    const float slack = fminf(T::kSlack / a.scale_log2, 1e30f);
-
-    uint8_t *group = lds + kw * Sh::kGroupBytes;
-    const uint32_t gtid = rw * 64u + lane;  // thread among those of the key group
-    const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
-    const E *kbase = static_cast<const E *>(a.k) + int64_t(kvh) * a.k_stride[2];
-    const E *vbase = static_cast<const E *>(a.v) + int64_t(kvh) * a.v_stride[2];
-    const int32_t page_mask = (1 << a.page_shift) - 1;
-    const int32_t n_tiles = (hi - lo + KT - 1) / KT;
-    const int32_t n_steps = (n_tiles + KW - 1) / KW;  // the same for every group: they meet at barriers
-    bool missing = false;
-    uint32_t odd = 0;  // a tile with masked keys held a value that is not finite
-
-    // The entry of the block table for key start + lane of a tile (-1 past the
-    // piece), as it was read: it is looked at a step later.
-    auto pages_of = [&](int32_t start) -> int32_t {
-        const int32_t key = start + int32_t(lane % KT);
-        return key < hi ? table[key >> a.page_shift] : -1;
-    };
-    // A load instruction of a wavefront covers kRpi rows, whole ones.  Where a
-    // tile lies wholly inside the piece and such rows inside a page, their
-    // address is one scalar and a constant per lane; other tiles find every
-    // lane's row by itself and leave zeros where there is none.
-    constexpr int kRpi = 64 / CPR;
-    const bool in_dim = lane % CPR * 8u < a.dim;
-    const uint32_t lane_off = uint32_t((int64_t(lane / CPR) * a.k_stride[1] + (in_dim ? lane % CPR * 8u : 0u)) * 2);
-    uint4 kr[NL], vr[NL];
-    auto load = [&](int32_t start, int32_t pages) {
-        const bool none = uint32_t(pages) >= a.n_pages;
-        if (a.simple_rows && start + KT <= hi && !__any(none)) {
-#pragma unroll
-            for (int n = 0; n < NL; ++n) {
-                const uint32_t r0 = (rw + uint32_t(n) * RW) * kRpi;
-                const uint32_t page = __builtin_amdgcn_readlane(pages, r0);
-                const uint32_t in_page = (uint32_t(start) + r0) & uint32_t(page_mask);
-                const uint64_t off = (uint64_t(page) * a.page_units + uint64_t(in_page) * a.slot_units) * 16u;
-                kr[n] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(kbase) + off + lane_off);
-                vr[n] = *reinterpret_cast<const uint4 *>(reinterpret_cast<const uint8_t *>(vbase) + off + lane_off);
-            }
-            if (a.dim != DP) {
-                // lanes past the head have read its first piece
-                const uint32_t keep = in_dim ? ~0u : 0u;
-#pragma unroll
-                for (int n = 0; n < NL; ++n) {
-                    kr[n].x &= keep, kr[n].y &= keep, kr[n].z &= keep, kr[n].w &= keep;
-                    vr[n].x &= keep, vr[n].y &= keep, vr[n].z &= keep, vr[n].w &= keep;
-                }
-            }
-            return;
-        }
-        if (none && start + int32_t(lane % KT) < hi) missing = true;
-#pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const uint32_t i = gtid + uint32_t(n) * GT;
-            const uint32_t r = i / CPR, ch = i % CPR;
-            const int32_t page = __shfl(none ? -1 : pages, int(r));
-            kr[n] = vr[n] = uint4{0, 0, 0, 0};
-            if (page >= 0 && ch * 8u < a.dim) {
-                const int64_t in_page = (start + int32_t(r)) & page_mask;
-                kr[n] = *reinterpret_cast<const uint4 *>(kbase + page * a.k_stride[0] + in_page * a.k_stride[1] + ch * 8u);
-                vr[n] = *reinterpret_cast<const uint4 *>(vbase + page * a.v_stride[0] + in_page * a.v_stride[1] + ch * 8u);
-            }
-        }
-    };
-    auto tile_start = [&](int32_t step) { return lo + (step * KW + int32_t(kw)) * KT; };
-
-    int32_t pages = pages_of(tile_start(0));
-    load(tile_start(0), pages);
-    pages = pages_of(tile_start(1));
-
-    // Where this lane reads its operands in a tile's K and V.  A later piece of
-    // a K row is an exclusive or away, later rows an immediate offset.
-    const uint32_t k_at = k_place<DP>(c, h) * 16u;
-    uint32_t v_at[ND];
-#pragma unroll
-    for (int d = 0; d < ND; ++d) {
+        for (int d = 0; d < ND; ++d) acc[d] = f32x16{};
+        m = -INFINITY;
+        l = 0.0f;
+        slack = fminf(T::kSlack / a.scale_log2, 1e30f);
+        odd = 0;
+        // a later piece of a K row is an exclusive or away, later rows of K
+        // and of V an immediate offset
         const uint32_t i16 = lane % 16u;
-        v_at[d] = Sh::kTileBytes + 8u * (i16 & 1u) +
-                  16u * v_place<DP>(4u * h + i16 / 4u, 4u * uint32_t(d) + 2u * ((lane >> 4) & 1u) + (i16 % 4u) / 2u);
+        k_at = k_place<DP>(c, h) * 16u;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+            v_at[d] = 8u * (i16 & 1u) + 16u * v_place<DP>(4u * h + i16 / 4u, 4u * uint32_t(d) + 2u * ((lane >> 4) & 1u) +
+                                                                                 (i16 % 4u) / 2u);
     }
 
-    for (int32_t step = 0; step < n_steps; ++step) {
-        const int32_t start = tile_start(step);
-        uint8_t *buf = group + (Sh::kBuffers == 2 ? uint32_t(step & 1) : 0u) * 2u * Sh::kTileBytes;
-        uint4 *kl = reinterpret_cast<uint4 *>(buf);
-        uint4 *vl = reinterpret_cast<uint4 *>(buf + Sh::kTileBytes);
-        if constexpr (RW == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    // The queries are there from here on: a wait for them inside the loop would
+    // wait for the tiles under way.
+    __device__ __forceinline__ void settle() const {
 #pragma unroll
-        for (int n = 0; n < NL; ++n) {
-            const uint32_t i = gtid + uint32_t(n) * GT;
-            kl[k_place<DP>(i / CPR, i % CPR)] = kr[n];
-            vl[v_place<DP>(i / CPR, i % CPR)] = vr[n];
-        }
-        // one barrier a step: a buffer is written again two steps later, when
-        // every wavefront has passed the next step's barrier
-        if constexpr (RW == 1)
-            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        else
-            __syncthreads();
-        if (step + 1 < n_steps) {
-            load(tile_start(step + 1), pages);
-            pages = pages_of(tile_start(step + 2));
-        }
-        if (idle || start >= hi_max || start + KT <= lo_min) continue;
+        for (int s = 0; s < NQ; ++s) asm volatile("" ::"v"(qf[s]));
+    }
 
-        // S^T = K Q^T.  Operands are read a group of four ahead of the
-        // products that use them; left to itself the compiler reads each one
-        // just before its product and waits for it.
-        f32x16 s[NB];
+    // No row sees a key of the tile; some row does not see all of them.
+    __device__ __forceinline__ bool skips(int32_t start) const {
+        return idle || start >= hi_max || start + KT <= lo_min;
+    }
+    __device__ __forceinline__ bool masks(int32_t start) const { return start + KT > hi_min || start < lo_max; }
+
+    // `beside`(g) is other work that may go among the products of group g.
+    // O^T += V^T P^T (PV), S^T = K Q^T (QK), in groups of four products whose
+    // operands are read kAhead groups before they are used: four wavefronts
+    // that read at once wait longer for LDS than one group of products takes.
+    // Left to itself the compiler reads each operand just before its product.
+    template <bool PV, bool QK, int kAhead, typename F>
+    __device__ __forceinline__ void products(const uint8_t *vt, const V8 (&p)[NS], const uint8_t *kt, f32x16 (&s)[NB],
+                                             F &&beside) {
+        constexpr int VG = ND < 4 ? ND : 4;                   // products of V in a group
+        constexpr int NV = PV ? NS * ND / VG : 0;
+        constexpr int KG = 4 / NB;                            // 16-column steps of K in a group
+        constexpr int N = NV + (QK ? NQ / KG : 0);
+        V8 f[kAhead + 1][4];
+        auto read = [&](int g) {
+            V8(&to)[4] = f[g % (kAhead + 1)];
+            if (g < NV) {
 #pragma unroll
-        for (int b = 0; b < NB; ++b) s[b] = f32x16{};
-        {
-            constexpr int KG = 4 / NB;       // 16-column steps per group
-            constexpr int NG = NQ / KG;
-            V8 kf[2][KG][NB];
-            auto read = [&](int g) {
+                for (int j = 0; j < VG; ++j) {
+                    using L4 = __attribute__((address_space(3))) s16x4;
+                    struct Two {
+                        s16x4 a, b;
+                    } t;
+                    const uint8_t *at = vt + v_at[(g * VG + j) % ND] + (g * VG + j) / ND * 16 * DP * 2;
+                    t.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)at);
+                    t.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 8 * DP * 2));
+                    to[j] = __builtin_bit_cast(V8, t);
+                }
+            } else {
 #pragma unroll
                 for (int k = 0; k < KG; ++k)
 #pragma unroll
                     for (int b = 0; b < NB; ++b)
-                        kf[g & 1][k][b] = *reinterpret_cast<const V8 *>(
-                            buf + (k_at ^ (uint32_t(g * KG + k) << 5)) + b * 32 * DP * 2);
-            };
-            read(0);
+                        to[k * NB + b] = *reinterpret_cast<const V8 *>(
+                            kt + (k_at ^ (uint32_t((g - NV) * KG + k) << 5)) + b * 32 * DP * 2);
+            }
+        };
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (g + 1 < NG) read(g + 1);
-                __builtin_amdgcn_sched_barrier(0);
+        for (int g = 0; g < kAhead; ++g)
+            if (g < N) read(g);
+#pragma unroll
+        for (int g = 0; g < N; ++g) {
+            if (g + kAhead < N) read(g + kAhead);
+            __builtin_amdgcn_sched_barrier(0);
+            beside(g);
+            const V8(&from)[4] = f[g % (kAhead + 1)];
+            if (g < NV) {
+#pragma unroll
+                for (int j = 0; j < VG; ++j) {
+                    const int d = (g * VG + j) % ND;
+                    acc[d] = T::mfma(from[j], p[(g * VG + j) / ND], acc[d]);
+                }
+            } else {
 #pragma unroll
                 for (int k = 0; k < KG; ++k)
 #pragma unroll
-                    for (int b = 0; b < NB; ++b) s[b] = T::mfma(kf[g & 1][k][b], qf[g * KG + k], s[b]);
-                __builtin_amdgcn_sched_barrier(0);
+                    for (int b = 0; b < NB; ++b) {
+                        const int step = (g - NV) * KG + k;
+                        s[b] = T::mfma(from[k * NB + b], qf[step], step == 0 ? f32x16{} : s[b]);
+                    }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
-        const bool masked = start + KT > hi_min || start < lo_max;
+    }
+
+    // Weights of a tile's scores, rounded; the sums move to a new reference
+    // where a row's maximum has left the slack.
+    __device__ __forceinline__ void weights(const AttnArgs &a, int32_t start, bool masked, f32x16 (&s)[NB], V8 (&p)[NS]) {
         if (masked) {
+            // seen: the keys see_lo .. see_lo + width - 1, in one comparison
+            const uint32_t first = uint32_t(start - see_lo) + 4u * ((threadIdx.x >> 5) & 1u);
+            const uint32_t width = uint32_t(max(see_hi - see_lo, 0));
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int32_t key = start + 32 * b + 8 * (r / 4) + 4 * int32_t(h) + r % 4;
-                    if (key >= see_hi || key < see_lo) s[b][r] = -INFINITY;
-                }
+                for (int r = 0; r < 16; ++r)
+                    if (first + uint32_t(32 * b + 8 * (r / 4) + r % 4) >= width) s[b][r] = -INFINITY;
         }
-        // the running reference
         float top = s[0][0];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
@@ -638,7 +340,6 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             for (int d = 0; d < ND; ++d) acc[d] *= f;
         }
         const float off = T::kBias - (m == -INFINITY ? 0.0f : m * a.scale_log2);
-        V8 p[NS];
 #pragma unroll
         for (int b = 0; b < NB; ++b)
 #pragma unroll
@@ -647,71 +348,134 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
                 l += e;
                 p[2 * b + r / 8][r % 8] = E(e);
             }
+    }
 
-        // O^T += V^T P^T
-        auto v_frag = [&](int st, int d) -> V8 {
-            using L4 = __attribute__((address_space(3))) s16x4;
-            struct Two {
-                s16x4 a, b;
-            } t;
-            const uint8_t *at = buf + v_at[d] + st * 16 * DP * 2;
-            t.a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)at);
-            t.b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((L4 *)(at + 8 * DP * 2));
-            return __builtin_bit_cast(V8, t);
-        };
-        if (masked) {
-            // a masked key adds nothing, whatever its value holds, but 0 x inf
-            // in the product below is not nothing: note it, and see the end
-            constexpr uint32_t kE = T::kExp * 0x10001u, kO = T::kOne * 0x10001u;
-            uint32_t bits = 0;
+    // A masked key adds nothing, whatever its value holds, but 0 x inf in the
+    // product is not nothing: note it, and see store().
+    __device__ __forceinline__ void check(const uint8_t *vt) {
+        constexpr uint32_t kE = T::kExp * 0x10001u, kO = T::kOne * 0x10001u;
+        uint32_t bits = 0;
 #pragma unroll 2
-            for (uint32_t i = lane; i < uint32_t(KT * CPR); i += 64u) {
-                const uint4 x = vl[i];
-                bits |= ((x.x & kE) + kO) | ((x.y & kE) + kO) | ((x.z & kE) + kO) | ((x.w & kE) + kO);
-            }
-            odd |= bits & 0x80008000u;
+        for (uint32_t i = threadIdx.x % kWave; i < uint32_t(KT * DP / 8); i += 64u) {
+            const uint4 x = reinterpret_cast<const uint4 *>(vt)[i];
+            bits |= ((x.x & kE) + kO) | ((x.y & kE) + kO) | ((x.z & kE) + kO) | ((x.w & kE) + kO);
         }
-        {
-            // groups of up to four operands, as above
-            constexpr int VG = ND < 4 ? ND : 4;
-            constexpr int NG = NS * ND / VG;
-            V8 vf[2][VG];
-            auto read = [&](int g) {
+        odd |= bits & 0x80008000u;
+    }
+};
+
+// Tiles of K and V on their way from the cache to LDS through the registers of
+// NT threads, thread gtid of them: NL pieces of 16 bytes of each.
+template <typename E, int DP, int KT, int NT, bool Same>
+struct Loader {
+    static constexpr int CPR = DP / 8;             // pieces per row
+    static constexpr int NL = KT * CPR / NT;       // pieces per thread
+    static constexpr int kStep = NT / CPR;         // rows from one piece of a thread to its next
+
+    const uint8_t *kbase, *vbase;                  // of the cache head
+    const int32_t *table;
+    int32_t hi;
+    uint32_t gtid, row, chunk;                     // of the thread's first piece
+    uint32_t n_pages, page_shift, page_most;       // page_most: the largest page seen
+    uint32_t k_page, k_slot, v_page, v_slot;       // strides in pieces
+    bool whole_dim, same;
+    int32_t pages[NL];
+    uint4 kr[NL], vr[NL];
+
+    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t rw) {
+        gtid = rw * 64u + threadIdx.x % kWave;
+        row = gtid / CPR;
+        chunk = gtid % CPR * 8u < a.dim ? gtid % CPR : 0u;
+        table = a.table + int64_t(w.req) * a.table_stride;
+        whole_dim = a.dim == DP;
+        kbase = static_cast<const uint8_t *>(a.k) + uint64_t(kvh) * a.k_units[2] * 16u;
+        vbase = static_cast<const uint8_t *>(a.v) + uint64_t(kvh) * a.v_units[2] * 16u;
+        k_page = a.k_units[0], k_slot = a.k_units[1], v_page = a.v_units[0], v_slot = a.v_units[1];
+        same = k_page == v_page && k_slot == v_slot;
+        hi = w.hi;
+        n_pages = a.n_pages;
+        page_shift = a.page_shift;
+        page_most = 0;
+    }
+
+    // The block table's entries for the thread's rows of the tile at `start`
+    // (the piece's last row stands for those past it): read a tile ahead of
+    // the load that uses them.
+    __device__ __forceinline__ void fetch_pages(int32_t start) {
 #pragma unroll
-                for (int j = 0; j < VG; ++j) vf[g & 1][j] = v_frag((g * VG + j) / ND, (g * VG + j) % ND);
-            };
-            read(0);
+        for (int n = 0; n < NL; ++n) pages[n] = table[min(start + int32_t(row) + n * kStep, hi - 1) >> page_shift];
+    }
+
+    // A page that is none of the cache's is noted and the last one read in
+    // its place; rows past the piece are read, from a page of the request, and
+    // left out by put().
+    __device__ __forceinline__ void load(int32_t start) {
+        const uint32_t page_mask = (1u << page_shift) - 1u;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                if (g + 1 < NG) read(g + 1);
-                __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-                for (int j = 0; j < VG; ++j) {
-                    const int d = (g * VG + j) % ND;
-                    acc[d] = T::mfma(vf[g & 1][j], p[(g * VG + j) / ND], acc[d]);
-                }
-                __builtin_amdgcn_sched_barrier(0);
-            }
+        for (int n = 0; n < NL; ++n) {
+            const uint32_t in_page = (uint32_t(start) + row + uint32_t(n * kStep)) & page_mask;
+            page_most = max(page_most, uint32_t(pages[n]));
+            const uint32_t page = min(uint32_t(pages[n]), n_pages - 1u);
+            const uint64_t at = uint64_t(page) * k_page + (uint64_t(in_page) * k_slot + chunk);
+            kr[n] = *reinterpret_cast<const uint4 *>(kbase + at * 16u);
+            if (Same || same)
+                vr[n] = *reinterpret_cast<const uint4 *>(vbase + at * 16u);
+            else
+                vr[n] = *reinterpret_cast<const uint4 *>(
+                    vbase + (uint64_t(page) * v_page + (uint64_t(in_page) * v_slot + chunk)) * 16u);
         }
     }
-    if (missing && a.status) atomicOr(a.status, kStatusCorrupt);
+    __device__ __forceinline__ bool missing() const { return page_most >= n_pages; }
 
-    // Join the key groups and write.  A wavefront's rows go to LDS; the
-    // wavefronts of a row group then each take a share of its rows, so that
-    // stores run along the rows.
-    l += other_half(l);
-    float *ml = reinterpret_cast<float *>(lds + Sh::kMl) + 64u * wave;
+    // Into LDS; rows past the piece and columns past the head become zeros.
+    __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, int32_t start) {
+        if (!whole_dim || start + KT > hi) {
+            const bool in_dim = whole_dim || gtid % CPR == chunk;
+#pragma unroll
+            for (int n = 0; n < NL; ++n) {
+                const uint32_t keep = in_dim && start + int32_t(row) + n * kStep < hi ? ~0u : 0u;
+                kr[n].x &= keep, kr[n].y &= keep, kr[n].z &= keep, kr[n].w &= keep;
+                vr[n].x &= keep, vr[n].y &= keep, vr[n].z &= keep, vr[n].w &= keep;
+            }
+        }
+#pragma unroll
+        for (int n = 0; n < NL; ++n) {
+            const uint32_t i = gtid + uint32_t(n) * NT;
+            reinterpret_cast<uint4 *>(kt)[k_place<DP>(i / CPR, i % CPR)] = kr[n];
+            reinterpret_cast<uint4 *>(vt)[v_place<DP>(i / CPR, i % CPR)] = vr[n];
+        }
+    }
+};
+
+// The end of a workgroup of RW x KW wavefronts (along the rows, along the
+// keys): every wavefront's rows go to LDS, and the wavefronts of a row group
+// each write a share of its rows, joined over the key groups, so that stores
+// run along the rows.  All of LDS but the maxima and sums at `ml_at` is free.
+template <int DP>
+constexpr uint32_t out_bytes() { return 32u * DP * 4u; }
+
+template <typename E, int DP, int KT, int RW, int KW>
+__device__ __forceinline__ void store(const AttnArgs &a, const Piece &w, uint32_t kvh, uint8_t *lds, uint32_t ml_at,
+                                      Rows<E, DP, KT> &x, uint32_t wave) {
+    using T = Type<E>;
+    using V8 = typename T::V8;
+    constexpr int CPR = DP / 8, ND = DP / 32;
+    const uint32_t lane = threadIdx.x % kWave, c = lane & 31u, h = lane >> 5;
+    const uint32_t rw = wave % RW, kw = wave / RW;
+    const int32_t n_rows = w.q_len * int32_t(a.group);
+    const float l = x.l + other_half(x.l);
+    float *ml = reinterpret_cast<float *>(lds + ml_at) + 64u * wave;
     auto place = [&](uint32_t r, uint32_t q4) { return r * (DP / 4) + (q4 ^ (r & 7u)); };
-    float4 *own = reinterpret_cast<float4 *>(lds + wave * Sh::kOutBytes);
+    float4 *own = reinterpret_cast<float4 *>(lds + wave * out_bytes<DP>());
     __syncthreads();
-    if (!__any(odd != 0)) {
-        if (h == 0) *reinterpret_cast<float2 *>(ml + 2u * c) = float2{m, l};
+    if (!__any(x.odd != 0)) {
+        if (h == 0) *reinterpret_cast<float2 *>(ml + 2u * c) = float2{x.m, l};
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
             for (int q4 = 0; q4 < 4; ++q4)
-                own[place(c, 8u * uint32_t(d) + 2u * uint32_t(q4) + h)] =
-                    float4{acc[d][4 * q4], acc[d][4 * q4 + 1], acc[d][4 * q4 + 2], acc[d][4 * q4 + 3]};
+                own[place(c, 8u * uint32_t(d) + 2u * uint32_t(q4) + h)] = float4{
+                    x.acc[d][4 * q4], x.acc[d][4 * q4 + 1], x.acc[d][4 * q4 + 2], x.acc[d][4 * q4 + 3]};
     } else {
         rows_one_by_one<E, DP>(a, w, kvh, 32u * rw, kw * KT, uint32_t(KW * KT), KT, reinterpret_cast<float *>(own), ml);
     }
@@ -719,18 +483,9 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     auto weight = [&](float mk, float top) {
         return mk == top ? 1.0f : __builtin_amdgcn_exp2f((mk - top) * a.scale_log2);
     };
-    ml = reinterpret_cast<float *>(lds + Sh::kMl);
+    ml = reinterpret_cast<float *>(lds + ml_at);
     const bool whole = w.splits == 1;
     const uint64_t slot = (uint64_t(w.slot + w.split) * a.kv_heads + kvh) * a.rows_per_tile;
-    if (a.tiles && kvh == 0 && w.split == 0 && threadIdx.x == 0) {
-        Tile t;
-        t.splits = w.splits;
-        t.slot = w.slot;
-        t.token0 = w.q_start;
-        t.row0 = w.row0;
-        t.rows = uint32_t(min(int32_t(a.rows_per_tile), n_rows - int32_t(w.row0)));
-        a.tiles[w.tile] = t;
-    }
 #pragma unroll 2
     for (uint32_t i = lane; i < 32u / KW * CPR; i += 64u) {
         const uint32_t r = kw * (32u / KW) + i / CPR, ch = i % CPR;
@@ -739,17 +494,17 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         float top = -INFINITY, sum = 0.0f;
 #pragma unroll
         for (int k = 0; k < KW; ++k) top = fmaxf(top, ml[2u * (32u * (uint32_t(k) * RW + rw) + r)]);
-        float x[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        float o[8] = {0, 0, 0, 0, 0, 0, 0, 0};
 #pragma unroll
         for (int k = 0; k < KW; ++k) {
             const uint32_t src = uint32_t(k) * RW + rw;
             const float2 v = *reinterpret_cast<const float2 *>(ml + 2u * (32u * src + r));
             const float f = KW == 1 ? 1.0f : weight(v.x, top);
             sum += v.y * f;
-            const float4 *o = reinterpret_cast<const float4 *>(lds + src * Sh::kOutBytes);
-            const float4 x0 = o[place(r, 2u * ch)], x1 = o[place(r, 2u * ch + 1u)];
-            x[0] += x0.x * f, x[1] += x0.y * f, x[2] += x0.z * f, x[3] += x0.w * f;
-            x[4] += x1.x * f, x[5] += x1.y * f, x[6] += x1.z * f, x[7] += x1.w * f;
+            const float4 *from = reinterpret_cast<const float4 *>(lds + src * out_bytes<DP>());
+            const float4 x0 = from[place(r, 2u * ch)], x1 = from[place(r, 2u * ch + 1u)];
+            o[0] += x0.x * f, o[1] += x0.y * f, o[2] += x0.z * f, o[3] += x0.w * f;
+            o[4] += x1.x * f, o[5] += x1.y * f, o[6] += x1.z * f, o[7] += x1.w * f;
         }
         if (whole) {
             const int32_t t = at / int32_t(a.group), hg = at - t * int32_t(a.group);
@@ -758,7 +513,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // a row that sees no key gives 0
             V8 y;
 #pragma unroll
-            for (int j = 0; j < 8; ++j) y[j] = E(x[j] * inv);
+            for (int j = 0; j < 8; ++j) y[j] = E(o[j] * inv);
             *reinterpret_cast<V8 *>(static_cast<E *>(a.out) + token * a.out_stride[0] + int64_t(head) * a.out_stride[1] +
                                     ch * 8u) = y;
             if (a.lse && ch == 0)
@@ -766,18 +521,212 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
                     sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
         } else {
             const uint64_t pr = slot + (uint32_t(at) - w.row0);
-            float4 *o = reinterpret_cast<float4 *>(a.part_o + pr * DP + ch * 8u);
-            o[0] = float4{x[0], x[1], x[2], x[3]};
-            o[1] = float4{x[4], x[5], x[6], x[7]};
+            float4 *to = reinterpret_cast<float4 *>(a.part_o + pr * DP + ch * 8u);
+            to[0] = float4{o[0], o[1], o[2], o[3]};
+            to[1] = float4{o[4], o[5], o[6], o[7]};
             if (ch == 0) *reinterpret_cast<float2 *>(a.part_ml + 2u * pr) = float2{top, sum};
         }
     }
 }
 
+// RW wavefronts along the rows and 4 / RW groups along the keys, tiles of KT
+// keys dealt out to the groups in turn.
+template <int DP, int RW, int KT>
+struct Shape {
+    static constexpr int KW = kWaves / RW;
+    static constexpr int kBuffers = RW == 1 ? 1 : 2;             // a wavefront alone needs no second one
+    static constexpr uint32_t kTileBytes = KT * DP * 2;          // of K or of V
+    static constexpr uint32_t kGroupBytes = 2 * kTileBytes * kBuffers;
+    static constexpr uint32_t kLoop = KW * kGroupBytes;
+    static constexpr uint32_t kEnd = kWaves * out_bytes<DP>();
+    static constexpr uint32_t kMl = kLoop > kEnd ? kLoop : kEnd;
+    static constexpr uint32_t kLds = kMl + kWaves * 32 * 8;
+};
+
+template <typename E, int DP, int RW, int KT>
+__global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a) {
+    using Sh = Shape<DP, RW, KT>;
+    using R = Rows<E, DP, KT>;
+    constexpr int KW = Sh::KW;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
+    Piece w;
+    if (!find_piece<kThreads>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t rw = wave % RW, kw = wave / RW;
+    Loader<E, DP, KT, 64 * RW, false> ld;
+    ld.init(a, w, kvh, rw);
+    const int32_t n_tiles = (w.hi - w.lo + KT - 1) / KT;
+    const int32_t n_steps = (n_tiles + KW - 1) / KW;  // the same for every group: they meet at barriers
+    auto tile_start = [&](int32_t step) { return w.lo + (step * KW + int32_t(kw)) * KT; };
+    R x;
+    if (n_steps) ld.fetch_pages(tile_start(0));
+    x.init(a, w, kvh, 32u * rw);
+    if (tile_start(0) < w.hi) {
+        ld.load(tile_start(0));
+        ld.fetch_pages(tile_start(1));
+    }
+    x.settle();
+
+    for (int32_t step = 0; step < n_steps; ++step) {
+        const int32_t start = tile_start(step);
+        uint8_t *kt = lds + kw * Sh::kGroupBytes + (Sh::kBuffers == 2 ? uint32_t(step & 1) : 0u) * 2u * Sh::kTileBytes;
+        uint8_t *vt = kt + Sh::kTileBytes;
+        if constexpr (RW == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        ld.put(kt, vt, start);
+        // one barrier a step: a buffer is written again two steps later, when
+        // every wavefront has passed the next step's barrier
+        if constexpr (RW == 1)
+            __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        else
+            __syncthreads();
+        if (tile_start(step + 1) < w.hi) {
+            ld.load(tile_start(step + 1));
+            ld.fetch_pages(tile_start(step + 2));
+        }
+        if (x.skips(start)) continue;
+        f32x16 s[R::NB];
+        typename R::V8 p[R::NS];
+        x.template products<false, true, 1>(vt, p, kt, s, nothing);
+        const bool masked = x.masks(start);
+        x.weights(a, start, masked, s, p);
+        if (masked) x.check(vt);
+        x.template products<true, false, 1>(vt, p, kt, s, nothing);
+    }
+    const AttnArgs &b = again(a);
+    if (ld.missing() && b.status) atomicOr(b.status, kStatusCorrupt);
+    store<E, DP, KT, RW, KW>(b, w, kvh, lds, Sh::kMl, x, wave);
+}
+
+// Eight wavefronts of 32 rows each, for steps with tiles of 256 rows for
+// every compute unit.  Two wavefronts share a SIMD.  Left alone they fall into
+// step, both at their products and then both at their exponentials, and the
+// matrix unit idles half the time; here the second half of the workgroup runs
+// one phase behind the first, held there by a barrier after every phase: while
+// one half multiplies (V of the tile before, K of this one), the other takes
+// its exponentials and moves the next tiles.
+//
+//   phase    2i              2i + 1          2i + 2
+//   half 0   products i      weights i       products i + 1
+//   half 1   weights i - 1   products i      weights i
+//
+// A half's loads of a tile leave the cache during its products and go to LDS
+// as its weights begin.
+//
+// Products i read K tile i and V tile i - 1 in phases 2i and 2i + 1, so both
+// halves put tile i + 1 into LDS by the end of phase 2i + 1: K into the place
+// of K tile i - 1 and V, of three places, into that of V tile i - 2, which
+// were last read in phase 2i - 1.
+template <int DP>
+struct Shape8 {
+    static constexpr int KT = 64;
+    static constexpr uint32_t kWaves8 = 8;
+    static constexpr uint32_t kTileBytes = KT * DP * 2;
+    static constexpr uint32_t kLoop = 5 * kTileBytes;            // two of K, three of V
+    static constexpr uint32_t kEnd = kWaves8 * out_bytes<DP>();
+    static constexpr uint32_t kMl = kLoop > kEnd ? kLoop : kEnd;
+    static constexpr uint32_t kLds = kMl + kWaves8 * 32 * 8;
+};
+
+template <typename E, int DP>
+__global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
+    using Sh = Shape8<DP>;
+    constexpr int KT = Sh::KT;
+    using R = Rows<E, DP, KT>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
+    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
+    Piece w;
+    if (!find_piece<512>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const bool second = wave >= 4u;
+    Loader<E, DP, KT, 512, true> ld;  // (the launcher sees to it)
+    ld.init(a, w, kvh, wave);
+    const int32_t n = (w.hi - w.lo + KT - 1) / KT;
+    auto tile_start = [&](int32_t t) { return w.lo + t * KT; };
+    auto k_tile = [&](int32_t t) { return lds + uint32_t(t & 1) * Sh::kTileBytes; };
+    R x;
+    if (n) ld.fetch_pages(tile_start(0));
+    x.init(a, w, kvh, 32u * wave);
+    // half 0 moves tile t + 1 in its turn t, half 1 tile t + 2
+    const int32_t lead = second ? 2 : 1;
+    auto v_tile = [&](int32_t t) { return lds + uint32_t(2 + t % 3) * Sh::kTileBytes; };
+    auto put = [&](int32_t t) {
+        if (t < n) ld.put(k_tile(t), v_tile(t), tile_start(t));
+    };
+    // (past the end, the last tile again: nothing waits for it)
+    auto load = [&](int32_t t) { ld.load(tile_start(min(t, n - 1))); };
+    auto fetch = [&](int32_t t) { ld.fetch_pages(tile_start(min(t, n - 1))); };
+    if (n) {
+        load(0);
+        fetch(1);
+        put(0);
+        if (second) {
+            load(1);
+            fetch(2);
+        }
+    }
+    x.settle();
+    __syncthreads();
+    if (second) {
+        put(1);
+        __syncthreads();
+    }
+    // the wavefront's own tiles: t0 .. t1 - 1
+    int32_t t = 0, t0 = 0, t1 = 0;
+    if (!x.idle) {
+        t0 = min(max((x.lo_min - w.lo) / KT, 0), n);
+        t1 = min(max((x.hi_max - w.lo + KT - 1) / KT, t0), n);
+    }
+    auto turn_without_rows = [&]() {
+        load(t + lead);
+        fetch(t + lead + 1);
+        __syncthreads();
+        put(t + lead);
+        __syncthreads();
+        ++t;
+    };
+    while (t < t0) turn_without_rows();
+    if (t0 < t1) {
+        f32x16 s[R::NB];
+        typename R::V8 p[R::NS];
+        load(t + lead);
+        fetch(t + lead + 1);
+        x.template products<false, true, 1>(lds, p, k_tile(t), s, nothing);
+        __syncthreads();
+        put(t + lead);
+        bool masked = x.masks(tile_start(t));
+        x.weights(a, tile_start(t), masked, s, p);
+        __syncthreads();
+        for (++t; t < t1; ++t) {
+            uint8_t *vt = v_tile(t - 1);
+            if (masked) x.check(vt);
+            x.template products<true, true, 2>(vt, p, k_tile(t), s, [&](int g) {
+                if (g == 1) load(t + lead);
+                if (g == 3) fetch(t + lead + 1);
+            });
+            __syncthreads();
+            put(t + lead);
+            masked = x.masks(tile_start(t));
+            x.weights(a, tile_start(t), masked, s, p);
+            __syncthreads();
+        }
+        uint8_t *vt = v_tile(t - 1);
+        if (masked) x.check(vt);
+        x.template products<true, false, 1>(vt, p, lds, s, nothing);
+        if (t < n) turn_without_rows();
+    }
+    while (t < n) turn_without_rows();
+    if (!second) __syncthreads();
+    const AttnArgs &b = again(a);
+    if (ld.missing() && b.status) atomicOr(b.status, kStatusCorrupt);
+    store<E, DP, KT, 8, 1>(b, w, kvh, lds, Sh::kMl, x, wave);
+}
+
 // The pieces of a split tile joined.  A wavefront takes a row (WPR = 1, for
 // tiles of many rows and few pieces) or a quarter of its pieces (WPR = 4);
 // lanes run along the row in 16-byte steps and, where the row is shorter,
-// over several pieces.  Each lane keeps its own running maximum.
+// over several pieces.  Each lane keeps its own running maximum.  A step in
+// which nothing is split costs the launch alone.
 template <typename E, int DP, int WPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     using T = Type<E>;
@@ -786,60 +735,64 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     constexpr uint32_t kRows = kWaves / WPR;             // rows at a time
     __shared__ float4 part_x[WPR == 4 ? 4 : 1][CPR];
     __shared__ float2 part_ml[4];
-    const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
-    if (index >= *a.tile_count) return;
-    const Tile w = a.tiles[index];
-    const uint32_t splits = __builtin_amdgcn_readfirstlane(w.splits), slot = __builtin_amdgcn_readfirstlane(w.slot);
-    const uint32_t row0 = __builtin_amdgcn_readfirstlane(w.row0), rows = __builtin_amdgcn_readfirstlane(w.rows);
-    const int32_t token0 = __builtin_amdgcn_readfirstlane(w.token0);
-    if (splits == 1u) return;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const uint32_t ch = lane % CPR, sl = lane / CPR;
     auto weight = [&](float m, float top) { return m == top ? 1.0f : __builtin_amdgcn_exp2f((m - top) * a.scale_log2); };
-    for (uint32_t r = blockIdx.y * kRows + (WPR == 4 ? 0u : wave); r < rows; r += gridDim.y * kRows) {
-        float top = -INFINITY, sum = 0.0f;
-        float4 x{0, 0, 0, 0};
-        auto add = [&](float m, float l, const float4 &o) {
-            const float t2 = fmaxf(top, m), f = weight(top, t2), g = weight(m, t2);
-            top = t2;
-            sum = sum * f + l * g;
-            x.x = x.x * f + o.x * g, x.y = x.y * f + o.y * g, x.z = x.z * f + o.z * g, x.w = x.w * f + o.w * g;
-        };
+    // units: a share of the rows of one cache head of one tile
+    const uint32_t units = *a.tile_count * a.kv_heads * a.join_shares;
+    for (uint32_t unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        const uint32_t kvh = unit % a.kv_heads, rest = unit / a.kv_heads;
+        const uint32_t share = rest % a.join_shares;
+        const Tile w = a.tiles[rest / a.join_shares];
+        const uint32_t splits = __builtin_amdgcn_readfirstlane(w.splits), slot = __builtin_amdgcn_readfirstlane(w.slot);
+        const uint32_t row0 = __builtin_amdgcn_readfirstlane(w.row0), rows = __builtin_amdgcn_readfirstlane(w.rows);
+        const int32_t token0 = __builtin_amdgcn_readfirstlane(w.token0);
+        if (splits == 1u) continue;  // a shorter tile than its request's longest
+        for (uint32_t r = share * kRows + (WPR == 4 ? 0u : wave); r < rows; r += a.join_shares * kRows) {
+            float top = -INFINITY, sum = 0.0f;
+            float4 x{0, 0, 0, 0};
+            auto add = [&](float m, float l, const float4 &o) {
+                const float t2 = fmaxf(top, m), f = weight(top, t2), g = weight(m, t2);
+                top = t2;
+                sum = sum * f + l * g;
+                x.x = x.x * f + o.x * g, x.y = x.y * f + o.y * g, x.z = x.z * f + o.z * g, x.w = x.w * f + o.w * g;
+            };
 #pragma unroll 4
-        for (uint32_t s = (WPR == 4 ? wave * SL : 0u) + sl; s < splits; s += SL * WPR) {
-            const uint64_t pr = (uint64_t(slot + s) * a.kv_heads + kvh) * a.rows_per_tile + r;
-            const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2u * pr);
-            add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part_o + pr * DP + 4u * ch));
-        }
-#pragma unroll
-        for (uint32_t d = CPR; d < 64u; d *= 2) {
-            const float m = __shfl_xor(top, int(d)), l = __shfl_xor(sum, int(d));
-            add(m, l, float4{__shfl_xor(x.x, int(d)), __shfl_xor(x.y, int(d)), __shfl_xor(x.z, int(d)),
-                             __shfl_xor(x.w, int(d))});
-        }
-        if constexpr (WPR == 4) {
-            __syncthreads();  // the row before has been read
-            if (sl == 0) part_x[wave][ch] = x;
-            if (lane == 0) part_ml[wave] = float2{top, sum};
-            __syncthreads();
-            if (wave == 0 && sl == 0) {
-#pragma unroll
-                for (int k = 1; k < 4; ++k) add(part_ml[k].x, part_ml[k].y, part_x[k][ch]);
+            for (uint32_t s = (WPR == 4 ? wave * SL : 0u) + sl; s < splits; s += SL * WPR) {
+                const uint64_t pr = (uint64_t(slot + s) * a.kv_heads + kvh) * a.rows_per_tile + r;
+                const float2 v = *reinterpret_cast<const float2 *>(a.part_ml + 2u * pr);
+                add(v.x, v.y, *reinterpret_cast<const float4 *>(a.part_o + pr * DP + 4u * ch));
             }
-            if (wave != 0) continue;
+#pragma unroll
+            for (uint32_t d = CPR; d < 64u; d *= 2) {
+                const float m = __shfl_xor(top, int(d)), l = __shfl_xor(sum, int(d));
+                add(m, l, float4{__shfl_xor(x.x, int(d)), __shfl_xor(x.y, int(d)), __shfl_xor(x.z, int(d)),
+                                 __shfl_xor(x.w, int(d))});
+            }
+            if constexpr (WPR == 4) {
+                __syncthreads();  // the row before has been read
+                if (sl == 0) part_x[wave][ch] = x;
+                if (lane == 0) part_ml[wave] = float2{top, sum};
+                __syncthreads();
+                if (wave == 0 && sl == 0) {
+#pragma unroll
+                    for (int k = 1; k < 4; ++k) add(part_ml[k].x, part_ml[k].y, part_x[k][ch]);
+                }
+                if (wave != 0) continue;
+            }
+            if (sl != 0 || ch * 4u >= a.dim) continue;
+            const uint32_t gr = row0 + r;
+            const uint32_t t = gr / a.group, head = kvh * a.group + gr % a.group;
+            const int64_t token = int64_t(token0) + t;
+            const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+            using E4 = __attribute__((ext_vector_type(4))) E;
+            const E4 y = {E(x.x * inv), E(x.y * inv), E(x.z * inv), E(x.w * inv)};
+            *reinterpret_cast<E4 *>(static_cast<E *>(a.out) + token * a.out_stride[0] + int64_t(head) * a.out_stride[1] +
+                                    4u * ch) = y;
+            if (a.lse && ch == 0)
+                a.lse[token * a.heads + head] =
+                    sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
         }
-        if (sl != 0 || ch * 4u >= a.dim) continue;
-        const uint32_t gr = row0 + r;
-        const uint32_t t = gr / a.group, head = kvh * a.group + gr % a.group;
-        const int64_t token = int64_t(token0) + t;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        using E4 = __attribute__((ext_vector_type(4))) E;
-        const E4 y = {E(x.x * inv), E(x.y * inv), E(x.z * inv), E(x.w * inv)};
-        *reinterpret_cast<E4 *>(static_cast<E *>(a.out) + token * a.out_stride[0] + int64_t(head) * a.out_stride[1] +
-                                4u * ch) = y;
-        if (a.lse && ch == 0)
-            a.lse[token * a.heads + head] =
-                sum == 0.0f ? -INFINITY : top * a.scale + (__builtin_amdgcn_logf(sum) - T::kBias) * 0.69314718f;
     }
 }
 
@@ -862,12 +815,15 @@ LaunchPlan launch_plan(const dfc_attention_args &a) {
     // one wavefront holds a whole key tile of K and V on its way to LDS: too
     // many registers at 256 columns
     p.rw = most <= 32 && p.dp <= 128 ? 1 : most <= 64 ? 2 : 4;
-    p.kt = p.rw == 4 && p.dp <= 128 ? 64 : 32;
+    bool same = true;  // K and V have one layout
+    for (int i = 0; i < 2; ++i) same = same && a.cache.k_stride[i] == a.cache.v_stride[i];
+    if (p.rw == 4 && p.dp <= 128 && same && a.tokens * group / 256u * a.cache.kv_heads >= 256u) p.rw = 8;
+    p.kt = p.rw >= 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
-    p.resident = p.dp > 128 ? 256u : 512u;
-    p.min_piece = p.rw == 4 ? 2u : kWaves / uint32_t(p.rw);
-    p.piece_cost = p.rw == 4 ? 1.0f : 4.0f;
-    p.join_cost = p.rw == 4 ? 2.0f : 8.0f;
+    p.resident = p.dp > 128 || p.rw == 8 ? 256u : 512u;
+    p.min_piece = p.rw >= 4 ? 2u : kWaves / uint32_t(p.rw);
+    p.piece_cost = p.rw >= 4 ? 1.0f : 4.0f;
+    p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
     const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
                                               uint64_t(a.tokens) * group);
     // a tile of c key tiles has at most ceil(c / min_piece) pieces; there are
@@ -881,7 +837,7 @@ LaunchPlan launch_plan(const dfc_attention_args &a) {
     p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, tiles + extra));
     p.most_rows = uint32_t(std::min<uint64_t>(most, p.rows_per_tile));
     p.off_tiles = 256;
-    p.off_ml = p.off_tiles + uint64_t(p.tile_cap) * sizeof(Tile);
+    p.off_ml = (p.off_tiles + uint64_t(p.extra) * sizeof(Tile) + 255u) & ~uint64_t(255);
     const uint64_t rows = uint64_t(p.slot_cap) * a.cache.kv_heads * p.rows_per_tile;
     p.off_o = (p.off_ml + rows * 8u + 255u) & ~uint64_t(255);
     p.bytes = p.off_o + rows * uint64_t(p.dp) * 4u;
@@ -896,6 +852,8 @@ dfc_status check_attention(const dfc_attention_args &a) {
     // rows (tokens x heads of a group), and the tiles of 64 requests, are
     // counted in 32 bits
     if (a.tokens * (a.heads / a.cache.kv_heads) > 0x3fffffffull) return DFC_EUNSUPPORTED;
+    for (int i = 0; i < 3; ++i)
+        if (a.cache.k_stride[i] >> 34 || a.cache.v_stride[i] >> 34) return DFC_EUNSUPPORTED;
     if (!(a.scale > 0.0f) || !std::isfinite(a.scale)) return DFC_EINVAL;
     if (a.window > 0x7fffffffu) return DFC_EINVAL;
     return DFC_OK;
@@ -903,31 +861,39 @@ dfc_status check_attention(const dfc_attention_args &a) {
 
 template <typename E, int DP, int RW, int KT>
 dfc_status launch(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
-    using Sh = Shape<E, DP, RW, KT>;
-    const void *fn = reinterpret_cast<const void *>(&attention_kernel<E, DP, RW, KT>);
-    if (!allow_full_lds(fn)) return DFC_EHIP;
+    constexpr uint32_t kLds = RW == 8 ? Shape8<DP>::kLds : Shape<DP, RW == 8 ? 4 : RW, KT>::kLds;
+    void (*kernel)(AttnArgs);
+    if constexpr (RW == 8)
+        kernel = &attention8_kernel<E, DP>;
+    else
+        kernel = &attention_kernel<E, DP, RW, KT>;
+    if (!allow_full_lds(reinterpret_cast<const void *>(kernel))) return DFC_EHIP;
     const uint64_t grid = (uint64_t(p.tile_cap) + p.extra) * a.kv_heads;
     if (grid > 0x7fffffffull) return DFC_EUNSUPPORTED;
-    hipLaunchKernelGGL((attention_kernel<E, DP, RW, KT>), dim3(uint32_t(grid)), dim3(kThreads), Sh::kLds, st, a);
+    hipLaunchKernelGGL(kernel, dim3(uint32_t(grid)), dim3(RW == 8 ? 512 : kThreads), kLds, st, a);
     if (a.tiles) {
-        constexpr int WPR = RW == 4 ? 1 : 4;
-        hipLaunchKernelGGL((join_kernel<E, DP, WPR>),
-                           dim3(p.tile_cap * a.kv_heads, WPR == 4 ? p.most_rows : (p.most_rows + 7u) / 8u),
-                           dim3(kThreads), 0, st, a);
+        constexpr int WPR = RW >= 4 ? 1 : 4;
+        // as many workgroups as may have work, up to a few per compute unit
+        const uint64_t units = uint64_t(p.extra) * a.kv_heads * a.join_shares;
+        if (units > 0xffffffffull) return DFC_EUNSUPPORTED;
+        hipLaunchKernelGGL((join_kernel<E, DP, WPR>), dim3(uint32_t(std::min<uint64_t>(units, 2048u))), dim3(kThreads), 0,
+                           st, a);
     }
     return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
 }
 
 template <typename E>
 dfc_status launch_type(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
-    switch (p.dp * 8 + p.rw) {
-        case 64 * 8 + 1: return launch<E, 64, 1, 32>(a, p, st);
-        case 64 * 8 + 2: return launch<E, 64, 2, 32>(a, p, st);
-        case 64 * 8 + 4: return launch<E, 64, 4, 64>(a, p, st);
-        case 128 * 8 + 1: return launch<E, 128, 1, 32>(a, p, st);
-        case 128 * 8 + 2: return launch<E, 128, 2, 32>(a, p, st);
-        case 128 * 8 + 4: return launch<E, 128, 4, 64>(a, p, st);
-        case 256 * 8 + 2: return launch<E, 256, 2, 32>(a, p, st);
+    switch (p.dp * 16 + p.rw) {
+        case 64 * 16 + 1: return launch<E, 64, 1, 32>(a, p, st);
+        case 64 * 16 + 2: return launch<E, 64, 2, 32>(a, p, st);
+        case 64 * 16 + 4: return launch<E, 64, 4, 64>(a, p, st);
+        case 64 * 16 + 8: return launch<E, 64, 8, 64>(a, p, st);
+        case 128 * 16 + 1: return launch<E, 128, 1, 32>(a, p, st);
+        case 128 * 16 + 2: return launch<E, 128, 2, 32>(a, p, st);
+        case 128 * 16 + 4: return launch<E, 128, 4, 64>(a, p, st);
+        case 128 * 16 + 8: return launch<E, 128, 8, 64>(a, p, st);
+        case 256 * 16 + 2: return launch<E, 256, 2, 32>(a, p, st);
         default: return launch<E, 256, 4, 32>(a, p, st);
     }
 }
@@ -974,16 +940,13 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
         a.out_stride[i] = in.out_stride[i];
     }
     for (int i = 0; i < 3; ++i) {
-        a.k_stride[i] = in.cache.k_stride[i];
-        a.v_stride[i] = in.cache.v_stride[i];
+        a.k_units[i] = uint32_t(in.cache.k_stride[i] / 8);
+        a.v_units[i] = uint32_t(in.cache.v_stride[i] / 8);
     }
-    bool simple = in.cache.page_size >= 512u / uint32_t(p.dp);
-    for (int i = 0; i < 3; ++i) simple = simple && a.k_stride[i] == a.v_stride[i] && a.k_stride[i] / 8 < (int64_t(1) << 31);
-    // a lane's offset within its instruction's rows is 32 bits
-    simple = simple && a.k_stride[1] < (int64_t(1) << 27);
-    a.simple_rows = simple ? 1 : 0;
-    a.page_units = simple ? uint32_t(a.k_stride[0] / 8) : 0u;
-    a.slot_units = simple ? uint32_t(a.k_stride[1] / 8) : 0u;
+    // a load instruction's rows in one page, and a lane's offset among them in
+    // 32 bits
+    a.simple_rows = in.cache.page_size >= 512u / uint32_t(p.dp) && in.cache.k_stride[1] < (int64_t(1) << 27) &&
+                    in.cache.v_stride[1] == in.cache.k_stride[1];
     a.table_stride = in.table_stride;
     a.n_pages = in.cache.n_pages;
     a.page_shift = dfc::log2_of(in.cache.page_size);
@@ -1000,12 +963,15 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     a.scale_log2 = in.scale * 1.44269504088896340736f;
     a.rows_per_tile = p.rows_per_tile;
     a.key_tile = uint32_t(p.kt);
+    a.rows_shift = dfc::log2_of(p.rows_per_tile);
+    a.key_shift = dfc::log2_of(uint32_t(p.kt));
     a.min_piece = p.min_piece;
     a.resident = p.resident;
     a.piece_cost = p.piece_cost;
     a.join_cost = p.join_cost;
     a.extra = p.extra;
     a.tile_cap = p.tile_cap;
+    a.join_shares = p.rw >= 4 ? (p.most_rows + 7u) / 8u : p.most_rows;
     uint8_t *ws = static_cast<uint8_t *>(in.workspace_dev);
     a.tile_count = reinterpret_cast<uint32_t *>(ws);
     a.tiles = p.extra ? reinterpret_cast<Tile *>(ws + p.off_tiles) : nullptr;
