@@ -810,19 +810,31 @@ LaunchPlan launch_plan(const dfc_attention_args &a) {
     LaunchPlan p;
     const uint32_t group = a.heads / a.cache.kv_heads;
     p.dp = a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256;
-    // most rows a request has per cache head
+    // most rows a request has per cache head: no tile needs more
     const uint64_t most = std::min<uint64_t>(a.max_q_len ? a.max_q_len : a.tokens, a.tokens) * group;
-    // one wavefront holds a whole key tile of K and V on its way to LDS: too
-    // many registers at 256 columns
-    p.rw = most <= 32 && p.dp <= 128 ? 1 : most <= 64 ? 2 : 4;
+    const int fit = most <= 32 ? 1 : most <= 64 ? 2 : most <= 128 ? 4 : 8;
+    // Small tiles give a small step more workgroups, large ones read K and V
+    // less often.  Decided by the pairs of 32 rows and 64 keys there may be
+    // (us, Llama-3-8B heads, tiles of 32 / 64 / 128 / 256 rows; prompts of
+    // 128, 512, 2048, 4096: 11.7 / 12.7 / 14.8 / 17.9, 25.9 / 21.6 / 25.9 /
+    // 26.5, 108 / 83 / 75 / 78, 321 / 251 / 203 / 185; 128 tokens over 4000:
+    // 40 / 39 / 36 / 37, 256 over 32000: 274 / 224 / 183 / 166).
+    uint64_t keys = uint64_t(a.max_pages) * a.cache.page_size;
+    if (a.window) keys = std::min<uint64_t>(keys, uint64_t(a.window) + most / group);
+    const double pairs = double(a.tokens * group) / 32.0 * a.cache.kv_heads * double(keys) / 64.0;
+    p.rw = std::min(fit, pairs < 2048.0 ? 1 : pairs < 12288.0 ? 2 : pairs < 49152.0 ? 4 : 8);
+    if (most <= 32) p.rw = 1;
     bool same = true;  // K and V have one layout
     for (int i = 0; i < 2; ++i) same = same && a.cache.k_stride[i] == a.cache.v_stride[i];
-    if (p.rw == 4 && p.dp <= 128 && same && a.tokens * group / 256u * a.cache.kv_heads >= 256u) p.rw = 8;
+    if (p.rw == 8 && (p.dp > 128 || !same)) p.rw = 4;
+    // one wavefront holds a whole key tile of K and V on its way to LDS: too
+    // many registers at 256 columns
+    if (p.rw == 1 && p.dp > 128) p.rw = 2;
     p.kt = p.rw >= 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
     p.resident = p.dp > 128 || p.rw == 8 ? 256u : 512u;
     p.min_piece = p.rw >= 4 ? 2u : kWaves / uint32_t(p.rw);
-    p.piece_cost = p.rw >= 4 ? 1.0f : 4.0f;
+    p.piece_cost = 4.0f;
     p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
     const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
                                               uint64_t(a.tokens) * group);
@@ -943,10 +955,6 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
         a.k_units[i] = uint32_t(in.cache.k_stride[i] / 8);
         a.v_units[i] = uint32_t(in.cache.v_stride[i] / 8);
     }
-    // a load instruction's rows in one page, and a lane's offset among them in
-    // 32 bits
-    a.simple_rows = in.cache.page_size >= 512u / uint32_t(p.dp) && in.cache.k_stride[1] < (int64_t(1) << 27) &&
-                    in.cache.v_stride[1] == in.cache.k_stride[1];
     a.table_stride = in.table_stride;
     a.n_pages = in.cache.n_pages;
     a.page_shift = dfc::log2_of(in.cache.page_size);

@@ -42,7 +42,6 @@ struct AttnArgs {
     uint32_t n_pages, page_shift, kv_heads, group, heads, dim;
     uint32_t n_requests, tokens, max_pages, window;
     int32_t causal;
-    int32_t simple_rows;       // a load instruction's rows lie in one page
     float scale, scale_log2;   // scores by exp2: scale log2(e)
     uint32_t rows_per_tile, key_tile, rows_shift, key_shift;  // powers of two
     uint32_t min_piece;  // a piece has min_piece key tiles or more

@@ -174,10 +174,17 @@ def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_siz
               table_stride, _vector(free_pages, i32, free_pages.shape[0], dev, "free_pages"),
               _vector(cursor, i64, 2, dev, "cursor"))
     if out is None:
-        out = PagedPlan(new_lens.new_empty(n), new_lens.new_empty(n + 1), cursor.new_empty(tokens),
-                        new_lens.new_empty(tokens), cursor.new_empty(2))
-        _keep(stream, dev, *out)
-        seq_lens, cu_q, slots, positions, cursor_out = (t.data_ptr() for t in out)
+        # two allocations rather than five
+        narrow = torch.empty(2 * n + 1 + tokens, dtype=i32, device=dev)
+        wide = torch.empty(tokens + 2, dtype=i64, device=dev)
+        _keep(stream, dev, narrow, wide)
+        at = narrow.data_ptr()
+        seq_lens, cu_q, positions = at, at + 4 * n, at + 4 * (2 * n + 1)
+        slots = wide.data_ptr()
+        cursor_out = slots + 8 * tokens
+        lens, starts, places = narrow.split_with_sizes((n, n + 1, tokens))
+        slot_view, cursor_view = wide.split_with_sizes((tokens, 2))
+        out = PagedPlan(lens, starts, slot_view, places, cursor_view)
     else:
         seq_lens = _vector(out.seq_lens, i32, n, dev, "the plan's seq_lens")
         cu_q = _vector(out.cu_q, i32, n + 1, dev, "the plan's cu_q")
@@ -215,7 +222,7 @@ def paged_append(k, v, k_cache, v_cache, slots, q=None, q_out=None, positions=No
         q_heads = q.shape[1]
         q_ptr, q0, q1 = _rows(q, "q", source, q.shape, dev)
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=q.device)
+            q_out = torch.empty(q.shape, dtype=k_cache.dtype, device=dev)
             _keep(stream, dev, q_out)
         out_ptr, o0, o1 = _rows(q_out, "q_out", k_cache.dtype, q.shape, dev)
     rot = angles = max_pos = pos = 0
@@ -284,12 +291,12 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: flo
     _count(max_q_len, "max_q_len")
     q_ptr, q0, q1 = _rows(q, "q", dtype, shape, dev)
     if out is None:
-        out = torch.empty(shape, dtype=dtype, device=q.device)
+        out = torch.empty_like(q) if q.is_contiguous() else torch.empty(shape, dtype=dtype, device=dev)
         _keep(stream, dev, out)
     out_ptr, o0, o1 = _rows(out, "out", dtype, shape, dev)
     lse_ptr = 0
     if lse is True:
-        lse = torch.empty((tokens, heads), dtype=torch.float32, device=q.device)
+        lse = torch.empty((tokens, heads), dtype=torch.float32, device=dev)
         _keep(stream, dev, lse)
         lse_ptr = lse.data_ptr()
     elif lse is not None:
@@ -299,7 +306,7 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: flo
         lse_ptr = lse.data_ptr()
     if workspace is None:
         workspace = torch.empty(_workspace_bytes(*cache[9:], heads, n, width, max_q_len, tokens), dtype=torch.uint8,
-                                device=q.device)
+                                device=dev)
         _keep(stream, dev, workspace)
     elif workspace.get_device() != dev or not workspace.is_contiguous():
         raise TypeError("workspace must be a contiguous tensor on the call's device")

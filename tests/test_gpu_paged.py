@@ -137,6 +137,91 @@ def test_attention_against_the_definition(case, dtype):
         s.check(*s.run(max_q_len=hint))
 
 
+def check_rows(s, out, lse, window=0, r=0, rows=None):
+    """Rows of request r one at a time against the definition (causal)."""
+    a, n, total = int(s.cu[r]), s.new[r], s.total[r]
+    k, v = (op.gather(as64(c), s.table[r].numpy(), s.page, total) for c in (s.k, s.v))
+    dim, u = s.q.shape[2], U[s.q.dtype]
+    q, got, got_lse = as64(s.q[a: a + n]), as64(out[a: a + n]), as64(lse[a: a + n])
+    edges = [i for i in (0, 1, 7, 8, 15, 16, 31, 32, 63, 64, 65, n // 2, n - 65, n - 33, n - 2, n - 1) if 0 <= i < n]
+    for i in sorted(set(edges if rows is None else rows)):
+        m = total - n + i + 1
+        lo = max(0, m - window) if window else 0
+        ref, ref_lse, spread, top, mass = op.attention(q[i: i + 1], k[lo:m], v[lo:m], dim ** -0.5)
+        e = 2.0 ** -23 * (dim * mass + 2 * top + (m - lo) + 16)[..., None]
+        bound = (u + 2 * e) * spread + u * np.abs(ref) + 2.0 ** -32 * (m - lo) * np.abs(v).max()
+        assert (np.abs(got[i] - ref[0]) <= bound[0]).all(), (i, np.abs(got[i] - ref[0]).max())
+        assert (np.abs(got_lse[i] - ref_lse[0]) <= 4 * e[0, :, 0] + 2.0 ** -21 * (1 + np.abs(ref_lse[0]))).all(), i
+
+
+# Steps large enough for the tallest tiles: a prompt, a chunk whose keys are
+# split, chunks beside single tokens under a window, heads narrower than the
+# registers' columns, pages smaller than a load's rows.
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("total,new,heads,kv_heads,dim,page,window", [
+    ([2051], [2051], 32, 8, 128, 16, 0),
+    ([2050], [2049], 32, 8, 64, 64, 0),
+    ([20000], [333], 16, 2, 128, 32, 0),
+    ([4100, 1300, 1, 700], [1900, 1, 1, 500], 36, 12, 64, 16, 777),
+    ([3000, 70], [2500, 70], 24, 8, 80, 2, 0),
+])
+def test_attention_of_large_steps(total, new, heads, kv_heads, dim, page, window, dtype):
+    s = Step(total, new, heads, kv_heads, dim, page, dtype, seed=sum(total))
+    say("large step", total, new, dtype)
+    out, lse = s.run(window=window, max_q_len=max(new))
+    assert torch.isfinite(out.float()).all() and torch.isfinite(lse).all()
+    for r in range(len(total)):
+        check_rows(s, out, lse, window, r)
+
+
+def test_large_step_without_the_causal_mask():
+    s = Step([2100], [2080], 32, 8, 64, 16, torch.bfloat16, seed=20)
+    say("large step, not causal")
+    out, lse = s.run(causal=False)
+    keep, s.new, s.q = s.new, [40], s.q[[*range(8), *range(1000, 1024), *range(2072, 2080)]]
+    rows = [*range(8), *range(1000, 1024), *range(2072, 2080)]
+    s.cu = torch.tensor([0, 40], dtype=torch.int32)
+    s.check(out[rows], lse[rows], causal=False)
+    assert keep == [2080]
+
+
+def test_large_step_with_values_that_are_not_finite_in_masked_places():
+    s = Step([2100], [2080], 32, 8, 128, 16, torch.bfloat16, seed=21)
+    clean = s.run()
+    tok = 1000   # position 1000: row 980
+    s.v[s.table[0, tok // 16], tok % 16, 0, 5] = float("inf")
+    s.k[s.table[0, tok // 16], tok % 16, 1, 7] = float("nan")
+    say("large step, not finite")
+    out, lse = s.run()
+    assert torch.isfinite(out[:980].float()).all() and torch.isfinite(lse[:980]).all()
+    check_rows(s, out, lse, rows=[0, 600, 900, 950, 970, 979])
+    assert torch.isposinf(out[980:, :4, 5].float()).all() and torch.isfinite(out[980:, :4, :5].float()).all()
+    assert torch.isnan(out[980:, 4:8].float()).all()
+    assert torch.equal(out[:, 8:], clean[0][:, 8:])
+
+
+def test_layouts_of_k_and_v_that_differ():
+    s = Step([1900], [1900], 32, 8, 64, 16, torch.bfloat16, seed=22)
+    v = s.v.permute(0, 2, 1, 3).contiguous().cuda().permute(0, 2, 1, 3)
+    out, lse = (torch.empty(s.q.shape, dtype=s.q.dtype, device="cuda"), torch.empty(s.q.shape[:2], device="cuda"))
+    say("K and V of different layouts")
+    dfc.paged_attention(s.q.cuda(), s.k.cuda(), v, s.table.cuda(), s.cu.cuda(), s.lens.cuda(), out=out, lse=lse)
+    torch.cuda.synchronize()
+    check_rows(s, out, lse)
+
+
+def test_many_requests():
+    # more requests than a wavefront has lanes, and than a workgroup has threads
+    for n in (65, 300, 700):
+        total = [(37 * r) % 90 + 1 for r in range(n)]
+        new = [min(t, 1 + r % 3) for r, t in enumerate(total)]
+        total[n // 2] += 1500
+        s = Step(total, new, 4, 2, 64, 16, torch.bfloat16, seed=n)
+        for hint in (3, 0):
+            say("many requests", n, hint)
+            s.check(*s.run(max_q_len=hint))
+
+
 @pytest.mark.parametrize("window", [1, 7, 64, 100, 2 ** 31 - 1])
 def test_attention_window(window):
     s = Step([300, 90, 64], [70, 1, 64], 8, 2, 128, 16, torch.bfloat16, seed=window % 1000)
