@@ -25,7 +25,7 @@ namespace {
 
 // ------------------------------------------------------------------- plan
 
-constexpr uint32_t kPlanThreads = 1024;
+constexpr uint32_t kPlanThreads = 256;
 constexpr uint32_t kPlanWaves = kPlanThreads / kWave;
 
 struct PlanArgs {
@@ -33,39 +33,37 @@ struct PlanArgs {
     uint32_t page_shift;
 };
 
+// Inclusive prefix sum of 32-bit values across the wavefront, in 64 bits: the
+// halves of a value add up apart from each other.
+__device__ __forceinline__ uint64_t wave_scan64(uint32_t x) {
+    return wave_inclusive_scan(x & 0xffffu) + (uint64_t(wave_inclusive_scan(x >> 16)) << 16);
+}
+
 // Exclusive prefix sums of (x, y) over the workgroup; the totals come back in
 // sum_x and sum_y.  `part` is 2 * kPlanWaves values of LDS.
-__device__ __forceinline__ void scan2(uint64_t &x, uint64_t &y, uint64_t &sum_x, uint64_t &sum_y, uint64_t *part) {
+__device__ __forceinline__ void scan2(uint32_t x, uint32_t y, uint64_t &before_x, uint64_t &before_y, uint64_t &sum_x,
+                                      uint64_t &sum_y, uint64_t *part) {
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    uint64_t ix = x, iy = y;
-#pragma unroll
-    for (int d = 1; d < kWave; d *= 2) {
-        const uint64_t ux = __shfl_up(ix, d), uy = __shfl_up(iy, d);
-        if (lane >= uint32_t(d)) {
-            ix += ux;
-            iy += uy;
-        }
-    }
+    const uint64_t ix = wave_scan64(x), iy = wave_scan64(y);
     __syncthreads();  // the previous scan's part has been read
     if (lane == kWave - 1) {
         part[wave] = ix;
         part[kPlanWaves + wave] = iy;
     }
     __syncthreads();
-    uint64_t bx = 0, by = 0;
+    before_x = ix - x;
+    before_y = iy - y;
     sum_x = sum_y = 0;
 #pragma unroll
     for (uint32_t w = 0; w < kPlanWaves; ++w) {
         const uint64_t px = part[w], py = part[kPlanWaves + w];
         if (w < wave) {
-            bx += px;
-            by += py;
+            before_x += px;
+            before_y += py;
         }
         sum_x += px;
         sum_y += py;
     }
-    x = bx + ix - x;
-    y = by + iy - y;
 }
 
 // The last j in [0, n) with key[j] <= t (key ascending, key[0] <= t).
@@ -81,10 +79,12 @@ __device__ __forceinline__ uint32_t last_at_most(const uint64_t *key, uint32_t n
     return lo;
 }
 
-// Every workgroup scans all requests (1,024 at a time) and then writes its
-// share of the step's tokens and new pages, in groups of 1,024 dealt out in
-// turn: no workgroup waits for another, and one launch does it all.  Tokens
-// and pages find their request by binary search in the scanned starts.
+// Every workgroup scans all requests (256 at a time) and then writes its share
+// of the step's tokens and new pages, in groups of 256 dealt out in turn: no
+// workgroup waits for another, and one launch does it all.  Tokens and pages
+// find their request by binary search in the scanned starts.  What bounds it
+// is the chain of latencies (lengths, scan, search, page, store), not the
+// few bytes.
 __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
     __shared__ uint64_t part[2 * kPlanWaves];
     __shared__ uint64_t tok_start[kPlanThreads], page_start[kPlanThreads];
@@ -104,6 +104,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
         const int32_t page = a.free_pages[(head + rank) % a.n_ring];
         return page < 0 ? -1 : page;
     };
+    // the first of this workgroup's groups that holds rank x or later ones
+    auto first_group = [&](uint64_t x) -> uint64_t {
+        const uint64_t g = x / kPlanThreads;
+        return g + (b + nb - uint32_t(g % nb)) % nb;
+    };
     uint64_t tok_base = 0, page_base = 0;
     for (uint32_t r0 = 0; r0 < a.n_requests; r0 += kPlanThreads) {
         const uint32_t r = r0 + tid, n_here = min(kPlanThreads, a.n_requests - r0);
@@ -121,8 +126,8 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
         const uint32_t have0 = (uint32_t(ctx) + P - 1) >> shift, need0 = (total + P - 1) >> shift;
         if (need0 > a.max_pages) bad |= uint32_t(DFC_ESIZE);
         const uint32_t have = min(have0, a.max_pages), need = min(need0, a.max_pages);
-        uint64_t ts = uint32_t(n_new), ps = need - have, t_sum, p_sum;
-        scan2(ts, ps, t_sum, p_sum, part);
+        uint64_t ts, ps, t_sum, p_sum;
+        scan2(uint32_t(n_new), need - have, ts, ps, t_sum, p_sum, part);
         ts += tok_base;
         ps += page_base;
         tok_start[tid] = ts;
@@ -136,8 +141,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
         }
         __syncthreads();
         // new pages of these requests
-        for (uint64_t g = page_base / kPlanThreads; g * kPlanThreads < page_base + p_sum; ++g) {
-            if (g % nb != b) continue;
+        for (uint64_t g = first_group(page_base); g * kPlanThreads < page_base + p_sum; g += nb) {
             const uint64_t j = g * kPlanThreads + tid;
             if (j < page_base || j >= page_base + p_sum) continue;
             const uint32_t k = last_at_most(page_start, n_here, j);
@@ -147,8 +151,7 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
         }
         // new tokens of these requests
         const uint64_t t_end = min(tok_base + t_sum, a.tokens);
-        for (uint64_t g = tok_base / kPlanThreads; g * kPlanThreads < t_end; ++g) {
-            if (g % nb != b) continue;
+        for (uint64_t g = first_group(tok_base); g * kPlanThreads < t_end; g += nb) {
             const uint64_t t = g * kPlanThreads + tid;
             if (t < tok_base || t >= t_end) continue;
             const uint32_t k = last_at_most(tok_start, n_here, t);
@@ -187,8 +190,9 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
 struct AppendArgs {
     dfc_append_args a;
     uint32_t page_shift;
-    uint32_t per_head, per_token;  // 8-value chunks of a head, of a token's q, k and v
-    uint64_t chunks;
+    uint32_t chunks, units;      // 8-value chunks of a head; threads per head
+    uint32_t per_token;          // threads per token
+    uint64_t threads;
 };
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
@@ -205,21 +209,46 @@ __device__ __forceinline__ void load8(const S *p, float (&x)[8]) {
     for (int i = 0; i < 8; ++i) x[i] = float(v[i]);
 }
 
-// One thread handles 8 values of one head of one token: it reads them (and
-// the 8 they pair with when the pairs lie half a rotation apart), rotates,
-// rounds to nearest even and writes 16 bytes.
+// The pairs (x, y) of 8 turned by their angles.
+__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float *cosines, const float *sines) {
+    float c[8], s[8];
+    load8(cosines, c);
+    load8(sines, s);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float u = x[i], w = y[i];
+        x[i] = u * c[i] - w * s[i];
+        y[i] = w * c[i] + u * s[i];
+    }
+}
+
+__device__ __forceinline__ void turn_inside(float (&x)[8], const float *cosines, const float *sines) {
+    const float4 co = *reinterpret_cast<const float4 *>(cosines), si = *reinterpret_cast<const float4 *>(sines);
+    const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float u = x[2 * i], w = x[2 * i + 1];
+        x[2 * i] = u * c[i] - w * s[i];
+        x[2 * i + 1] = w * c[i] + u * s[i];
+    }
+}
+
+// One thread takes two chunks of 8 values of one head of one token: those that
+// pair up half a rotation apart, elsewhere two that lie as far from each other
+// as the head's other threads reach.  Every value is read and written once.
+// Memory bound: 8,192 tokens of 32 + 8 heads of 128 in bfloat16 move 206 MB.
 template <typename S, typename E>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     using E8 = __attribute__((ext_vector_type(8))) E;
     const dfc_append_args &a = p.a;
     const uint64_t base = uint64_t(blockIdx.x) * 256u;
-    if (base + threadIdx.x >= p.chunks) return;
+    if (base + threadIdx.x >= p.threads) return;
     // the block's first token by one uniform division, the rest in 32 bits
     const uint64_t t_base = base / p.per_token;
     const uint32_t rest = uint32_t(base - t_base * p.per_token) + threadIdx.x;
     const uint64_t t = t_base + rest / p.per_token;
     const uint32_t in_token = rest % p.per_token;
-    const uint32_t row = in_token / p.per_head, d = 8u * (in_token % p.per_head);
+    const uint32_t row = in_token / p.units, u = in_token % p.units;
     const uint32_t nk = a.cache.kv_heads;
     // rows of a token: k heads, v heads, q heads
     const uint32_t which = row < nk ? 0u : row < 2u * nk ? 1u : 2u;
@@ -244,40 +273,36 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
         src = which == 0u ? static_cast<const S *>(a.k_dev) + int64_t(t) * a.k_src_stride[0] + int64_t(h) * a.k_src_stride[1]
                           : static_cast<const S *>(a.v_dev) + int64_t(t) * a.v_src_stride[0] + int64_t(h) * a.v_src_stride[1];
     }
-    float x[8];
-    load8(src + d, x);
-    if (which != 1u && d < a.rot_dim) {
-        const uint32_t half = a.rot_dim / 2u;
+    const uint32_t turned = which == 1u ? 0u : a.rot_dim / 8u;  // chunks that are rotated, an even number
+    const uint32_t c0 = u < turned / 2u ? u : u + turned / 2u;
+    const uint32_t c1 = u < turned / 2u ? u + turned / 2u : c0 + p.units - turned / 2u;
+    const bool two = c1 < p.chunks;
+    float x[8], y[8] = {};
+    load8(src + 8u * c0, x);
+    if (two) load8(src + 8u * c1, y);
+    if (c0 < turned) {
         int32_t pos = a.positions[t];
         if (pos < 0 || uint32_t(pos) >= a.max_positions) {
             if (a.status_dev) atomicOr(a.status_dev, kStatusCorrupt);
             pos = 0;
         }
-        const float *cs = a.rotary_dev + int64_t(pos) * a.rot_dim;
+        const float *cosines = a.rotary_dev + int64_t(pos) * a.rot_dim, *sines = cosines + a.rot_dim / 2u;
         if (a.interleaved) {
-            const float4 co = *reinterpret_cast<const float4 *>(cs + d / 2u);
-            const float4 si = *reinterpret_cast<const float4 *>(cs + half + d / 2u);
-            const float c[4] = {co.x, co.y, co.z, co.w}, s[4] = {si.x, si.y, si.z, si.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float u = x[2 * i], w = x[2 * i + 1];
-                x[2 * i] = u * c[i] - w * s[i];
-                x[2 * i + 1] = w * c[i] + u * s[i];
-            }
+            turn_inside(x, cosines + 4u * c0, sines + 4u * c0);
+            turn_inside(y, cosines + 4u * c1, sines + 4u * c1);
         } else {
-            const bool second = d >= half;
-            float y[8], c[8], s[8];
-            load8(src + (second ? d - half : d + half), y);
-            load8(cs + (second ? d - half : d), c);
-            load8(cs + (second ? d : d + half), s);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = x[i] * c[i] + (second ? y[i] : -y[i]) * s[i];
+            turn(x, y, cosines + 8u * c0, sines + 8u * c0);
         }
     }
     E8 out;
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = E(x[i]);
-    *reinterpret_cast<E8 *>(dst + d) = out;
+    *reinterpret_cast<E8 *>(dst + 8u * c0) = out;
+    if (two) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) out[i] = E(y[i]);
+        *reinterpret_cast<E8 *>(dst + 8u * c1) = out;
+    }
 }
 
 template <typename S, typename E>
@@ -335,16 +360,16 @@ dfc_status dfc_paged_append(const dfc_append_args *args, void *stream) {
         if (!aligned16(a.q_dev) || !aligned16(a.q_out_dev)) return DFC_EINVAL;
         for (int i = 0; i < 2; ++i)
             if (a.q_stride[i] % unit || a.q_out_stride[i] % 8) return DFC_EINVAL;
-        // a chunk is read again by the thread of the chunk it pairs with
-        if (a.rot_dim && a.q_dev == a.q_out_dev) return DFC_EINVAL;
+        if (a.q_dev == a.q_out_dev && (a.rot_dim || a.source_dtype == DFC_F32)) return DFC_EINVAL;
     }
     AppendArgs p;
     p.a = a;
     p.page_shift = dfc::log2_of(a.cache.page_size);
-    p.per_head = a.cache.head_dim / 8u;
-    p.per_token = p.per_head * (a.q_heads + 2u * a.cache.kv_heads);
-    p.chunks = uint64_t(p.per_token) * a.tokens;
-    const uint64_t blocks = dfc::ceil_div(p.chunks, uint64_t(256));
+    p.chunks = a.cache.head_dim / 8u;
+    p.units = (p.chunks + 1u) / 2u;
+    p.per_token = p.units * (a.q_heads + 2u * a.cache.kv_heads);
+    p.threads = uint64_t(p.per_token) * a.tokens;
+    const uint64_t blocks = dfc::ceil_div(p.threads, uint64_t(256));
     if (blocks > 0x7fffffffull) return DFC_EUNSUPPORTED;
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool bf = a.cache.dtype == DFC_BF16;
