@@ -509,8 +509,10 @@ typedef struct {
  * 2^30, strides of the cache past 2^34), DFC_EHIP. */
 dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream);
 
-/* Bytes of the workspace for those arguments (host; reads sizes only, no
- * pointers but the cache's are needed). */
+/* Bytes of the workspace for those arguments (host; no pointers but the
+ * cache's are needed).  A function of the cache's sizes and type, heads,
+ * n_requests, max_pages, max_q_len and tokens alone: it serves calls of any
+ * window, mask and strides. */
 dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_t *bytes);
 
 /* Human-readable name of a status code. */

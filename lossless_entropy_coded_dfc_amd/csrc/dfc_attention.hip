@@ -806,30 +806,39 @@ struct LaunchPlan {
     uint64_t off_tiles, off_ml, off_o, bytes;
 };
 
-LaunchPlan launch_plan(const dfc_attention_args &a) {
-    LaunchPlan p;
+// most rows a request has per cache head: no tile needs more
+uint64_t most_rows(const dfc_attention_args &a) {
+    return std::min<uint64_t>(a.max_q_len ? a.max_q_len : a.tokens, a.tokens) * (a.heads / a.cache.kv_heads);
+}
+
+// 32-row units of a tile of `most` rows, in the heights there are
+int tallest(uint64_t most) { return most <= 32 ? 1 : most <= 64 ? 2 : most <= 128 ? 4 : 8; }
+
+// Tile height, in units of 32 rows.  Small tiles give a small step more
+// workgroups, large ones read K and V less often.  Decided by the pairs of 32
+// rows and 64 keys there may be (us, Llama-3-8B heads, tiles of 32 / 64 / 128 /
+// 256 rows; prompts of 128, 512, 2048, 4096: 11.7 / 12.7 / 14.8 / 17.9, 25.9 /
+// 21.6 / 25.9 / 26.5, 108 / 83 / 75 / 78, 321 / 251 / 203 / 185; 128 tokens
+// over 4000: 40 / 39 / 36 / 37, 256 over 32000: 274 / 224 / 183 / 166).
+int tile_height(const dfc_attention_args &a) {
     const uint32_t group = a.heads / a.cache.kv_heads;
-    p.dp = a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256;
-    // most rows a request has per cache head: no tile needs more
-    const uint64_t most = std::min<uint64_t>(a.max_q_len ? a.max_q_len : a.tokens, a.tokens) * group;
-    const int fit = most <= 32 ? 1 : most <= 64 ? 2 : most <= 128 ? 4 : 8;
-    // Small tiles give a small step more workgroups, large ones read K and V
-    // less often.  Decided by the pairs of 32 rows and 64 keys there may be
-    // (us, Llama-3-8B heads, tiles of 32 / 64 / 128 / 256 rows; prompts of
-    // 128, 512, 2048, 4096: 11.7 / 12.7 / 14.8 / 17.9, 25.9 / 21.6 / 25.9 /
-    // 26.5, 108 / 83 / 75 / 78, 321 / 251 / 203 / 185; 128 tokens over 4000:
-    // 40 / 39 / 36 / 37, 256 over 32000: 274 / 224 / 183 / 166).
+    const uint64_t most = most_rows(a);
     uint64_t keys = uint64_t(a.max_pages) * a.cache.page_size;
     if (a.window) keys = std::min<uint64_t>(keys, uint64_t(a.window) + most / group);
     const double pairs = double(a.tokens * group) / 32.0 * a.cache.kv_heads * double(keys) / 64.0;
-    p.rw = std::min(fit, pairs < 2048.0 ? 1 : pairs < 12288.0 ? 2 : pairs < 49152.0 ? 4 : 8);
-    if (most <= 32) p.rw = 1;
+    const int rw = std::min(tallest(most), pairs < 2048.0 ? 1 : pairs < 12288.0 ? 2 : pairs < 49152.0 ? 4 : 8);
     bool same = true;  // K and V have one layout
     for (int i = 0; i < 2; ++i) same = same && a.cache.k_stride[i] == a.cache.v_stride[i];
-    if (p.rw == 8 && (p.dp > 128 || !same)) p.rw = 4;
-    // one wavefront holds a whole key tile of K and V on its way to LDS: too
-    // many registers at 256 columns
-    if (p.rw == 1 && p.dp > 128) p.rw = 2;
+    return rw == 8 && !same ? 4 : rw;
+}
+
+LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
+    LaunchPlan p;
+    const uint32_t group = a.heads / a.cache.kv_heads;
+    p.dp = a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256;
+    // at 256 columns eight wavefronts have no room for two key tiles, and one
+    // that holds a whole key tile of K and V on its way to LDS no registers
+    p.rw = p.dp > 128 ? std::min(std::max(rw, 2), 4) : rw;
     p.kt = p.rw >= 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
     p.resident = p.dp > 128 || p.rw == 8 ? 256u : 512u;
@@ -847,13 +856,21 @@ LaunchPlan launch_plan(const dfc_attention_args &a) {
     p.tile_cap = uint32_t(tiles);
     // a tile's pieces are at most twice those beyond its first
     p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, tiles + extra));
-    p.most_rows = uint32_t(std::min<uint64_t>(most, p.rows_per_tile));
+    p.most_rows = uint32_t(std::min<uint64_t>(most_rows(a), p.rows_per_tile));
     p.off_tiles = 256;
     p.off_ml = (p.off_tiles + uint64_t(p.extra) * sizeof(Tile) + 255u) & ~uint64_t(255);
     const uint64_t rows = uint64_t(p.slot_cap) * a.cache.kv_heads * p.rows_per_tile;
     p.off_o = (p.off_ml + rows * 8u + 255u) & ~uint64_t(255);
     p.bytes = p.off_o + rows * uint64_t(p.dp) * 4u;
     return p;
+}
+
+// What a call needs depends on its tile height, and so on the window and the
+// layouts; one size has to serve every call of the same sizes.
+uint64_t workspace_bytes(const dfc_attention_args &a) {
+    uint64_t bytes = 0;
+    for (int rw = 1; rw <= tallest(most_rows(a)); rw *= 2) bytes = std::max(bytes, launch_plan(a, rw).bytes);
+    return bytes;
 }
 
 dfc_status check_attention(const dfc_attention_args &a) {
@@ -918,7 +935,7 @@ dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_
     if (!args || !bytes) return DFC_EINVAL;
     const dfc_status s = check_attention(*args);
     if (s != DFC_OK) return s;
-    *bytes = args->tokens && args->n_requests ? launch_plan(*args).bytes : 0;
+    *bytes = args->tokens && args->n_requests ? workspace_bytes(*args) : 0;
     return DFC_OK;
 }
 
@@ -935,8 +952,8 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     if (reinterpret_cast<uintptr_t>(in.workspace_dev) & 255u) return DFC_EINVAL;
     for (int i = 0; i < 2; ++i)
         if (in.q_stride[i] % 8 || in.out_stride[i] % 8) return DFC_EINVAL;
-    const LaunchPlan p = launch_plan(in);
-    if (in.workspace_bytes < p.bytes) return DFC_ESIZE;
+    const LaunchPlan p = launch_plan(in, tile_height(in));
+    if (in.workspace_bytes < workspace_bytes(in)) return DFC_ESIZE;
     AttnArgs a;
     std::memset(&a, 0, sizeof(a));
     a.q = in.q_dev;

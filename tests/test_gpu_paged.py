@@ -210,6 +210,23 @@ def test_layouts_of_k_and_v_that_differ():
     check_rows(s, out, lse)
 
 
+@pytest.mark.parametrize("dim", [64, 256])
+def test_one_workspace_for_every_window_and_layout(dim):
+    # the bytes paged_attention_workspace gives, in a workspace that is NaN
+    s = Step([1900, 300], [1900, 30], 32, 8, dim, 16, torch.bfloat16, seed=23)
+    q, k, v, table, cu, lens = s.q.cuda(), s.k.cuda(), s.v.cuda(), s.table.cuda(), s.cu.cuda(), s.lens.cuda()
+    other = s.v.permute(0, 2, 1, 3).contiguous().cuda().permute(0, 2, 1, 3)
+    size = dfc.paged_attention_workspace(q, k, v, table, cu, lens)
+    for window in (0, 3, 500):
+        for values in (v, other):
+            say("workspace", dim, window, values.stride())
+            out, lse = dfc.paged_attention(q, k, values, table, cu, lens, window=window, lse=True,
+                                           workspace=torch.full((size,), 255, dtype=torch.uint8, device="cuda"))
+            torch.cuda.synchronize()
+            check_rows(s, out, lse, window)
+            check_rows(s, out, lse, window, r=1)
+
+
 def test_many_requests():
     # more requests than a wavefront has lanes, and than a workgroup has threads
     for n in (65, 300, 700):

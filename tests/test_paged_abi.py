@@ -54,3 +54,36 @@ def test_layout(name, tmp_path):
                 assert places == [offset + k * size // ARRAYS.get(field, 1)], field
             at += 1
     assert at == values
+
+
+def test_one_workspace_serves_every_window_and_layout():
+    # The kernel's shape follows the window and the layouts; the bytes a call
+    # dfc_paged_attention_workspace gives are a matter of the sizes alone
+    import ctypes
+    import lossless_entropy_coded_dfc_amd as dfc
+    paged = pytest.importorskip("lossless_entropy_coded_dfc_amd.paged")
+    lib = paged._lib()
+
+    def args(window, v_stride, dim, heads, n, tokens, width, hint):
+        kv = 8
+        return paged.ATTENTION_ARGS.pack(256, 256, 16 * kv * dim, kv * dim, dim, *v_stride, 4096, 16, kv, dim, 0, heads,
+                                         n, width, hint, tokens, 256, 256, heads * dim, dim, heads * dim, dim, 0, 256,
+                                         width, 256, 256, 1.0, 1, window, 256, 0, 0)
+
+    def need(a):
+        out = ctypes.c_uint64()
+        assert lib.dfc_paged_attention_workspace(a, ctypes.byref(out)) == 0
+        return out.value
+
+    for dim, heads, n, tokens, width, hint in [(128, 32, 1, 2048, 128, 0), (128, 32, 1, 513, 2032, 513),
+                                               (64, 32, 4, 1900, 400, 1900), (128, 32, 16, 680, 2048, 333),
+                                               (256, 16, 2, 700, 1000, 0), (80, 8, 3, 300, 9, 0), (128, 32, 64, 64, 512, 1)]:
+        sizes = dim, heads, n, tokens, width, hint
+        plain = 16 * 8 * dim, 8 * dim, dim
+        most = need(args(0, plain, *sizes))
+        for window in (0, 1, 64, 777, 5000):
+            for layout in (plain, (16 * 8 * dim, dim, 16 * dim)):
+                a = args(window, layout, *sizes)
+                assert need(a) == most, (sizes, window, layout)
+                # no bytes given: refused before anything is launched
+                assert lib.dfc_paged_attention(a, None) == dfc.ESIZE, (sizes, window, layout)
