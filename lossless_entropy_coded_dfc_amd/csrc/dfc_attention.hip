@@ -802,7 +802,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
 struct LaunchPlan {
     int rw, kt, dp;
     uint32_t rows_per_tile, min_piece, resident, extra, tile_cap, slot_cap, most_rows;
-    float piece_cost, join_cost;
+    float piece_cost, split_cost, join_cost;
     uint64_t off_tiles, off_ml, off_o, bytes;
 };
 
@@ -841,22 +841,45 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     p.rw = p.dp > 128 ? std::min(std::max(rw, 2), 4) : rw;
     p.kt = p.rw >= 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
+    p.most_rows = uint32_t(std::min<uint64_t>(most_rows(a), p.rows_per_tile));
     p.resident = p.dp > 128 || p.rw == 8 ? 256u : 512u;
     p.min_piece = p.rw >= 4 ? 2u : kWaves / uint32_t(p.rw);
+    // measured by their sweep: without split_cost 256 tokens over 256 took
+    // 29.5 us and not 20.5, eight times 64 over 500 47.2 and not 23.9; at half
+    // of it 300 over 700 took 33.6 and not 29.8
     p.piece_cost = 4.0f;
+    p.split_cost = float(p.most_rows) / 4.0f;
     p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
     const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
                                               uint64_t(a.tokens) * group);
-    // a tile of c key tiles has at most ceil(c / min_piece) pieces; there are
-    // up to four rounds of pieces beyond one a tile
-    const uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt)) + 1u;
+    // a tile of c key tiles has at most ceil(c / min_piece) pieces
+    uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt)) + 1u;
     const uint64_t each = longest > p.min_piece ? dfc::ceil_div(longest, uint64_t(p.min_piece)) - 1u : 0u;
-    const uint64_t extra = std::min<uint64_t>(4u * p.resident / a.cache.kv_heads + 1u, tiles * each);
+    // Up to two rounds of pieces beyond one a tile.  With one, 64 requests of
+    // 1 to 8191 tokens take 248 us and not 216 (four: 213); with four, 64 of
+    // 700 take 55 and not 49: workgroups that find no piece come last, 2 us a
+    // round.
+    uint64_t extra = std::min<uint64_t>(2u * p.resident / a.cache.kv_heads + 1u, tiles * each);
+    // The joining's launch alone costs 2.5 us, some five key tiles.  Where the
+    // device could not win that back by splitting tiles as long as they may
+    // be, none is split (one token over 250 keys: 9.4 and not 11.6 us, over 450
+    // 12.0 / 11.4; prompt of 512 18.7 / 21.5, 128 tokens over 600 17.4 / 23.7, 64
+    // single ones over 700 40 / 49).  The lengths of several requests may
+    // differ, so that splitting pays however many tiles there are (64 of 1 to
+    // 8191: 245 without, 216 with it): they are left to the device from 40 key
+    // tiles on.
+    if (a.window && a.causal)
+        longest = std::min<uint64_t>(longest, (uint64_t(a.window) + p.rows_per_tile / group) / p.kt + 3u);
+    const uint64_t whole = dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile));
+    const double load = double(a.n_requests == 1 ? whole : tiles) * a.cache.kv_heads / p.resident;
+    const double rounds = a.n_requests == 1 ? std::ceil(load) : std::max(1.0, load);
+    const double unsplit = rounds * (double(longest) + p.piece_cost);
+    const double split = load * double(longest) + p.piece_cost + p.split_cost + p.join_cost + 5.0;
+    if (unsplit <= split && (a.n_requests == 1 || longest <= 40u)) extra = 0;
     p.extra = uint32_t(extra);
     p.tile_cap = uint32_t(tiles);
     // a tile's pieces are at most twice those beyond its first
     p.slot_cap = uint32_t(std::min<uint64_t>(2u * extra, tiles + extra));
-    p.most_rows = uint32_t(std::min<uint64_t>(most_rows(a), p.rows_per_tile));
     p.off_tiles = 256;
     p.off_ml = (p.off_tiles + uint64_t(p.extra) * sizeof(Tile) + 255u) & ~uint64_t(255);
     const uint64_t rows = uint64_t(p.slot_cap) * a.cache.kv_heads * p.rows_per_tile;
@@ -865,10 +888,12 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     return p;
 }
 
-// What a call needs depends on its tile height, and so on the window and the
-// layouts; one size has to serve every call of the same sizes.
-uint64_t workspace_bytes(const dfc_attention_args &a) {
+// What a call needs depends on the window, and by the tile height on the
+// layouts; one size has to serve every call of the same sizes.  A window never
+// needs more.
+uint64_t workspace_bytes(dfc_attention_args a) {
     uint64_t bytes = 0;
+    a.window = 0;
     for (int rw = 1; rw <= tallest(most_rows(a)); rw *= 2) bytes = std::max(bytes, launch_plan(a, rw).bytes);
     return bytes;
 }
@@ -993,6 +1018,7 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     a.min_piece = p.min_piece;
     a.resident = p.resident;
     a.piece_cost = p.piece_cost;
+    a.split_cost = p.split_cost;
     a.join_cost = p.join_cost;
     a.extra = p.extra;
     a.tile_cap = p.tile_cap;

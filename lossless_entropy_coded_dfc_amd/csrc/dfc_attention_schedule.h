@@ -46,7 +46,9 @@ struct AttnArgs {
     uint32_t rows_per_tile, key_tile, rows_shift, key_shift;  // powers of two
     uint32_t min_piece;  // a piece has min_piece key tiles or more
     uint32_t resident;         // workgroups that run at once
-    float piece_cost, join_cost;  // what a piece, and the joining, cost in key tiles
+    // in key tiles: what a piece costs beside its keys, one of several of a
+    // tile more (its sums written and read again), and the joining
+    float piece_cost, split_cost, join_cost;
     uint32_t extra;            // pieces there may be beyond one a tile
     uint32_t tile_cap;
     uint32_t join_shares;      // shares a tile's rows are joined in
@@ -127,26 +129,40 @@ __device__ __forceinline__ float wave_max(float x) {
 // for its time; the least wins.  Cutting one long request into as many equal
 // pieces as run at once, cutting many ragged ones finer so that the last
 // round is full, and not cutting where it does not pay all come out of it.
-__device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, uint32_t c) {
-    const uint32_t lane = threadIdx.x % kWave;
+// The wavefronts count a share of the requests each: one that counts all of
+// 64 takes 2 us, which the workgroups left without a piece spend as well.
+template <uint32_t NT>
+__device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, uint32_t c, uint32_t *scratch) {
+    constexpr uint32_t kShares = NT / kWave;
+    const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
     const float longest = wave_max(float(c));
     const float parts = lane < 32u ? float(lane + 1u) : 32.0f * __builtin_amdgcn_exp2f(float(lane - 31u) * 0.15625f);
     const uint32_t piece = max(a.min_piece, uint32_t(ceilf(longest / parts)));
     const float inv = 1.0f / float(piece);
-    uint64_t p = 0;
-    uint32_t tiles = 0;
-    for (uint32_t r = 0; r < a.n_requests; ++r) {
+    const bool shared = a.n_requests > 4u;
+    uint64_t more = 0;  // pieces beyond one a tile
+    for (uint32_t r = shared ? wave : 0u; r < a.n_requests; r += shared ? kShares : 1u) {
         const uint32_t nr = __builtin_amdgcn_readlane(n, r), cr = __builtin_amdgcn_readlane(c, r);
         uint32_t s = uint32_t(float(cr) * inv);  // never below ceil(c / piece) after this
         s += s * piece < cr;
         s += s * piece < cr;
-        tiles += nr;
-        p += uint64_t(nr) * max(s, 1u);
+        more += uint64_t(nr) * (max(s, 1u) - 1u);
     }
-    const float rounds = ceilf(float(p) * float(a.kv_heads) / float(a.resident));
-    float t = rounds * (float(piece) + a.piece_cost);
-    if (float(piece) < longest) t += a.join_cost;
-    if (p - tiles > a.extra) t = 3e38f;
+    if (shared) {
+        uint64_t *sums = reinterpret_cast<uint64_t *>(scratch);
+        sums[threadIdx.x] = more;
+        __syncthreads();
+        more = 0;
+#pragma unroll
+        for (uint32_t k = 0; k < kShares; ++k) more += sums[k * kWave + lane];
+        __syncthreads();  // read by all before the scratch is used again
+    }
+    const uint32_t tiles = __builtin_amdgcn_readlane(wave_inclusive_scan(n), 63);
+    const float rounds = ceilf(float(more + tiles) * float(a.kv_heads) / float(a.resident));
+    const bool split = float(piece) < longest;
+    float t = rounds * (float(piece) + a.piece_cost + (split ? a.split_cost : 0.0f));
+    if (split) t += a.join_cost;
+    if (more > a.extra) t = 3e38f;
     const float best = -wave_max(-t);
     const uint32_t who = __builtin_ctzll(__ballot(t == best));
     return __builtin_amdgcn_readlane(piece, who);
@@ -166,7 +182,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
         if (lane < a.n_requests) q = request(a, lane, bad);
         uint32_t n, c;
         tiles_of(a, q, n, c);
-        piece = a.extra ? choose_piece(a, n, c) : 1u << 30;
+        piece = a.extra ? choose_piece<NT>(a, n, c, scratch) : 1u << 30;
         const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u, z = s > 1u ? n : 0u;
         const uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), iz = wave_inclusive_scan(z);
         const uint32_t in = wave_inclusive_scan(n);
@@ -209,7 +225,11 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
         const bool fits = tiles <= a.tile_cap;
         if (!fits) bad |= kStatusCorrupt;
         const uint64_t target = uint64_t(a.extra) * a.kv_heads;
-        piece = a.extra ? uint32_t(min(uint64_t(1) << 30, max(uint64_t(a.min_piece), (all + target - 1u) / target)))
+        // with about as many tiles as run at once, pieces are not worth
+        // their joining below some length (80 requests of 5 tokens over 700:
+        // 85 us cut in two, 58 whole)
+        const uint32_t least = tiles * a.kv_heads >= a.resident ? 24u : a.min_piece;
+        piece = a.extra ? uint32_t(min(uint64_t(1) << 30, max(uint64_t(least), (all + target - 1u) / target)))
                         : 1u << 30;
         uint32_t px = 0, py = 0, pz = 0;  // before this chunk of requests
         uint32_t *found = scratch + NT / 16u, *part = found + 16;

@@ -137,6 +137,19 @@ def test_attention_against_the_definition(case, dtype):
         s.check(*s.run(max_q_len=hint))
 
 
+@pytest.mark.parametrize("case", range(len(CASES)))
+def test_attention_where_the_tables_are_wide(case):
+    # room for far more tokens than there are: tiles may be split, here some
+    # hundred tokens later too
+    total, new, heads, kv_heads, dim, page = CASES[case]
+    for more in (0, 900):
+        s = Step([t + more for t in total], new, heads, kv_heads, dim, page, torch.bfloat16, seed=100 + case,
+                 extra_pages=8192 // page)
+        for hint in (0, max(new)):
+            say("wide table", case, more, "hint", hint)
+            s.check(*s.run(max_q_len=hint))
+
+
 def check_rows(s, out, lse, window=0, r=0, rows=None):
     """Rows of request r one at a time against the definition (causal)."""
     a, n, total = int(s.cu[r]), s.new[r], s.total[r]
