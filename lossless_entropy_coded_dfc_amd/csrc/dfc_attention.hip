@@ -811,22 +811,36 @@ uint64_t most_rows(const dfc_attention_args &a) {
     return std::min<uint64_t>(a.max_q_len ? a.max_q_len : a.tokens, a.tokens) * (a.heads / a.cache.kv_heads);
 }
 
+int padded_dim(const dfc_attention_args &a) { return a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256; }
+
 // 32-row units of a tile of `most` rows, in the heights there are
 int tallest(uint64_t most) { return most <= 32 ? 1 : most <= 64 ? 2 : most <= 128 ? 4 : 8; }
 
-// Tile height, in units of 32 rows.  Small tiles give a small step more
-// workgroups, large ones read K and V less often.  Decided by the pairs of 32
-// rows and 64 keys there may be (us, Llama-3-8B heads, tiles of 32 / 64 / 128 /
-// 256 rows; prompts of 128, 512, 2048, 4096: 11.7 / 12.7 / 14.8 / 17.9, 25.9 /
-// 21.6 / 25.9 / 26.5, 108 / 83 / 75 / 78, 321 / 251 / 203 / 185; 128 tokens
-// over 4000: 40 / 39 / 36 / 37, 256 over 32000: 274 / 224 / 183 / 166).
+uint64_t most_tiles(const dfc_attention_args &a, int rw) {
+    const uint64_t rows = a.tokens * (a.heads / a.cache.kv_heads);
+    return std::min<uint64_t>(dfc::ceil_div(rows, uint64_t(32 * rw)) + (a.n_requests == 1 ? 0u : a.n_requests), rows);
+}
+
+uint32_t workgroups_at_once(int dp, int rw) { return dp > 128 || rw == 8 ? 256u : 512u; }
+
+// Tile height, in units of 32 rows: the least whose tiles all run at once, but
+// large tiles where keys are long, since they read K and V less often.  (us,
+// Llama-3-8B heads, tiles of 32 / 64 / 128 / 256 rows; prompts of 200, 512,
+// 1024, 2000, 4100: 11.1 / 12.8 / 16.5 / 19.7, 17.4 / 18.8 / 23.2 / 27.7, 40.0 /
+// 33.3 / 39.2 / 45.0, 98 / 79 / 72 / 76, 327 / 254 / 213 / 193; 256 tokens over
+// 2000: 43 / 42 / 63 / 70, 512 over 4000: 86 / 89 / 74 / 132, 256 over 32000: 274
+// / 224 / 183 / 166.)
 int tile_height(const dfc_attention_args &a) {
     const uint32_t group = a.heads / a.cache.kv_heads;
     const uint64_t most = most_rows(a);
+    const int dp = padded_dim(a), fit = tallest(most);
     uint64_t keys = uint64_t(a.max_pages) * a.cache.page_size;
     if (a.window) keys = std::min<uint64_t>(keys, uint64_t(a.window) + most / group);
+    // pairs of 32 rows and 64 keys there may be
     const double pairs = double(a.tokens * group) / 32.0 * a.cache.kv_heads * double(keys) / 64.0;
-    const int rw = std::min(tallest(most), pairs < 2048.0 ? 1 : pairs < 12288.0 ? 2 : pairs < 49152.0 ? 4 : 8);
+    int rw = 1;
+    for (double limit = 6000.0; rw < fit; rw *= 2, limit *= 3.3)
+        if (pairs < limit && most_tiles(a, rw) * a.cache.kv_heads <= workgroups_at_once(dp, rw)) break;
     bool same = true;  // K and V have one layout
     for (int i = 0; i < 2; ++i) same = same && a.cache.k_stride[i] == a.cache.v_stride[i];
     return rw == 8 && !same ? 4 : rw;
@@ -835,14 +849,14 @@ int tile_height(const dfc_attention_args &a) {
 LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     LaunchPlan p;
     const uint32_t group = a.heads / a.cache.kv_heads;
-    p.dp = a.cache.head_dim <= 64 ? 64 : a.cache.head_dim <= 128 ? 128 : 256;
+    p.dp = padded_dim(a);
     // at 256 columns eight wavefronts have no room for two key tiles, and one
     // that holds a whole key tile of K and V on its way to LDS no registers
     p.rw = p.dp > 128 ? std::min(std::max(rw, 2), 4) : rw;
     p.kt = p.rw >= 4 && p.dp <= 128 ? 64 : 32;
     p.rows_per_tile = 32u * uint32_t(p.rw);
     p.most_rows = uint32_t(std::min<uint64_t>(most_rows(a), p.rows_per_tile));
-    p.resident = p.dp > 128 || p.rw == 8 ? 256u : 512u;
+    p.resident = workgroups_at_once(p.dp, p.rw);
     p.min_piece = p.rw >= 4 ? 2u : kWaves / uint32_t(p.rw);
     // measured by their sweep: without split_cost 256 tokens over 256 took
     // 29.5 us and not 20.5, eight times 64 over 500 47.2 and not 23.9; at half
@@ -850,8 +864,7 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     p.piece_cost = 4.0f;
     p.split_cost = float(p.most_rows) / 4.0f;
     p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
-    const uint64_t tiles = std::min<uint64_t>(dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile)) + a.n_requests,
-                                              uint64_t(a.tokens) * group);
+    const uint64_t tiles = most_tiles(a, p.rw);
     // a tile of c key tiles has at most ceil(c / min_piece) pieces
     uint64_t longest = dfc::ceil_div(uint64_t(a.max_pages) * a.cache.page_size, uint64_t(p.kt)) + 1u;
     const uint64_t each = longest > p.min_piece ? dfc::ceil_div(longest, uint64_t(p.min_piece)) - 1u : 0u;
@@ -870,8 +883,7 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     // tiles on.
     if (a.window && a.causal)
         longest = std::min<uint64_t>(longest, (uint64_t(a.window) + p.rows_per_tile / group) / p.kt + 3u);
-    const uint64_t whole = dfc::ceil_div(a.tokens * group, uint64_t(p.rows_per_tile));
-    const double load = double(a.n_requests == 1 ? whole : tiles) * a.cache.kv_heads / p.resident;
+    const double load = double(tiles) * a.cache.kv_heads / p.resident;
     const double rounds = a.n_requests == 1 ? std::ceil(load) : std::max(1.0, load);
     const double unsplit = rounds * (double(longest) + p.piece_cost);
     const double split = load * double(longest) + p.piece_cost + p.split_cost + p.join_cost + 5.0;

@@ -135,9 +135,12 @@ template <uint32_t NT>
 __device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, uint32_t c, uint32_t *scratch) {
     constexpr uint32_t kShares = NT / kWave;
     const uint32_t lane = threadIdx.x % kWave, wave = threadIdx.x / kWave;
-    const float longest = wave_max(float(c));
+    uint32_t longest = c;
+#pragma unroll
+    for (int d = 32; d; d /= 2) longest = max(longest, uint32_t(__shfl_xor(longest, d)));
     const float parts = lane < 32u ? float(lane + 1u) : 32.0f * __builtin_amdgcn_exp2f(float(lane - 31u) * 0.15625f);
-    const uint32_t piece = max(a.min_piece, uint32_t(ceilf(longest / parts)));
+    // (the first lane's leaves every tile whole)
+    const uint32_t piece = max(a.min_piece, lane ? uint32_t(ceilf(float(longest) / parts)) : longest);
     const float inv = 1.0f / float(piece);
     const bool shared = a.n_requests > 4u;
     uint64_t more = 0;  // pieces beyond one a tile
@@ -159,7 +162,7 @@ __device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, 
     }
     const uint32_t tiles = __builtin_amdgcn_readlane(wave_inclusive_scan(n), 63);
     const float rounds = ceilf(float(more + tiles) * float(a.kv_heads) / float(a.resident));
-    const bool split = float(piece) < longest;
+    const bool split = piece < longest;
     float t = rounds * (float(piece) + a.piece_cost + (split ? a.split_cost : 0.0f));
     if (split) t += a.join_cost;
     if (more > a.extra) t = 3e38f;
