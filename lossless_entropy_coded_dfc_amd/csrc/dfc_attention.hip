@@ -10,9 +10,10 @@
 //
 // Rows.  The n_r G (token, head of the group) pairs of a request and cache
 // head are its rows; a tile is 32 RW of them, 32 per wavefront.  A workgroup
-// of four wavefronts takes one tile and one piece of its keys: RW wavefronts
-// along the rows times 4 / RW groups along the keys, whose results it joins
-// at the end.
+// takes one tile and one piece of its keys.  Of four wavefronts (RW = 1, 2,
+// 4), RW lie along the rows times 4 / RW groups along the keys, whose results
+// the workgroup joins at the end; of eight (RW = 8) all lie along the rows.
+// Pieces of one tile are joined by a second kernel.
 //
 // Layout.  Scores are computed transposed, S^T = K Q^T, with 32x32x16
 // MFMA: lane l then holds, for the row l mod 32, the keys 8 (r / 4) +
@@ -21,7 +22,15 @@
 // rounded probabilities are, as they stand, the B operand of O^T = V^T P^T
 // (the order of the keys within a step of 16 is free as long as V^T follows
 // it: the transposing LDS read gives each lane those four keys at its
-// column).
+// column).  LDS reads of both products are free of bank conflicts.
+//
+// Bounds (one MI355X, 32 heads over 8 cache heads of 128, bfloat16, time a call
+// among others; a device copy reaches 5.1 TB/s and a product of 16384-square
+// matrices 1.35 PFLOP/s).  One token a request: the bytes of K and V (64
+// requests of 1 to 8191: 212-217 us, 5.0-5.2 TB/s; 131072 keys in float16 106
+// us, 5.0 TB/s), for a short one latencies: launches, lengths, page, keys (700
+// keys 11.6 us).  Prompts: the two products (8192 tokens 548-566 us, 0.97-1.0
+// PFLOP/s; 512 tokens, a workgroup or two on each compute unit, 17 us).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -178,7 +187,7 @@ __device__ __forceinline__ const AttnArgs &again(const AttnArgs &a) {
 #endif
 }
 
-constexpr auto nothing = [](int) {};
+constexpr auto nothing = [](int) {};  // no work beside the products
 
 // A wavefront's 32 rows: their queries, limits and running sums.  Lane l has
 // row l mod 32 (half l / 32 of its keys and columns).
@@ -248,11 +257,11 @@ struct Rows {
     }
     __device__ __forceinline__ bool masks(int32_t start) const { return start + KT > hi_min || start < lo_max; }
 
-    // `beside`(g) is other work that may go among the products of group g.
     // O^T += V^T P^T (PV), S^T = K Q^T (QK), in groups of four products whose
     // operands are read kAhead groups before they are used: four wavefronts
     // that read at once wait longer for LDS than one group of products takes.
     // Left to itself the compiler reads each operand just before its product.
+    // `beside`(g) is other work that may go among the products of group g.
     template <bool PV, bool QK, int kAhead, typename F>
     __device__ __forceinline__ void products(const uint8_t *vt, const V8 (&p)[NS], const uint8_t *kt, f32x16 (&s)[NB],
                                              F &&beside) {
@@ -529,6 +538,14 @@ __device__ __forceinline__ void store(const AttnArgs &a, const Piece &w, uint32_
     }
 }
 
+// Four wavefronts, for decoding and small steps.  K and V go from the cache to
+// registers and on to LDS: the load of the next tile is under way while this
+// one is multiplied.  With RW = 1 every wavefront reads keys of its own, into
+// one buffer and without barriers: what a step of few rows needs, since the
+// keys pass through each compute unit once and two workgroups a compute unit
+// keep 5 TB/s in flight (a second buffer would leave room for one).  With more
+// along the rows, which share a tile's keys, one barrier a step suffices with
+// two buffers.
 // RW wavefronts along the rows and 4 / RW groups along the keys, tiles of KT
 // keys dealt out to the groups in turn.
 template <int DP, int RW, int KT>
@@ -612,6 +629,14 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
 //
 // A half's loads of a tile leave the cache during its products and go to LDS
 // as its weights begin.
+//
+// Against the four-wavefront kernel's 128-row tiles: a prompt of 8192 tokens 549
+// and not 608 us, of 4100 193 and not 213.  The matrix units work 47% of the
+// time (1.0 PFLOP/s): a phase of products takes some 1,900 cycles where its 32
+// products take 1,024, since the reads of K and V (LDS gives 128 bytes a cycle
+// to eight wavefronts) and the loads issue beside them.  No part alone decides:
+// with its LDS reads left out the kernel takes 93% of the time, without its
+// loads 92%, without its exponentials 95%.
 //
 // Products i read K tile i and V tile i - 1 in phases 2i and 2i + 1, so both
 // halves put tile i + 1 into LDS by the end of phase 2i + 1: K into the place
@@ -725,8 +750,11 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
 // The pieces of a split tile joined.  A wavefront takes a row (WPR = 1, for
 // tiles of many rows and few pieces) or a quarter of its pieces (WPR = 4);
 // lanes run along the row in 16-byte steps and, where the row is shorter,
-// over several pieces.  Each lane keeps its own running maximum.  A step in
-// which nothing is split costs the launch alone.
+// over several pieces.  Each lane keeps its own running maximum.  The order
+// of the pieces is fixed, so results repeat bit for bit.  Bound by the latency
+// of its chain (count, tile, sums): 2.6 us for one tile of 4 rows, 9 us for the
+// 28 MB of a step of 513 tokens over 32000.  A step in which nothing is split
+// costs the launch alone.
 template <typename E, int DP, int WPR>
 __global__ __launch_bounds__(kThreads) void join_kernel(AttnArgs a) {
     using T = Type<E>;

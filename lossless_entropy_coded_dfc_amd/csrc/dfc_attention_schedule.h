@@ -65,7 +65,7 @@ struct AttnArgs {
 // pieces each, so the pieces before a request are a prefix sum of n S, and
 // what all workgroups have to agree on is L.  Reading the lengths costs each
 // workgroup about a microsecond; a kernel that lists the pieces first, and
-// its launch, cost the step more than ten.
+// its launch, cost the step more than ten (700 keys: 23.9 us so, 12.5 this way).
 
 struct Req {
     int32_t q_start, q_len, kv_len;
