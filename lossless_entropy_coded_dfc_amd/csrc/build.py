@@ -1,5 +1,6 @@
-"""Build libdfc.so in place (host codec with g++, gfx950 decoder with hipcc),
-and libdfc_probe.so, the benchmark's streaming-ceiling kernel.
+"""Build libdfc.so in place (host codec with g++, gfx950 kernels with hipcc),
+_paged.so, the paged cache's binding to torch's tensors (g++), and
+libdfc_probe.so, the benchmark's streaming-ceiling kernel.
 
 Usage: python -m lossless_entropy_coded_dfc_amd.csrc.build [-v]
 """
@@ -17,6 +18,8 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT = os.path.join(PKG, "libdfc.so")
 # the benchmark's streaming ceiling (not part of the codec)
 PROBE_OUT = os.path.join(PKG, "libdfc_probe.so")
+# the paged cache's binding: a CPython module against torch's headers
+BIND_OUT = os.path.join(PKG, "_paged.so")
 ARCH = "gfx950"
 
 # Packed FP32 instructions are kept out of every HIP object.  Unaligned
@@ -43,6 +46,20 @@ def _run(cmd, verbose):
     subprocess.run(cmd, check=True)
 
 
+def _build_bind(verbose):
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"]]
+    lib = os.path.join(base, "lib")
+    tmp = BIND_OUT + ".tmp"
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          "-I", INCLUDE, *(x for i in include for x in ("-isystem", i)), os.path.join(HERE, "dfc_paged_bind.cpp"),
+          "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
+    os.replace(tmp, BIND_OUT)
+
+
 def build(verbose: bool = False, out: str = OUT) -> str:
     """Compile every source and link libdfc.so next to the package."""
     hipcc = _hipcc()
@@ -66,6 +83,7 @@ def build(verbose: bool = False, out: str = OUT) -> str:
         tmp = PROBE_OUT + ".tmp"
         _run([hipcc, *HIP_FLAGS, "-shared", "-o", tmp, os.path.join(HERE, "dfc_probe.hip")], verbose)
         os.replace(tmp, PROBE_OUT)
+        _build_bind(verbose)
     return out
 
 

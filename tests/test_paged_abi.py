@@ -1,77 +1,45 @@
-"""The paged cache's argument structures as the Python binding packs them
-against the C compiler's layout of include/dfc.h, field by field."""
-import os
-import subprocess
+"""The paged cache's entry points where no GPU is needed: the workspace's size
+through the C ABI, and the Python binding's refusals."""
+import ctypes
 
 import pytest
 
-ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+import lossless_entropy_coded_dfc_amd as dfc
 
-FIELDS = {
-    "dfc_paged_cache": ("CACHE", ["k_dev", "v_dev", "k_stride", "v_stride", "n_pages", "page_size", "kv_heads",
-                                  "head_dim", "dtype"]),
-    "dfc_plan_args": ("PLAN_ARGS", ["n_requests", "max_pages", "page_size", "n_ring", "tokens", "context_lens",
-                                    "new_lens", "block_table", "table_stride", "free_pages", "cursor", "seq_lens",
-                                    "cu_q", "slots", "positions", "cursor_out", "status_dev"]),
-    "dfc_append_args": ("APPEND_ARGS", ["cache", "tokens", "k_dev", "v_dev", "k_src_stride", "v_src_stride", "slots",
-                                        "source_dtype", "q_heads", "q_dev", "q_out_dev", "q_stride", "q_out_stride",
-                                        "rot_dim", "interleaved", "max_positions", "positions", "rotary_dev",
-                                        "status_dev"]),
-    "dfc_attention_args": ("ATTENTION_ARGS", ["cache", "heads", "n_requests", "max_pages", "max_q_len", "tokens",
-                                              "q_dev", "out_dev", "q_stride", "out_stride", "lse_dev", "block_table",
-                                              "table_stride", "cu_q", "seq_lens", "scale", "causal", "window",
-                                              "workspace_dev", "workspace_bytes", "status_dev"]),
-}
-ARRAYS = {"k_stride": 3, "v_stride": 3, "k_src_stride": 2, "v_src_stride": 2, "q_stride": 2, "q_out_stride": 2,
-          "out_stride": 2, "cache": 13}
+torch = pytest.importorskip("torch")
+U32, U64, I64, PTR = ctypes.c_uint32, ctypes.c_uint64, ctypes.c_int64, ctypes.c_void_p
 
 
-@pytest.mark.parametrize("name", sorted(FIELDS))
-def test_layout(name, tmp_path):
-    paged = pytest.importorskip("lossless_entropy_coded_dfc_amd.paged")
-    packer, fields = FIELDS[name]
-    packer = getattr(paged, packer)
-    lines = "\n".join(f'printf("%zu %zu\\n", offsetof({name}, {f}), sizeof(x.{f}));' for f in fields)
-    src = tmp_path / "layout.c"
-    src.write_text(f"#include <stdio.h>\n#include \"dfc.h\"\n"
-                   f"int main(void) {{ {name} x; (void)x; {lines}\n printf(\"%zu 0\\n\", sizeof(x)); return 0; }}\n")
-    exe = tmp_path / "layout"
-    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(ROOT, "include"), str(src), "-o", str(exe)], check=True)
-    rows = [tuple(map(int, line.split())) for line in
-            subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()]
-    assert packer.size == rows[-1][0]
-    # one field at a time: its value lands at its offset and nowhere else
-    values = len(packer.unpack(bytes(packer.size)))
-    at = 0
-    for field, (offset, size) in zip(fields, rows):
-        for k in range(ARRAYS.get(field, 1)):
-            mark = [0] * values
-            mark[at] = 1
-            data = packer.pack(*mark)
-            places = [i for i, b in enumerate(data) if b]
-            assert all(offset <= i < offset + size for i in places), field
-            if field not in ("cache", "scale"):
-                assert places == [offset + k * size // ARRAYS.get(field, 1)], field
-            at += 1
-    assert at == values
+class Cache(ctypes.Structure):
+    _fields_ = [("k_dev", PTR), ("v_dev", PTR), ("k_stride", I64 * 3), ("v_stride", I64 * 3), ("n_pages", U32),
+                ("page_size", U32), ("kv_heads", U32), ("head_dim", U32), ("dtype", U32)]
+
+
+class Attention(ctypes.Structure):
+    _fields_ = [("cache", Cache), ("heads", U32), ("n_requests", U32), ("max_pages", U32), ("max_q_len", U32),
+                ("tokens", U64), ("q_dev", PTR), ("out_dev", PTR), ("q_stride", I64 * 2), ("out_stride", I64 * 2),
+                ("lse_dev", PTR), ("block_table", PTR), ("table_stride", I64), ("cu_q", PTR), ("seq_lens", PTR),
+                ("scale", ctypes.c_float), ("causal", U32), ("window", U32), ("workspace_dev", PTR),
+                ("workspace_bytes", U64), ("status_dev", PTR)]
 
 
 def test_one_workspace_serves_every_window_and_layout():
     # The kernel's shape follows the window and the layouts; the bytes a call
-    # dfc_paged_attention_workspace gives are a matter of the sizes alone
-    import ctypes
-    import lossless_entropy_coded_dfc_amd as dfc
-    paged = pytest.importorskip("lossless_entropy_coded_dfc_amd.paged")
-    lib = paged._lib()
+    # asks for are a matter of the sizes alone
+    lib = dfc.library()
+    lib.dfc_paged_attention_workspace.argtypes = [ctypes.POINTER(Attention), ctypes.POINTER(U64)]
+    lib.dfc_paged_attention.argtypes = [ctypes.POINTER(Attention), PTR]
 
     def args(window, v_stride, dim, heads, n, tokens, width, hint):
         kv = 8
-        return paged.ATTENTION_ARGS.pack(256, 256, 16 * kv * dim, kv * dim, dim, *v_stride, 4096, 16, kv, dim, 0, heads,
-                                         n, width, hint, tokens, 256, 256, heads * dim, dim, heads * dim, dim, 0, 256,
-                                         width, 256, 256, 1.0, 1, window, 256, 0, 0)
+        plain = 16 * kv * dim, kv * dim, dim
+        cache = Cache(256, 256, (I64 * 3)(*plain), (I64 * 3)(*v_stride), 4096, 16, kv, dim, 0)
+        rows = (I64 * 2)(heads * dim, dim)
+        return Attention(cache, heads, n, width, hint, tokens, 256, 256, rows, rows, None, 256, width, 256, 256, 1.0, 1,
+                         window, 256, 0, None)
 
     def need(a):
-        out = ctypes.c_uint64()
+        out = U64()
         assert lib.dfc_paged_attention_workspace(a, ctypes.byref(out)) == 0
         return out.value
 
@@ -87,3 +55,16 @@ def test_one_workspace_serves_every_window_and_layout():
                 assert need(a) == most, (sizes, window, layout)
                 # no bytes given: refused before anything is launched
                 assert lib.dfc_paged_attention(a, None) == dfc.ESIZE, (sizes, window, layout)
+
+
+def test_refusals_without_a_device():
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    q, i, table = torch.zeros(1, 4, 64, dtype=torch.bfloat16), torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4).int()
+    for call in (lambda: dfc.paged_attention(q, k, k, table, torch.zeros(2).int(), i),
+                 lambda: dfc.paged_append(q[:, :2], q[:, :2], k, k, i.long()),
+                 lambda: dfc.paged_plan(i, i, table, i, torch.zeros(2).long(), 16, 1),
+                 lambda: dfc.paged_attention_workspace(q, k, k, table, i, i),
+                 lambda: dfc.paged_attention(None, k, k, table, i, i),
+                 lambda: dfc.paged_plan(i, i, table.tolist(), i, i, 16, 1)):
+        with pytest.raises(TypeError):
+            call()
