@@ -235,14 +235,28 @@ __device__ __forceinline__ void turn_inside(float (&x)[8], const float *cosines,
     }
 }
 
+// Eight values.  Past: they pass the L2 cache by, since nothing here reads them
+// again and what is left dirty in it is written back when the kernel ends
+// (300 tokens 4.0 us so and 4.2 otherwise, 1,000 6.7 and 7.6, 3,500 16.8 and
+// 18.5, 8,192 35.3-39.2 and 39.3-39.8; but 64 tokens 6.6 and 6.2).
+template <bool Past, typename E8, typename E>
+__device__ __forceinline__ void store8(E *at, const E8 &v) {
+    using U4 = __attribute__((ext_vector_type(4))) uint32_t;
+    U4 *to = reinterpret_cast<U4 *>(at);
+    if constexpr (Past)
+        __builtin_nontemporal_store(__builtin_bit_cast(U4, v), to);
+    else
+        *to = __builtin_bit_cast(U4, v);
+}
+
 // One thread takes two chunks of 8 values of one head of one token: those that
 // pair up half a rotation apart, elsewhere two that lie as far from each other
 // as the head's other threads reach.  Every value is read and written once.
 // Memory bound: 8,192 tokens of 32 + 8 heads of 128 in bfloat16 move 206 MB, in
-// 39 us (5.3 TB/s; one chunk a thread, and with it every rotated value read
-// twice, 52 us).  64 tokens from float32 take 6 us, a launch and one chain of
+// 35.5-39 us (5.3-5.8 TB/s; one chunk a thread, and with it every rotated value
+// read twice, took 52).  64 tokens from float32 take 6 us, a launch and one chain of
 // loads.
-template <typename S, typename E>
+template <typename S, typename E, bool Past>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     using E8 = __attribute__((ext_vector_type(8))) E;
     const dfc_append_args &a = p.a;
@@ -302,17 +316,21 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     E8 out;
 #pragma unroll
     for (int i = 0; i < 8; ++i) out[i] = E(x[i]);
-    *reinterpret_cast<E8 *>(dst + 8u * c0) = out;
+    store8<Past>(dst + 8u * c0, out);
     if (two) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) out[i] = E(y[i]);
-        *reinterpret_cast<E8 *>(dst + 8u * c1) = out;
+        store8<Past>(dst + 8u * c1, out);
     }
 }
 
 template <typename S, typename E>
 void launch_append(const AppendArgs &p, uint32_t blocks, hipStream_t stream) {
-    hipLaunchKernelGGL((append_kernel<S, E>), dim3(blocks), dim3(256), 0, stream, p);
+    // 32 bytes a thread
+    if (p.threads * 32u > (2u << 20))
+        hipLaunchKernelGGL((append_kernel<S, E, true>), dim3(blocks), dim3(256), 0, stream, p);
+    else
+        hipLaunchKernelGGL((append_kernel<S, E, false>), dim3(blocks), dim3(256), 0, stream, p);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
