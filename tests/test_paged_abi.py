@@ -1,6 +1,8 @@
 """The paged cache's entry points where no GPU is needed: the workspace's size
 through the C ABI, and the Python binding's refusals."""
 import ctypes
+import os
+import subprocess
 
 import pytest
 
@@ -21,6 +23,22 @@ class Attention(ctypes.Structure):
                 ("lse_dev", PTR), ("block_table", PTR), ("table_stride", I64), ("cu_q", PTR), ("seq_lens", PTR),
                 ("scale", ctypes.c_float), ("causal", U32), ("window", U32), ("workspace_dev", PTR),
                 ("workspace_bytes", U64), ("status_dev", PTR)]
+
+
+@pytest.mark.parametrize("name,mirror", [("dfc_paged_cache", Cache), ("dfc_attention_args", Attention)])
+def test_layout(name, mirror, tmp_path):
+    # the structures above against the C compiler's
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    fields = [f[0] for f in mirror._fields_]
+    lines = "\n".join(f'printf("%zu %zu\\n", offsetof({name}, {f}), sizeof(x.{f}));' for f in fields)
+    src, exe = tmp_path / "layout.c", tmp_path / "layout"
+    src.write_text(f"#include <stddef.h>\n#include <stdio.h>\n#include \"dfc.h\"\n"
+                   f"int main(void) {{ {name} x; (void)x; {lines}\n printf(\"%zu 0\\n\", sizeof(x)); return 0; }}\n")
+    subprocess.run(["gcc", "-std=c99", "-I", os.path.join(root, "include"), str(src), "-o", str(exe)], check=True)
+    got = [tuple(map(int, line.split())) for line in
+           subprocess.run([str(exe)], check=True, capture_output=True, text=True).stdout.splitlines()]
+    assert got[-1][0] == ctypes.sizeof(mirror)
+    assert got[:-1] == [(getattr(mirror, f).offset, getattr(mirror, f).size) for f in fields]
 
 
 def test_one_workspace_serves_every_window_and_layout():
