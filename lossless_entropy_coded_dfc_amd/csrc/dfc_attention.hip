@@ -385,10 +385,11 @@ struct Loader {
     const int32_t *table;
     int32_t hi;
     uint32_t gtid, row, chunk;                     // of the thread's first piece
-    uint32_t n_pages, page_shift, page_most;       // page_most: the largest page seen
+    uint32_t n_pages, page_shift;
     uint32_t k_page, k_slot, v_page, v_slot;       // strides in pieces
     bool whole_dim, same;
     int32_t pages[NL];
+    bool absent, missing;                          // a page that is none of the cache's: under way, ever (wavefront)
     uint4 kr[NL], vr[NL];
 
     __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t rw) {
@@ -404,26 +405,30 @@ struct Loader {
         hi = w.hi;
         n_pages = a.n_pages;
         page_shift = a.page_shift;
-        page_most = 0;
+        absent = missing = false;
     }
 
     // The block table's entries for the thread's rows of the tile at `start`
     // (the piece's last row stands for those past it): read a tile ahead of
     // the load that uses them.
+    __device__ __forceinline__ int32_t page_of(int32_t start, int n) const {
+        return table[min(start + int32_t(row) + n * kStep, hi - 1) >> page_shift];
+    }
     __device__ __forceinline__ void fetch_pages(int32_t start) {
 #pragma unroll
-        for (int n = 0; n < NL; ++n) pages[n] = table[min(start + int32_t(row) + n * kStep, hi - 1) >> page_shift];
+        for (int n = 0; n < NL; ++n) pages[n] = page_of(start, n);
     }
 
     // A page that is none of the cache's is noted and the last one read in
-    // its place; rows past the piece are read, from a page of the request, and
-    // left out by put().
+    // its place, for an address that exists; rows past the piece are read, from
+    // a page of the request.  put() leaves both out.
     __device__ __forceinline__ void load(int32_t start) {
         const uint32_t page_mask = (1u << page_shift) - 1u;
+        uint32_t most = 0;
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const uint32_t in_page = (uint32_t(start) + row + uint32_t(n * kStep)) & page_mask;
-            page_most = max(page_most, uint32_t(pages[n]));
+            most = max(most, uint32_t(pages[n]));
             const uint32_t page = min(uint32_t(pages[n]), n_pages - 1u);
             const uint64_t at = uint64_t(page) * k_page + (uint64_t(in_page) * k_slot + chunk);
             kr[n] = *reinterpret_cast<const uint4 *>(kbase + at * 16u);
@@ -433,16 +438,20 @@ struct Loader {
                 vr[n] = *reinterpret_cast<const uint4 *>(
                     vbase + (uint64_t(page) * v_page + (uint64_t(in_page) * v_slot + chunk)) * 16u);
         }
+        absent = __any(most >= n_pages);
+        missing |= absent;
     }
-    __device__ __forceinline__ bool missing() const { return page_most >= n_pages; }
 
-    // Into LDS; rows past the piece and columns past the head become zeros.
+    // Into LDS; rows past the piece, columns past the head and pages that are
+    // none of the cache's become zeros.
     __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, int32_t start) {
-        if (!whole_dim || start + KT > hi) {
+        if (!whole_dim || start + KT > hi || absent) {
             const bool in_dim = whole_dim || gtid % CPR == chunk;
 #pragma unroll
             for (int n = 0; n < NL; ++n) {
-                const uint32_t keep = in_dim && start + int32_t(row) + n * kStep < hi ? ~0u : 0u;
+                bool there = in_dim && start + int32_t(row) + n * kStep < hi;
+                if (absent) there = there && uint32_t(page_of(start, n)) < n_pages;  // (which ones: seldom asked)
+                const uint32_t keep = there ? ~0u : 0u;
                 kr[n].x &= keep, kr[n].y &= keep, kr[n].z &= keep, kr[n].w &= keep;
                 vr[n].x &= keep, vr[n].y &= keep, vr[n].z &= keep, vr[n].w &= keep;
             }
@@ -611,7 +620,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         x.template products<true, false, 1>(vt, p, kt, s, nothing);
     }
     const AttnArgs &b = again(a);
-    if (ld.missing() && b.status) atomicOr(b.status, kStatusCorrupt);
+    if (ld.missing && b.status) atomicOr(b.status, kStatusCorrupt);
     store<E, DP, KT, RW, KW>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 
@@ -743,7 +752,7 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     while (t < n) turn_without_rows();
     if (!second) __syncthreads();
     const AttnArgs &b = again(a);
-    if (ld.missing() && b.status) atomicOr(b.status, kStatusCorrupt);
+    if (ld.missing && b.status) atomicOr(b.status, kStatusCorrupt);
     store<E, DP, KT, 8, 1>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 

@@ -735,3 +735,47 @@ def test_a_captured_step_follows_the_lengths():
             at += c
         ctx.copy_(plan.seq_lens)
         cursor.copy_(plan.cursor)
+
+
+# ---------------------------------------------- pages that are not there
+
+# Tables so wide that a step of 130 tokens of 8 heads over 2 takes each tile
+# height (the keys a table has room for choose it); heads wider than 128 take
+# two of them.
+HEIGHTS = [(16, 128), (16384, 128), (65536, 128), (262144, 128), (16384, 64), (262144, 64), (65536, 80), (16, 200),
+           (262144, 256)]
+
+
+def run_with_pages(s, holes, window=0, last=50.0):
+    """The step with the table entries `holes` ((request, place): page) in
+    place of its own, over a cache whose last page nobody owns and holds
+    `last`.  Returns out, lse, the status."""
+    page = torch.full((1,) + tuple(s.k.shape[1:]), last, dtype=s.k.dtype)
+    k, v = (torch.cat([c, page]).cuda() for c in (s.k, s.v))
+    table = s.table.clone()
+    for (r, i), p in holes.items():
+        table[r, i] = p
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out, lse = dfc.paged_attention(s.q.cuda(), k, v, table.cuda(), s.cu.cuda(), s.lens.cuda(), window=window, lse=True,
+                                   status=status)
+    torch.cuda.synchronize()
+    return out, lse, int(status.item())
+
+
+@pytest.mark.parametrize("last", [50.0, float("nan")], ids=["finite", "nan"])
+@pytest.mark.parametrize("keys,dim", HEIGHTS)
+def test_pages_that_are_not_there_count_as_zeros(keys, dim, last):
+    s = Step([300, 90], [130, 1], 8, 2, dim, 16, torch.bfloat16, seed=30 + dim, extra_pages=keys // 16)
+    for absent in (-1, s.k.shape[0] + 1, 10 ** 6, -2 ** 31):
+        holes = {(0, 2): absent, (0, 11): absent, (0, 18): absent, (1, 5): absent}
+        say("absent pages", keys, dim, absent, last)
+        out, lse, status = run_with_pages(s, holes, last=last)
+        assert status == dfc.ECORRUPT
+        # the definition over a cache with a page of zeros there
+        z = Step.__new__(Step)
+        z.__dict__.update(s.__dict__)
+        zeros = torch.zeros((1,) + tuple(s.k.shape[1:]), dtype=s.k.dtype)
+        z.k, z.v, z.table = torch.cat([s.k, zeros]), torch.cat([s.v, zeros]), s.table.clone()
+        for r, i in holes:
+            z.table[r, i] = s.k.shape[0]
+        z.check(out, lse)
