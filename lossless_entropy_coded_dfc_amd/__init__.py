@@ -269,6 +269,19 @@ def _stream(stream):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
+def _allocating_for(stream):
+    """The context in which a call allocates what its work on ``stream`` (a
+    handle or None) writes.  torch hands out memory that the current stream's
+    earlier work may still use, and a given stream does not wait for that work:
+    so the given stream is the current one meanwhile."""
+    import contextlib
+    import torch
+    if stream is None or int(stream) == torch.cuda.current_stream().cuda_stream:
+        return contextlib.nullcontext()
+    # (ExternalStream makes a new stream of the handle 0, the default stream's)
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
+
+
 def _dev_ptr(t) -> int:
     if t is None:
         return 0

@@ -19,7 +19,7 @@ from typing import NamedTuple
 
 import torch
 
-from . import DfcLibraryMissing, _check, library
+from . import DfcLibraryMissing, _allocating_for, _check, library
 
 __all__ = ["PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace"]
 
@@ -52,10 +52,21 @@ def _load():
     return _paged
 
 
-def _keep(stream, *tensors):
-    """Tensors allocated here are used on the caller's stream."""
-    for t in tensors:
-        t.record_stream(torch.cuda.ExternalStream(int(stream), device=t.device))
+def _call(stream, given, entry, *args):
+    """An entry of the binding, which allocates the workspace and the results
+    that are not ``given``, with its work on ``stream``.  What was allocated
+    for another stream than the current one counts as used on the current one
+    too, where the caller goes on with it: its memory is not handed to the
+    other stream's later work while the current one may still read it."""
+    if stream is None:
+        return entry(*args, None)
+    current = torch.cuda.current_stream()
+    with _allocating_for(stream):
+        r = entry(*args, stream)
+    for t in r[1:]:
+        if t is not None and not any(t is g for g in given):
+            t.record_stream(current)
+    return r
 
 
 def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_size: int, tokens: int, out=None,
@@ -71,15 +82,11 @@ def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_siz
     the length of the slots and positions, at least the step's new tokens (the
     rest become -1 and 0).  ``out``: a ``PagedPlan`` to write into (a captured
     step's buffers; its cursor may not be ``cursor``).  Asynchronous."""
-    r = (_BIND or _load()).plan(context_lens, new_lens, block_table, free_pages, cursor, page_size, tokens, out, status,
-                                stream)
+    r = _call(stream, out or (), (_BIND or _load()).plan, context_lens, new_lens, block_table, free_pages, cursor, page_size,
+              tokens, out, status)
     if r[0]:
         _check(r[0], "dfc_paged_plan")
-    if out is not None:
-        return out
-    if stream is not None:
-        _keep(stream, *r[1:])
-    return PagedPlan(*r[1:])
+    return PagedPlan(*r[1:]) if out is None else out
 
 
 def paged_append(k, v, k_cache, v_cache, slots, q=None, q_out=None, positions=None, rotary=None,
@@ -92,11 +99,10 @@ def paged_append(k, v, k_cache, v_cache, slots, q=None, q_out=None, positions=No
     by its token's ``positions`` (int32) first, and so is ``q`` (tokens,
     heads, head_dim); the rotated q, in the cache's type, is returned
     (``q_out``, or a new tensor).  Asynchronous."""
-    r = (_BIND or _load()).append(k, v, k_cache, v_cache, slots, q, q_out, positions, rotary, interleaved, status, stream)
+    r = _call(stream, (q_out,), (_BIND or _load()).append, k, v, k_cache, v_cache, slots, q, q_out, positions, rotary,
+              interleaved, status)
     if r[0]:
         _check(r[0], "dfc_paged_append")
-    if stream is not None and q is not None and q_out is None:
-        _keep(stream, r[1])
     return r[1]
 
 
@@ -122,19 +128,8 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: flo
     a device uint8 tensor of at least ``paged_attention_workspace`` bytes that
     nothing else uses until the call's work has run (None: allocated here).
     Returns out, or (out, lse).  Asynchronous."""
-    made = []  # here, and used on the caller's stream
-    if stream is not None and workspace is None:
-        workspace = torch.empty(paged_attention_workspace(q, k_cache, v_cache, block_table, cu_q, seq_lens, max_q_len),
-                                dtype=torch.uint8, device=q.device)
-        made.append(workspace)
-    r = (_BIND or _load()).attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale, causal, window, max_q_len,
-                                     out, lse, workspace, status, stream)
+    r = _call(stream, (out, lse), (_BIND or _load()).attention, q, k_cache, v_cache, block_table, cu_q, seq_lens, scale,
+              causal, window, max_q_len, out, lse, workspace, status)
     if r[0]:
         _check(r[0], "dfc_paged_attention")
-    if stream is not None:
-        if out is None:
-            made.append(r[1])
-        if lse is True:
-            made.append(r[2])
-        _keep(stream, *made)
     return r[1] if r[2] is None else r[1:]

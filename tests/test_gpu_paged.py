@@ -779,3 +779,80 @@ def test_pages_that_are_not_there_count_as_zeros(keys, dim, last):
         for r, i in holes:
             z.table[r, i] = s.k.shape[0]
         z.check(out, lse)
+
+
+# ------------------------------------------------- streams and allocations
+
+def pool_of(t):
+    """The stream (handle) from whose memory torch took a tensor."""
+    at = t.untyped_storage().data_ptr()
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= at < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not torch's memory")
+
+
+def reserved(handle):
+    return sum(s["total_size"] for s in torch.cuda.memory_snapshot() if s["stream"] == handle)
+
+
+def a_step(s, free, cursor, stream, current):
+    """Plan, append and attention with results that the calls allocate, their
+    work on `stream` (a handle or None)."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    t, (n, heads, dim), kv_heads = s.table.cuda(), s.q.shape, s.k.shape[2]
+    q, k, v = (torch.randn(n, h, dim, generator=g, device="cuda") for h in (heads, kv_heads, kv_heads))
+    angle = torch.randn(2048, dim, generator=g, device="cuda")
+    held = (s.lens - torch.tensor(s.new, dtype=torch.int32)).cuda()
+    new, kc, vc = torch.tensor(s.new, dtype=torch.int32, device="cuda"), *(torch.cat([c, c]).cuda()
+                                                                                  for c in (s.k, s.v))
+    torch.cuda.synchronize()
+    p = dfc.paged_plan(held, new, t, free, cursor, s.page, n, stream=stream)
+    r = dfc.paged_append(k, v, kc, vc, p.slots, q=q, positions=p.positions, rotary=angle, stream=stream)
+    torch.cuda.empty_cache()
+    before = reserved(current)
+    out, lse = dfc.paged_attention(r, kc, vc, t, p.cu_q, p.seq_lens, lse=True, stream=stream)
+    # neither the results nor the workspace come from elsewhere
+    if stream is not None and stream != current:
+        assert reserved(current) == before
+    torch.cuda.synchronize()
+    return [*p, r, out, lse]
+
+
+@pytest.mark.parametrize("given", ["another stream", "the default stream", "the current stream"])
+def test_what_a_call_allocates_belongs_to_its_stream(given):
+    # a given stream does not wait for the current one, whose earlier work may
+    # still use memory that torch hands out on the current stream
+    s = Step([900, 20, 300], [700, 1, 33], 32, 8, 128, 16, torch.bfloat16, seed=40, extra_pages=60)
+    n = s.k.shape[0]
+    free, cursor = torch.arange(n, 2 * n, dtype=torch.int32, device="cuda"), torch.tensor([0, n], device="cuda")
+    say("allocations", given)
+    torch.cuda.empty_cache()
+    plain = a_step(s, free, cursor, None, 0)
+    side = torch.cuda.Stream()
+    assert side.cuda_stream != 0 == torch.cuda.default_stream().cuda_stream
+    if given == "another stream":
+        got, handle = a_step(s, free, cursor, side.cuda_stream, 0), side.cuda_stream
+    elif given == "the default stream":
+        with torch.cuda.stream(side):
+            got, handle = a_step(s, free, cursor, 0, side.cuda_stream), 0
+    else:
+        with torch.cuda.stream(side):
+            got, handle = a_step(s, free, cursor, side.cuda_stream, side.cuda_stream), side.cuda_stream
+    assert torch.cuda.current_stream().cuda_stream == 0
+    for a, b in zip(plain, got):
+        assert pool_of(b) == handle
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
+
+
+def test_results_given_by_the_caller_stay_the_callers():
+    s = Step([140, 33], [67, 33], 8, 2, 128, 16, torch.bfloat16, seed=9)
+    q, k, v, table, cu, lens = s.q.cuda(), s.k.cuda(), s.v.cuda(), s.table.cuda(), s.cu.cuda(), s.lens.cuda()
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    say("results given, side stream")
+    r = dfc.paged_attention(q, k, v, table, cu, lens, out=out, lse=lse, stream=side.cuda_stream)
+    side.synchronize()
+    assert r[0] is out and r[1] is lse
+    s.check(out, lse)
