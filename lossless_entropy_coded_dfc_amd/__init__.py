@@ -269,17 +269,18 @@ def _stream(stream):
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
 
 
-def _allocating_for(stream):
+def _allocating_for(stream, device=None):
     """The context in which a call allocates what its work on ``stream`` (a
     handle or None) writes.  torch hands out memory that the current stream's
     earlier work may still use, and a given stream does not wait for that work:
     so the given stream is the current one meanwhile."""
     import contextlib
     import torch
-    if stream is None or int(stream) == torch.cuda.current_stream().cuda_stream:
+    if stream is None or int(stream) == torch.cuda.current_stream(device).cuda_stream:
         return contextlib.nullcontext()
     # (ExternalStream makes a new stream of the handle 0, the default stream's)
-    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device) if int(stream) else
+                             torch.cuda.default_stream(device))
 
 
 def _dev_ptr(t) -> int:
@@ -377,17 +378,17 @@ def encode_device(src, chunk_bytes: int = 0, lanes: int = 64, max_code_len: int 
     cap = encode_bound(n, p)
     wb = ctypes.c_uint64()
     _check(library().dfc_encode_device_workspace(n, ctypes.byref(wb)), "dfc_encode_device_workspace")
-    dst = torch.empty(cap, dtype=torch.uint8, device=src.device)
-    work = torch.empty(max(256, wb.value), dtype=torch.uint8, device=src.device)
+    with _allocating_for(stream, src.device):
+        dst = torch.empty(cap, dtype=torch.uint8, device=src.device)
+        # freed while the packing kernels may still run: to their own stream's memory
+        work = torch.empty(max(256, wb.value), dtype=torch.uint8, device=src.device)
     written = ctypes.c_uint64()
     _check(library().dfc_encode_device(ctypes.c_void_p(src.data_ptr() if n else 0), n, ctypes.byref(p),
                                        ctypes.byref(codebook) if codebook is not None else None,
                                        ctypes.c_void_p(dst.data_ptr()), cap, ctypes.c_void_p(work.data_ptr()),
                                        wb.value, ctypes.byref(written), _stream(stream)), "dfc_encode_device")
     if stream is not None:
-        # the packing kernels may still run on that stream: keep torch's
-        # allocator from handing the workspace to other streams' work first
-        work.record_stream(torch.cuda.ExternalStream(int(stream), device=src.device))
+        dst.record_stream(torch.cuda.current_stream(src.device))  # where the caller goes on with it
     return dst, written.value
 
 
@@ -418,11 +419,9 @@ def decode_gemm(blob_dev, info: Info, x, y, status=None, stream=None, tables=Non
         raise ValueError("x must be (B, K) 16-bit and y (B, M) float32 for the container's M x K")
     need = gemm_workspace_bytes(B, K)
     if workspace is None and need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
-        if stream is not None:
-            # the caching allocator must not hand this memory out before the
-            # call's work on that stream has run
-            workspace.record_stream(torch.cuda.ExternalStream(int(stream), device=x.device))
+        _dev_ptr(x)  # refused before anything is allocated
+        with _allocating_for(stream, x.device):
+            workspace = torch.empty(need, dtype=torch.uint8, device=x.device)
     if workspace is False or workspace is None:
         ws_ptr, ws_bytes = 0, 0
     else:
@@ -446,8 +445,12 @@ def derive_tables(blob_dev, info: Info, threads: int = 0, stream=None):
     the library's own) to pass as ``tables`` to the decoders.  Asynchronous."""
     import torch
     nbytes = derived_tables_bytes(info)
-    out = torch.empty(nbytes, dtype=torch.uint8, device=blob_dev.device)
-    _check(library().dfc_derive_tables(ctypes.c_void_p(_blob_ptr(blob_dev, info)), ctypes.byref(info), threads,
+    blob = _blob_ptr(blob_dev, info)
+    with _allocating_for(stream, blob_dev.device):
+        out = torch.empty(nbytes, dtype=torch.uint8, device=blob_dev.device)
+    if stream is not None:
+        out.record_stream(torch.cuda.current_stream(blob_dev.device))  # where the caller goes on with it
+    _check(library().dfc_derive_tables(ctypes.c_void_p(blob), ctypes.byref(info), threads,
                                        ctypes.c_void_p(out.data_ptr()), nbytes, _stream(stream)), "dfc_derive_tables")
     return out
 
