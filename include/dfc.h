@@ -503,8 +503,9 @@ typedef struct {
  * that sees no key gives 0 and an lse of -inf.  What a key or value that a
  * row does not see holds (inf and NaN included), and what lies in a page past
  * its request's tokens, has no influence on the row.  Pages outside the cache
- * count as zeros (DFC_ECORRUPT in the status).  Rows past cu_q[n_requests]
- * are not written.  Errors: DFC_EINVAL, DFC_ESIZE (workspace),
+ * count as zeros (DFC_ECORRUPT in the status if a row sees a key of them: the
+ * entries of pages that lie wholly behind every row's window may be anything).
+ * Rows past cu_q[n_requests] are not written.  Errors: DFC_EINVAL, DFC_ESIZE (workspace),
  * DFC_EUNSUPPORTED (types, head_dim over 256, tokens x heads / kv_heads past
  * 2^30, strides of the cache past 2^34), DFC_EHIP. */
 dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream);

@@ -465,6 +465,20 @@ struct Loader {
     }
 };
 
+// A page that is none of the cache's was read: told if a row sees a key of it.
+// The piece's first tile of keys may begin before every row's window, where a
+// request need not hold its pages any more.
+__device__ __forceinline__ void tell_missing(const AttnArgs &a, const Piece &w) {
+    int32_t lo, hi, first;
+    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, first);
+    const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
+    bool bad = false;
+    for (int32_t i = (max(first, w.lo) >> a.page_shift) + int32_t(threadIdx.x % kWave); i <= (w.hi - 1) >> a.page_shift;
+         i += int32_t(kWave))
+        bad |= uint32_t(table[i]) >= a.n_pages;
+    if (bad && a.status) atomicOr(a.status, kStatusCorrupt);
+}
+
 // The end of a workgroup of RW x KW wavefronts (along the rows, along the
 // keys): every wavefront's rows go to LDS, and the wavefronts of a row group
 // each write a share of its rows, joined over the key groups, so that stores
@@ -620,7 +634,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         x.template products<true, false, 1>(vt, p, kt, s, nothing);
     }
     const AttnArgs &b = again(a);
-    if (ld.missing && b.status) atomicOr(b.status, kStatusCorrupt);
+    if (ld.missing) tell_missing(b, w);
     store<E, DP, KT, RW, KW>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 
@@ -752,7 +766,7 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     while (t < n) turn_without_rows();
     if (!second) __syncthreads();
     const AttnArgs &b = again(a);
-    if (ld.missing && b.status) atomicOr(b.status, kStatusCorrupt);
+    if (ld.missing) tell_missing(b, w);
     store<E, DP, KT, 8, 1>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 

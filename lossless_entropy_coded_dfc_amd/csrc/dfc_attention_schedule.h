@@ -85,18 +85,19 @@ __device__ __forceinline__ Req request(const AttnArgs &a, uint32_t r, uint32_t &
     return q;
 }
 
-// Keys [lo, hi) that the rows row0 .. of a tile see between them, lo at a
-// multiple of the key tile.
-__device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint32_t row0, int32_t &lo, int32_t &hi) {
+// Keys [first, hi) that the rows row0 .. of a tile see between them, and lo,
+// first rounded down to a multiple of the key tile.
+__device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint32_t row0, int32_t &lo, int32_t &hi,
+                                          int32_t &first) {
     const int32_t t0 = int32_t(row0 / a.group);
     const int32_t rows = int32_t(min(a.rows_per_tile, uint32_t(q.q_len) * a.group - row0));
     const int32_t t1 = int32_t((row0 + uint32_t(rows) - 1) / a.group);
     const int64_t base = int64_t(q.kv_len) - q.q_len;
     const int64_t end = a.causal ? min(int64_t(q.kv_len), base + t1 + 1) : int64_t(q.kv_len);
-    int64_t begin = a.window ? max(int64_t(0), base + t0 + 1 - int64_t(a.window)) : 0;
-    begin = begin >> a.key_shift << a.key_shift;
+    const int64_t begin = a.window ? max(int64_t(0), base + t0 + 1 - int64_t(a.window)) : 0;
     hi = int32_t(max(end, int64_t(0)));
-    lo = int32_t(min(begin, int64_t(hi)));
+    first = int32_t(min(begin, int64_t(hi)));
+    lo = first >> a.key_shift << a.key_shift;
 }
 
 __device__ __forceinline__ uint32_t key_tiles(const AttnArgs &a, int32_t lo, int32_t hi) {
@@ -111,8 +112,8 @@ __device__ __forceinline__ void tiles_of(const AttnArgs &a, const Req &q, uint32
     n = (uint32_t(q.q_len) * a.group + a.rows_per_tile - 1u) >> a.rows_shift;
     c = 0;
     if (n) {
-        int32_t lo, hi;
-        tile_keys(a, q, (n - 1u) * a.rows_per_tile, lo, hi);
+        int32_t lo, hi, first;
+        tile_keys(a, q, (n - 1u) * a.rows_per_tile, lo, hi, first);
         c = key_tiles(a, lo, hi);
     }
 }
@@ -277,8 +278,8 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
     const uint32_t tile = within / parts;
     w.split = within - tile * parts;
     w.row0 = (n_tiles - 1u - tile) * a.rows_per_tile;
-    int32_t lo, hi;
-    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi);
+    int32_t lo, hi, seen;
+    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, seen);
     const uint32_t c = key_tiles(a, lo, hi);
     w.splits = min(parts, max(1u, ceil_of(c, piece)));
     w.slot = slot0 + tile * parts;

@@ -781,6 +781,27 @@ def test_pages_that_are_not_there_count_as_zeros(keys, dim, last):
         z.check(out, lse)
 
 
+@pytest.mark.parametrize("absent", [-1, 10 ** 6])
+@pytest.mark.parametrize("keys,dim", HEIGHTS)
+def test_pages_behind_the_window_may_be_gone(keys, dim, absent):
+    # pages that no row of the step sees: neither the result nor the status
+    # knows of them, wherever the window begins in a tile of keys
+    for window in (1, 20, 41, 100, 170):
+        s = Step([431, 290], [130, 1], 8, 2, dim, 16, torch.bfloat16, seed=50 + window, extra_pages=keys // 16)
+        holes = {}
+        for r, (t, n) in enumerate(zip(s.total, s.new)):
+            gone = max(0, t - n + 1 - window) // 16
+            assert gone > 0
+            holes.update({(r, i): absent for i in range(gone)})
+        say("behind the window", keys, dim, absent, window)
+        out, lse, status = run_with_pages(s, holes, window, last=float("nan"))
+        assert status == 0, window
+        s.check(out, lse, window=window)
+        # one page further some row sees a key
+        holes[(1, max(0, s.total[1] - window) // 16)] = absent
+        assert run_with_pages(s, holes, window)[2] == dfc.ECORRUPT
+
+
 # ------------------------------------------------- streams and allocations
 
 def pool_of(t):
