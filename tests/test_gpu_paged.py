@@ -737,7 +737,7 @@ def test_a_captured_step_follows_the_lengths():
         cursor.copy_(plan.cursor)
 
 
-# ---------------------------------------------- pages that are not there
+# ------------------------------------------------------- scores far apart
 
 # Tables so wide that a step of 130 tokens of 8 heads over 2 takes each tile
 # height (the keys a table has room for choose it); heads wider than 128 take
@@ -745,6 +745,57 @@ def test_a_captured_step_follows_the_lengths():
 HEIGHTS = [(16, 128), (16384, 128), (65536, 128), (262144, 128), (16384, 64), (262144, 64), (65536, 80), (16, 200),
            (262144, 256)]
 
+
+def far_apart(s, seed):
+    """Small whole numbers for q and k: scores before the scale are whole, exact
+    in fp32, and with a scale of 1024 those that are not a row's largest weigh
+    nothing.  Returns the largest score, how many keys have it, and the mean of
+    their values and of their magnitudes, by integers."""
+    rng = np.random.default_rng(seed)
+    q = rng.integers(-2, 3, s.q.shape)
+    s.q = torch.from_numpy(q).to(s.q.dtype)
+    tops, counts, means, spreads = [], [], [], []
+    for r, n in enumerate(s.total):
+        heads, kv_heads, dim = s.q.shape[1], s.k.shape[2], s.k.shape[3]
+        k = rng.integers(-2, 3, (n, kv_heads, dim))
+        k[n // 3] = k[n // 2]  # two keys of one score
+        for j in range(n):
+            s.k[s.table[r, j // s.page], j % s.page] = torch.from_numpy(k[j]).to(s.k.dtype)
+        v = op.gather(as64(s.v), s.table[r].numpy(), s.page, n)
+        for i in range(s.new[r]):
+            seen = n - s.new[r] + i + 1
+            for h in range(heads):
+                z = k[:seen, h * kv_heads // heads] @ q[int(s.cu[r]) + i, h]
+                best = v[:seen, h * kv_heads // heads][z == z.max()]
+                tops.append(z.max())
+                counts.append(len(best))
+                means.append(best.mean(0))
+                spreads.append(np.abs(best).mean(0))
+    shape = s.q.shape[:2]
+    return (*(np.array(x).reshape(shape) for x in (tops, counts)),
+            *(np.array(x).reshape(s.q.shape) for x in (means, spreads)))
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("keys,dim", HEIGHTS)
+def test_scores_of_tens_of_thousands(keys, dim, dtype):
+    s = Step([300, 90], [130, 1], 8, 2, dim, 16, dtype, seed=60 + dim, extra_pages=keys // 16)
+    top, count, mean, spread = far_apart(s, dim)
+    scale = 1024.0
+    assert np.abs(top).max() * scale > 30000
+    say("scores of tens of thousands", keys, dim, dtype)
+    out, lse = s.run(scale=scale)
+    # one rounding of the weights and one of the output, u each, and sums in
+    # fp32; a weight's exponent is rounded to 2^-24 of the score, but all
+    # weights that are not 0 are equal, so that it leaves the mean
+    bound = (2 * U[dtype] + 2.0 ** -15) * spread + 2.0 ** -24
+    assert (np.abs(as64(out) - mean) <= bound).all(), np.abs(as64(out) - mean).max()
+    assert (np.abs(mean) > 4 * bound).mean() > 0.9  # the bound tells a wrong row
+    ref = scale * top + np.log(count)
+    assert (np.abs(as64(lse) - ref) <= 2.0 ** -22 * scale * np.abs(top) + 2.0 ** -20).all()
+
+
+# ---------------------------------------------- pages that are not there
 
 def run_with_pages(s, holes, window=0, last=50.0):
     """The step with the table entries `holes` ((request, place): page) in
