@@ -1,6 +1,6 @@
 """Build libdfc.so in place (host codec with g++, gfx950 kernels with hipcc),
-_paged.so, the paged cache's binding to torch's tensors (g++), and
-libdfc_probe.so, the benchmark's streaming-ceiling kernel.
+_paged.so, the paged cache's binding to torch's tensors (g++; left out where
+torch or Python's headers are missing), and libdfc_probe.so, the benchmark's streaming-ceiling kernel.
 
 Usage: python -m lossless_entropy_coded_dfc_amd.csrc.build [-v]
 """
@@ -47,17 +47,31 @@ def _run(cmd, verbose):
 
 
 def _build_bind(verbose):
+    """_paged.so, where there is what it is built against: the codec needs
+    neither torch nor Python's headers, and its build goes on without them (the
+    paged cache's entry points then say what is missing)."""
     import sysconfig
-    import torch
+    try:
+        import torch
+    except ImportError:
+        return _no_bind("torch cannot be imported")
     base = os.path.dirname(torch.__file__)
     include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                sysconfig.get_paths()["include"]]
+    for folder, header in ((include[0], "ATen/core/Tensor.h"), (include[2], "Python.h")):
+        if not os.path.exists(os.path.join(folder, header)):
+            return _no_bind(f"{header} is not in {folder}")
     lib = os.path.join(base, "lib")
     tmp = BIND_OUT + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
           "-I", INCLUDE, *(x for i in include for x in ("-isystem", i)), os.path.join(HERE, "dfc_paged_bind.cpp"),
           "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
     os.replace(tmp, BIND_OUT)
+
+
+def _no_bind(why):
+    print(f"{os.path.basename(BIND_OUT)} (the paged cache's binding to torch) is not built: {why}", file=sys.stderr,
+          flush=True)
 
 
 def build(verbose: bool = False, out: str = OUT) -> str:
