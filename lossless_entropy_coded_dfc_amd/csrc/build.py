@@ -64,6 +64,7 @@ def _build_bind(verbose):
     lib = os.path.join(base, "lib")
     tmp = BIND_OUT + ".tmp"
     _run(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-Wall", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+          f"-DDFC_TORCH=\"{torch.__version__}\"",
           "-I", INCLUDE, *(x for i in include for x in ("-isystem", i)), os.path.join(HERE, "dfc_paged_bind.cpp"),
           "-o", tmp, "-L", lib, "-lc10", "-ltorch_cpu", "-ltorch_python", f"-Wl,-rpath,{lib}"], verbose)
     os.replace(tmp, BIND_OUT)

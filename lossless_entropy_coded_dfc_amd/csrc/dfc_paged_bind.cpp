@@ -431,4 +431,9 @@ PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, g_methods,
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__paged() { return PyModule_Create(&g_module); }
+PyMODINIT_FUNC PyInit__paged() {
+    PyObject *m = PyModule_Create(&g_module);
+    // the torch whose structures are compiled in: another's may differ
+    if (m && PyModule_AddStringConstant(m, "torch_version", DFC_TORCH) < 0) Py_CLEAR(m);
+    return m;
+}

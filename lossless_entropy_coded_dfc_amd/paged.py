@@ -44,6 +44,9 @@ def _load():
     except ImportError as e:
         raise DfcLibraryMissing(f"{os.path.join(os.path.dirname(__file__), '_paged.so')} cannot be loaded ({e}); run "
                                 "`python -c 'import __graft_entry__ as g; g.build()'`") from e
+    built = getattr(_paged, "torch_version", "of another build")
+    if built != torch.__version__:
+        raise DfcLibraryMissing(f"_paged.so is built against torch {built}, not {torch.__version__}; build it again")
     lib = library()
     _paged.setup(torch._C._cuda_getCurrentRawStream,
                  *(ctypes.cast(getattr(lib, name), ctypes.c_void_p).value for name in

@@ -44,3 +44,18 @@ def test_an_error_of_the_compiler_is_still_one(monkeypatch):
     monkeypatch.setattr(b, "_run", fails)
     with pytest.raises(subprocess.CalledProcessError):
         b._build_bind(False)
+
+
+def test_a_binding_of_another_torch_is_refused(monkeypatch):
+    # it reads tensors by that torch's structures
+    torch = pytest.importorskip("torch")
+    import lossless_entropy_coded_dfc_amd as dfc
+    from lossless_entropy_coded_dfc_amd import paged
+    monkeypatch.setattr(paged, "_BIND", None)
+    monkeypatch.setattr(torch, "__version__", "1.0.0")
+    x = torch.zeros(1, dtype=torch.int32)
+    with pytest.raises(dfc.DfcLibraryMissing, match="1.0.0"):
+        dfc.paged_plan(x, x, x, x, x, 16, 1)
+    monkeypatch.undo()
+    with pytest.raises(TypeError):  # (this torch's: as far as the arguments)
+        dfc.paged_plan(x, x, x[None], x, x, 16, 1)
