@@ -12,6 +12,7 @@
 #include <ATen/core/Tensor.h>
 #include <ATen/detail/CUDAHooksInterface.h>
 #include <ATen/ops/empty.h>
+#include <c10/core/GradMode.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <cmath>
@@ -47,9 +48,22 @@ decltype(&dfc_paged_append) g_append;
 decltype(&dfc_paged_attention) g_attention;
 decltype(&dfc_paged_attention_workspace) g_workspace;
 
+// None of the operators has a backward pass: a tensor that asks for one is
+// refused, or its gradient would be lost without a word.
 const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) type_error("%s must be a tensor", name);
-    return THPVariable_Unpack(o);
+    const at::Tensor &t = THPVariable_Unpack(o);
+    if (t.requires_grad() && c10::GradMode::is_enabled())
+        value_error("%s requires a gradient, which the paged cache's operators do not compute: detach it, or call under "
+                    "torch.no_grad()",
+                    name);
+    return t;
+}
+
+// A given tensor that the call writes: autograd is told, so that it does not
+// use a value saved before as if it still stood.
+void written(const at::Tensor &t) {
+    if (!t.is_inference()) t.unsafeGetTensorImpl()->bump_version();
 }
 
 int64_t integer(PyObject *o, const char *name) {
@@ -154,6 +168,7 @@ uint32_t *status_of(PyObject *o, int64_t dev) {
     const at::Tensor &t = tensor(o, "status");
     if (!on(t, dev) || t.element_size() != 4 || t.numel() < 1)
         value_error("status must be a device tensor of at least one 32-bit element");
+    written(t);
     return static_cast<uint32_t *>(t.data_ptr());
 }
 
@@ -274,13 +289,14 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             t[3] = part(all, at::kInt, 2 * wide + 2 * n + 1, tokens);
         } else {
             if (!PyTuple_Check(a[7]) || PyTuple_GET_SIZE(a[7]) != 5) type_error("out must be a PagedPlan");
-            for (int i = 0; i < 5; ++i) t[i] = tensor(PyTuple_GET_ITEM(a[7], i), "a field of out");
+            for (int i = 0; i < 5; ++i) written(t[i] = tensor(PyTuple_GET_ITEM(a[7], i), "a field of out"));
         }
         p.seq_lens = vector<int32_t>(t[0], at::kInt, n, dev, "the plan's seq_lens");
         p.cu_q = vector<int32_t>(t[1], at::kInt, n + 1, dev, "the plan's cu_q");
         p.slots = vector<int64_t>(t[2], at::kLong, tokens, dev, "the plan's slots");
         p.positions = vector<int32_t>(t[3], at::kInt, tokens, dev, "the plan's positions");
         p.cursor_out = vector<int64_t>(t[4], at::kLong, 2, dev, "the plan's cursor");
+        written(table);
         return answer(call(g_plan, p, stream_of(a[9], dev)), t);
     });
 }
@@ -290,11 +306,12 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
         want(n_args, 12);
-        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v"), &kc = tensor(a[2], "k_cache");
+        const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
+        const at::Tensor &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache");
         const int64_t dev = device_of(kc, "k_cache");
         dfc_append_args p;
         std::memset(&p, 0, sizeof(p));
-        cache_of(kc, tensor(a[3], "v_cache"), dev, p.cache);
+        cache_of(kc, vc, dev, p.cache);
         const at::ScalarType source = k.scalar_type(), type = kc.scalar_type();
         if (source != at::kFloat && source != type) type_error("k and v must be float32 or of the cache's type");
         const int64_t tokens = k.dim() ? k.size(0) : 0, dim = p.cache.head_dim;
@@ -312,6 +329,7 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             p.q_dev = rows(q, "q", source, q.sizes(), dev, p.q_stride);
             out[0] = a[6] == Py_None ? make(q.sizes(), type, q) : tensor(a[6], "q_out");
             p.q_out_dev = rows(out[0], "q_out", type, q.sizes(), dev, p.q_out_stride);
+            written(out[0]);
         }
         if (a[8] != Py_None) {
             const at::Tensor &angles = tensor(a[8], "rotary");
@@ -326,6 +344,8 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         }
         p.interleaved = truth(a[9]) ? 1u : 0u;
         p.status_dev = status_of(a[10], dev);
+        written(kc);
+        written(vc);
         return answer(call(g_append, p, stream_of(a[11], dev)), out);
     });
 }
@@ -373,6 +393,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         at::Tensor t[2];  // out, lse
         t[0] = a[10] == Py_None ? make(shape, type, q) : tensor(a[10], "out");
         p.out_dev = rows(t[0], "out", type, shape, dev, p.out_stride);
+        written(t[0]);
         if (a[11] == Py_True) {
             t[1] = make(shape.slice(0, 2), at::kFloat, q);
         } else if (a[11] != Py_None) {
@@ -381,7 +402,10 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
                 !t[1].is_contiguous())
                 type_error("lse must be a contiguous float32 tensor of shape (tokens, heads) on the call's device");
         }
-        if (t[1].defined()) p.lse_dev = static_cast<float *>(t[1].data_ptr());
+        if (t[1].defined()) {
+            written(t[1]);
+            p.lse_dev = static_cast<float *>(t[1].data_ptr());
+        }
         at::Tensor work;
         if (a[12] == Py_None) {
             uint64_t bytes = 0;
@@ -392,6 +416,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
             work = tensor(a[12], "workspace");
             if (!on(work, dev) || !work.is_contiguous())
                 type_error("workspace must be a contiguous tensor on the call's device");
+            written(work);
         }
         p.workspace_dev = work.data_ptr();
         p.workspace_bytes = uint64_t(work.nbytes());

@@ -6,6 +6,8 @@ A serving program whose products run on compressed weights
 lengths; per layer, ``paged_append`` rotates, rounds and stores the step's
 keys and values and ``paged_attention`` attends over everything stored.
 Lengths, tables and cursors stay on the device; nothing waits for the GPU.
+There is no backward pass: tensors that require a gradient are refused, unless
+gradients are off (``torch.no_grad()``).
 
 The checks of the arguments and their marshalling for the C ABI
 (``include/dfc.h``) are ``csrc/dfc_paged_bind.cpp``: done in Python, they take

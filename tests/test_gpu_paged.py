@@ -928,3 +928,57 @@ def test_results_given_by_the_caller_stay_the_callers():
     side.synchronize()
     assert r[0] is out and r[1] is lse
     s.check(out, lse)
+
+
+# ------------------------------------------------------------------ autograd
+
+def test_gradients_are_refused_and_writes_are_told():
+    s = Step([30, 7], [2, 1], 4, 2, 64, 16, torch.bfloat16, seed=70)
+    q, k, v, table, cu, lens = s.q.cuda(), s.k.cuda(), s.v.cuda(), s.table.cuda(), s.cu.cuda(), s.lens.cuda()
+    x, slots = torch.randn(3, 2, 64, device="cuda").bfloat16(), torch.arange(3, device="cuda")
+    angle, pos = torch.randn(4, 64, device="cuda"), torch.zeros(3, dtype=torch.int32, device="cuda")
+
+    def attention(**other):
+        a = dict(dict(q=q, k_cache=k, v_cache=v), **other)
+        return dfc.paged_attention(a.pop("q"), a.pop("k_cache"), a.pop("v_cache"), table, cu, lens, **a)
+
+    def append(**other):
+        a = dict(dict(k=x, v=x, k_cache=k.clone(), v_cache=v.clone(), q=q, rotary=angle), **other)
+        return dfc.paged_append(a.pop("k"), a.pop("v"), a.pop("k_cache"), a.pop("v_cache"), slots, positions=pos, **a)
+
+    say("gradients")
+    for call, names in ((attention, dict(q=q, k_cache=k, v_cache=v, out=q, lse=torch.empty(3, 4, device="cuda"))),
+                        (append, dict(k=x, v=x, k_cache=k, v_cache=v, q=q, q_out=q, rotary=angle))):
+        for name, t in names.items():
+            with pytest.raises(ValueError, match="gradient"):
+                call(**{name: t.clone().requires_grad_()})
+            with torch.no_grad():
+                got = call(**{name: t.clone().requires_grad_()})
+            assert not (got[0] if isinstance(got, tuple) else got).requires_grad or name in ("out", "q_out")
+    torch.cuda.synchronize()
+    # what a call writes in place: its version moves, what it reads does not
+    out, lse = torch.empty_like(q), torch.empty(3, 4, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    before = {n: t._version for n, t in dict(q=q, k=k, v=v, table=table, lens=lens).items()}
+    seen = [t._version for t in (out, lse, status)]
+    attention(out=out, lse=lse, status=status)
+    assert [t._version for t in (out, lse, status)] == [n + 1 for n in seen]
+    assert before == {n: t._version for n, t in dict(q=q, k=k, v=v, table=table, lens=lens).items()}
+    kept = (k.float() * 1.0).bfloat16().requires_grad_()
+    held = k.clone()
+    loss = (kept * held).sum()      # held is saved for the backward pass
+    append(k_cache=held, v_cache=v.clone())
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    with torch.inference_mode():
+        frozen = k.clone()
+    append(k_cache=frozen, v_cache=v.clone())   # outside the mode too
+    new = torch.ones(2, dtype=torch.int32, device="cuda")
+    free, cursor = torch.arange(10, dtype=torch.int32, device="cuda"), torch.tensor([0, 10], device="cuda")
+    at = table._version
+    p = dfc.paged_plan(lens, new, table, free, cursor, 16, 2)
+    assert table._version == at + 1
+    versions = [t._version for t in p]
+    dfc.paged_plan(lens, new, table, free, cursor, 16, 2, out=p)
+    assert [t._version for t in p] == [n + 1 for n in versions]
+    torch.cuda.synchronize()

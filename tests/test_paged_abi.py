@@ -86,3 +86,27 @@ def test_refusals_without_a_device():
                  lambda: dfc.paged_plan(i, i, table.tolist(), i, i, 16, 1)):
         with pytest.raises(TypeError):
             call()
+
+
+def test_tensors_that_require_a_gradient_are_refused():
+    # there is no backward pass; on the CPU the next refusal is the device's
+    k = torch.zeros(4, 16, 2, 64, dtype=torch.bfloat16)
+    x = torch.zeros(1, 2, 64, dtype=torch.bfloat16)
+    i, table, cu = torch.zeros(1, dtype=torch.int32), torch.zeros(1, 4).int(), torch.zeros(2).int()
+
+    def attention(q, kc, vc):
+        dfc.paged_attention(q, kc, vc, table, cu, i)
+
+    def append(kk, vv, kc, vc, q=None, rotary=None):
+        dfc.paged_append(kk, vv, kc, vc, i.long(), q=q, positions=i, rotary=rotary)
+
+    for call, args in ((attention, [x, k, k]), (append, [x, x, k, k])):
+        with pytest.raises(TypeError, match="device"):
+            call(*args)
+        for at in range(len(args) if call is append else 1):
+            wants = list(args)
+            wants[at] = args[at].clone().requires_grad_()
+            with pytest.raises(ValueError, match="gradient"):
+                call(*wants)
+            with torch.no_grad(), pytest.raises(TypeError, match="device"):
+                call(*wants)
