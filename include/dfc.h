@@ -433,7 +433,10 @@ typedef struct {
  * become -1 in the table and so do their tokens' slots (DFC_ESIZE in the
  * status, as for requests past max_pages and steps past `tokens`); negative
  * lengths count as 0 and a cursor that does not fit the ring as an empty one
- * (DFC_ECORRUPT).  Integers only: the result is exact.  Several workgroups
+ * (DFC_ECORRUPT).  A negative page is none: its tokens'
+ * slots become -1 (DFC_ESIZE for the ring's, DFC_ECORRUPT for the table's).  The
+ * plan knows no cache: pages past its end are told by the append and the
+ * attention.  Integers only: the result is exact.  Several workgroups
  * read the inputs while the outputs are written: cursor_out, seq_lens and
  * cu_q may not be the inputs themselves.  One launch.  Errors: DFC_EINVAL
  * (null pointers, page_size not a power of two, table_stride < max_pages, an
@@ -475,7 +478,8 @@ typedef struct {
     dfc_paged_cache cache;
     uint32_t heads;             /* query heads, a multiple of cache.kv_heads: head h reads cache head h / (heads / kv_heads) */
     uint32_t n_requests, max_pages;
-    uint32_t max_q_len;         /* a hint: the most new tokens a request has, 0 = unknown.  A wrong one costs time only */
+    uint32_t max_q_len;         /* a hint: the most new tokens a request has, 0 = unknown.  It decides the
+                                 * kernel's shape: a wrong one costs time, and any moves results within rounding */
     uint64_t tokens;            /* rows of q */
     const void *q_dev;          /* tokens x heads x head_dim in the cache's type, 16-byte aligned */
     void *out_dev;              /* the same shape and type */

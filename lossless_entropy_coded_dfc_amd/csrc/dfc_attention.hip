@@ -29,8 +29,11 @@
 // matrices 1.35 PFLOP/s).  One token a request: the bytes of K and V (64
 // requests of 1 to 8191: 212-217 us, 5.0-5.2 TB/s; 131072 keys in float16 106
 // us, 5.0 TB/s), for a short one latencies: launches, lengths, page, keys (700
-// keys 11.6 us).  Prompts: the two products (8192 tokens 548-566 us, 0.97-1.0
-// PFLOP/s; 512 tokens, a workgroup or two on each compute unit, 17 us).
+// keys 11.4 us).  Prompts: the two products (8192 tokens 550-600 us from box to
+// box, 0.92-1.0 PFLOP/s; 512 tokens, a workgroup or two on each compute unit,
+// 15-17 us).  Other heads have only been looked at: 64 ragged requests with
+// heads of 64, 80 and 256 take 130, 180 and 602 us (floors 107, 134 and 428),
+// prompts of 8192 349, 529 and 1864 (204, 255 and 815).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -98,7 +101,10 @@ __device__ __forceinline__ float other_half(float x) {
 // matrix instructions, so that a key that a row does not see takes no part at
 // all: for tiles in which such a key's value is not finite.  Lanes take keys
 // for the scores and columns for the sums.  The wavefront's keys are the
-// tiles of `kt` keys every `stride` from w.lo + first.
+// tiles of `kt` keys every `stride` from w.lo + first.  One after the other
+// these take long: one infinite value at token 1000 of a prompt of 2048 makes
+// 10 ms of 0.08, at token 4000 of 8192 42 ms of 0.6 (bfloat16, heads of 128),
+// before a window of 100,000 keys of a single token 0.75 ms of 0.11.
 template <typename E, int DP>
 __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t row_base,
                                                 uint32_t first, uint32_t stride, int kt, float *own, float *ml) {
@@ -321,8 +327,13 @@ struct Rows {
         }
     }
 
-    // Weights of a tile's scores, rounded; the sums move to a new reference
-    // where a row's maximum has left the slack.
+    // Weights of a tile's scores; the sums move to a new reference where a
+    // row's maximum has left the slack.  The sum takes the weights in 32 bits.
+    // The second product takes them rounded to the cache's type, since matrix
+    // instructions multiply 16 bits by 16: in two halves, 32 bits would cost it
+    // twice.  Against 64 bits the outputs are off by 0.0018-0.0022 in bfloat16
+    // and 0.0003 in float16 (root mean square, relative), where weights
+    // in 32 bits and one rounding of the output leave 0.0016-0.0017 and 0.0002.
     __device__ __forceinline__ void weights(const AttnArgs &a, int32_t start, bool masked, f32x16 (&s)[NB], V8 (&p)[NS]) {
         if (masked) {
             // seen: the keys see_lo .. see_lo + width - 1, in one comparison
@@ -653,13 +664,13 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
 // A half's loads of a tile leave the cache during its products and go to LDS
 // as its weights begin.
 //
-// Against the four-wavefront kernel's 128-row tiles: a prompt of 8192 tokens 549
-// and not 608 us, of 4100 193 and not 213.  The matrix units work 47% of the
-// time (1.0 PFLOP/s): a phase of products takes some 1,900 cycles where its 32
-// products take 1,024, since the reads of K and V (LDS gives 128 bytes a cycle
-// to eight wavefronts) and the loads issue beside them.  No part alone decides:
-// with its LDS reads left out the kernel takes 93% of the time, without its
-// loads 92%, without its exponentials 95%.
+// Against the four-wavefront kernel's 128-row tiles, on one box and in a graph:
+// a prompt of 8192 tokens 549 and not 608 us, of 4100 193 and not 213.  The
+// matrix units work 47% of the time: a phase of products takes some 1,900
+// cycles where its 32 products take 1,024, since the reads of K and V (LDS gives
+// 128 bytes a cycle to eight wavefronts) and the loads issue beside them.  No
+// part alone decides: with its LDS reads left out the kernel takes 93% of the
+// time, without its loads 92%, without its exponentials 95%.
 //
 // Products i read K tile i and V tile i - 1 in phases 2i and 2i + 1, so both
 // halves put tile i + 1 into LDS by the end of phase 2i + 1: K into the place
@@ -880,7 +891,11 @@ uint32_t workgroups_at_once(int dp, int rw) { return dp > 128 || rw == 8 ? 256u 
 // 1024, 2000, 4100: 11.1 / 12.8 / 16.5 / 19.7, 17.4 / 18.8 / 23.2 / 27.7, 40.0 /
 // 33.3 / 39.2 / 45.0, 98 / 79 / 72 / 76, 327 / 254 / 213 / 193; 256 tokens over
 // 2000: 43 / 42 / 63 / 70, 512 over 4000: 86 / 89 / 74 / 132, 256 over 32000: 274
-// / 224 / 183 / 166.)
+// / 224 / 183 / 166.)  The limits were measured with these heads and are used for
+// all.  The keys are those the table has room for, since the lengths are on the
+// device: under a table for 8192 tokens or more a prompt of 512 takes 28.4 and
+// not 16.1 us, of 200 16.7-19.5 and not 10.6, 64 single tokens over 700 49 and
+// not 40 (launch_plan leaves them to be split then).
 int tile_height(const dfc_attention_args &a) {
     const uint32_t group = a.heads / a.cache.kv_heads;
     const uint64_t most = most_rows(a);

@@ -126,10 +126,12 @@ __device__ __forceinline__ float wave_max(float x) {
 
 // L for up to 64 requests, one a lane: every lane tries one value, counts the
 // pieces p it makes and takes
-//     rounds (L + piece_cost), rounds = ceil(p heads / resident),
-// for its time; the least wins.  Cutting one long request into as many equal
-// pieces as run at once, cutting many ragged ones finer so that the last
-// round is full, and not cutting where it does not pay all come out of it.
+//     rounds (L + piece_cost + split_cost) + join_cost,
+//     rounds = ceil(p heads / resident),
+// for its time (the last two costs where something is split); the least wins.
+// Cutting one long request into as many equal pieces as run at once, cutting
+// many ragged ones finer so that the last round is full, and not cutting where
+// it does not pay all come out of it.
 // The wavefronts count a share of the requests each: one that counts all of
 // 64 takes 2 us, which the workgroups left without a piece spend as well.
 template <uint32_t NT>

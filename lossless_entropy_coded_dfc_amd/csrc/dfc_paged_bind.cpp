@@ -4,7 +4,7 @@
 //
 // The kernels of a decoding step run for 4 to 12 us.  Done in Python and ctypes
 // this took 9 to 11 us a call beside the launch's 3.6 (an append of 64 tokens
-// 12.8 us a call among others, now 5.3; one token over 700 16.3, now 11.8).
+// 12.8 us a call among others, now 5.2; one token over 700 16.3, now 11.4).
 // Nothing is computed here and nothing kept between calls.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>

@@ -7,7 +7,9 @@ lengths; per layer, ``paged_append`` rotates, rounds and stores the step's
 keys and values and ``paged_attention`` attends over everything stored.
 Lengths, tables and cursors stay on the device; nothing waits for the GPU.
 There is no backward pass: tensors that require a gradient are refused, unless
-gradients are off (``torch.no_grad()``).
+gradients are off (``torch.no_grad()``).  ``stream``: the handle of the stream
+that a call's work goes to (None: torch's current one); what the call allocates
+is that stream's memory.
 
 The checks of the arguments and their marshalling for the C ABI
 (``include/dfc.h``) are ``csrc/dfc_paged_bind.cpp``: done in Python, they take
@@ -87,8 +89,8 @@ def paged_plan(context_lens, new_lens, block_table, free_pages, cursor, page_siz
     the length of the slots and positions, at least the step's new tokens (the
     rest become -1 and 0).  ``out``: a ``PagedPlan`` to write into (a captured
     step's buffers; its cursor may not be ``cursor``).  Asynchronous."""
-    r = _call(stream, out or (), (_BIND or _load()).plan, context_lens, new_lens, block_table, free_pages, cursor, page_size,
-              tokens, out, status)
+    r = _call(stream, out or (), (_BIND or _load()).plan, context_lens, new_lens, block_table, free_pages, cursor,
+              page_size, tokens, out, status)
     if r[0]:
         _check(r[0], "dfc_paged_plan")
     return PagedPlan(*r[1:]) if out is None else out
@@ -127,8 +129,8 @@ def paged_attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale: flo
     ones included.  ``scale``: of the scores (None: head_dim ** -0.5).
     ``causal``: a token sees itself and what is before it.  ``window``: it
     sees that many at most (0: all).  ``max_q_len``: the most new tokens of a
-    request, if the caller knows (0: unknown; it decides the kernel's shape,
-    never its result).  ``lse``: a float32 (tokens, heads) tensor for the log
+    request, if the caller knows (0: unknown; it decides the kernel's shape
+    and so the result within rounding).  ``lse``: a float32 (tokens, heads) tensor for the log
     of every row's sum of exponentials, or True for a new one.  ``workspace``:
     a device uint8 tensor of at least ``paged_attention_workspace`` bytes that
     nothing else uses until the call's work has run (None: allocated here).
