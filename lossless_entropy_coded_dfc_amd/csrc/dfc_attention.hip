@@ -29,8 +29,8 @@
 // matrices 1.35 PFLOP/s).  One token a request: the bytes of K and V (64
 // requests of 1 to 8191: 212-217 us, 5.0-5.2 TB/s; 131072 keys in float16 106
 // us, 5.0 TB/s), for a short one latencies: launches, lengths, page, keys (700
-// keys 11.4 us).  Prompts: the two products (8192 tokens 550-600 us from box to
-// box, 0.92-1.0 PFLOP/s; 512 tokens, a workgroup or two on each compute unit,
+// keys 11.4 us).  Prompts: the two products (8192 tokens 550-600 us from card to
+// card, 0.92-1.0 PFLOP/s; 512 tokens, a workgroup or two on each compute unit,
 // 15-17 us).  Other heads have only been looked at: 64 ragged requests with
 // heads of 64, 80 and 256 take 130, 180 and 602 us (floors 107, 134 and 428),
 // prompts of 8192 349, 529 and 1864 (204, 255 and 815).
@@ -664,7 +664,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
 // A half's loads of a tile leave the cache during its products and go to LDS
 // as its weights begin.
 //
-// Against the four-wavefront kernel's 128-row tiles, on one box and in a graph:
+// Against the four-wavefront kernel's 128-row tiles, on one card and in a graph:
 // a prompt of 8192 tokens 549 and not 608 us, of 4100 193 and not 213.  The
 // matrix units work 47% of the time: a phase of products takes some 1,900
 // cycles where its 32 products take 1,024, since the reads of K and V (LDS gives
