@@ -520,6 +520,193 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream);
  * window, mask and strides. */
 dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_t *bytes);
 
+/* The same with sinks: a row also sees the first `sinks` tokens of its request,
+ * whatever the window, if they are before it (j < sinks beside j > p - window;
+ * with window == 0 they change nothing).  Keys between the sinks and the window
+ * are not read, and the entries of pages that lie wholly there may be anything
+ * (dfc_paged_release gives them back).  sinks == 0 is dfc_paged_attention.
+ * Errors as there, DFC_EINVAL for sinks past 2^31 - 1. */
+dfc_status dfc_paged_attention_sinks(const dfc_attention_args *args, uint32_t sinks, void *stream);
+
+/* Weights of the norms of the heads of q and of k: head_dim values each of
+ * type dtype (DFC_F32 or the cache's), 16-byte aligned; NULL: not normed.
+ * eps: added to the mean square, above 0 and finite. */
+typedef struct {
+    const void *q_norm_dev, *k_norm_dev;
+    uint32_t dtype;
+    float eps;
+} dfc_norm_args;
+
+/* dfc_paged_append with each head of k (and of q) normed before it is rotated:
+ * x becomes x w / sqrt(mean(x^2) + eps) over the head's head_dim values, in
+ * fp32 (the squares are summed in 64 bits), in the same pass and with the same
+ * single rounding.  norms NULL is dfc_paged_append.  q_out may be q only
+ * without rotation and norm.  Errors as there, DFC_EINVAL for the norms'
+ * pointers and eps, DFC_EUNSUPPORTED for their type. */
+dfc_status dfc_paged_append_normed(const dfc_append_args *args, const dfc_norm_args *norms, void *stream);
+
+/* Pages given back, shared and moved.  Beside the block tables and the ring of
+ * free pages, as dfc_paged_plan has them, a program that shares pages holds
+ * `shared`: for each of the cache's n_pages pages the number of requests that
+ * hold it beyond the first (0 for a page of one request and for a free one; a
+ * plan needs no word of it).  Zeros at first; from then on these calls keep it. */
+typedef struct {
+    uint32_t n_requests, max_pages; /* at most 65536 requests */
+    uint32_t page_size;             /* a power of two */
+    uint32_t n_ring, n_pages;       /* entries of free_pages and of shared */
+    uint32_t window, sinks;         /* window > 0: pages that no later token sees are given back too */
+    const int32_t *held_lens;       /* tokens each request holds (n_requests) */
+    const int32_t *keep_lens;       /* tokens of those it keeps */
+    int32_t *block_table;
+    int64_t table_stride;
+    int32_t *free_pages;            /* freed pages are written from the ring's tail on */
+    const int64_t *cursor;
+    int64_t *cursor_out;            /* out: the cursor with the tail moved on */
+    int32_t *shared;
+    uint32_t *workspace_dev;        /* DFC_RELEASE_WORKSPACE bytes, 16-byte aligned, that nothing else touches meanwhile */
+    uint32_t *status_dev;
+} dfc_release_args;
+enum { DFC_RELEASE_WORKSPACE = 4096 };
+
+/* Requests cut to their first keep_lens tokens (0: they end).  Request r gives
+ * up its entries ceil(keep / P) .. ceil(held / P) - 1 and, with a window, those
+ * of pages that lie wholly in [sinks, keep - window], which no token from
+ * position keep on sees.  Entries given up become -1; those that are negative
+ * already are passed over, so that a window's pages can be given back again and
+ * again.  A page that nobody holds any more is free: the call's free pages go
+ * to the ring in ascending order of their numbers, others count a holder less.
+ * In the status: DFC_ECORRUPT for lengths that are negative or keep more than
+ * is held (the request is passed over), pages past n_pages, pages given up more
+ * often than held (freed once), a cursor that does not fit the ring or a ring
+ * without room (nothing is written to the ring then); DFC_ESIZE for lengths past
+ * max_pages; DFC_EUNSUPPORTED for a request that is cut inside a page that
+ * others hold after the call: its next token would overwrite theirs (end such a
+ * request, and fork the part it is to keep).  Integers only, the same result on
+ * every run.  Errors: DFC_EINVAL (null pointers, page_size, table_stride <
+ * max_pages, an empty ring, n_pages 0 or past 2^30, cursor_out that is
+ * cursor), DFC_EUNSUPPORTED (more than 65536 requests), DFC_EHIP. */
+dfc_status dfc_paged_release(const dfc_release_args *args, void *stream);
+
+typedef struct {
+    uint32_t n_requests, max_pages; /* at most 65536 requests */
+    uint32_t page_size;
+    uint32_t n_ring, n_pages;
+    const int32_t *context_lens;    /* tokens each request holds (n_requests) */
+    const int32_t *parents;         /* the request that each becomes a copy of, -1: none */
+    const int32_t *fork_lens;       /* how many of the parent's first tokens; NULL: all of them */
+    int32_t *block_table;
+    int64_t table_stride;
+    const int32_t *free_pages;
+    const int64_t *cursor;
+    int64_t *cursor_out;
+    int32_t *shared;
+    int32_t *context_out;           /* out: tokens each request holds after the call */
+    int32_t *src, *dst;             /* out (n_requests): the page to copy for each request and where to, -1: none */
+    uint32_t *status_dev;
+} dfc_fork_args;
+
+/* Requests that hold nothing become copies of others' first tokens.  Full
+ * pages are shared (one holder more); a page that the copied tokens fill in
+ * part would be written by both, so the copy takes a page off the ring, in
+ * request order, and {src, dst} say what dfc_paged_copy has to copy before
+ * either is appended to.  Negative entries (pages given back behind a window)
+ * are copied as they are.  A request that cannot be forked keeps holding
+ * nothing, and neither table nor holders change for it: DFC_ECORRUPT in the
+ * status if it or its parent holds what it should not (a parent out of range or
+ * forked itself, a request that holds tokens, more tokens than the parent has,
+ * a page to copy that is none), DFC_ESIZE if the ring has no page or the row no
+ * room.  Entries past n_pages are copied as -1 (DFC_ECORRUPT).  Errors as
+ * dfc_paged_release; context_out may not be an input. */
+dfc_status dfc_paged_fork(const dfc_fork_args *args, void *stream);
+
+typedef struct {
+    uint32_t n_requests, max_pages;
+    uint32_t page_size;
+    uint32_t n_ring, n_pages;
+    const int32_t *context_lens;
+    int32_t *block_table;
+    int64_t table_stride;
+    int32_t *free_pages;
+    const int64_t *cursor;
+    int32_t *shared;
+    int32_t *src, *dst;             /* out (n_pages / 2 each): pages to copy, then -1 */
+    int32_t *used;                  /* out (1): pages held */
+    uint32_t *workspace_dev;        /* dfc_paged_compact_workspace(n_pages) bytes, 16-byte aligned */
+    uint32_t *status_dev;
+} dfc_compact_args;
+
+/* The held pages made dense.  Of the pages that are held (in the first
+ * ceil(context / P) entries of a row) or free (on the ring), in ascending order
+ * a_0 < a_1 < ..., U are held: those held beyond a_{U-1} move, in order, to the
+ * free ones up to it.  The tables, the holders and the ring (which then holds
+ * a_U, a_{U+1} ... in order; its cursor stays) are rewritten; {src, dst} say what
+ * dfc_paged_copy has to copy before the next step.  Sources and destinations are
+ * distinct.  Pages that are neither stay.  Where the ring and the tables
+ * contradict each other (a page twice on the ring, on it and held, or past
+ * n_pages, a cursor that does not fit) nothing moves and DFC_ECORRUPT is
+ * set; for lengths past max_pages DFC_ESIZE (the row's entries count).  Errors as
+ * dfc_paged_release. */
+dfc_status dfc_paged_compact(const dfc_compact_args *args, void *stream);
+uint64_t dfc_paged_compact_workspace(uint32_t n_pages);
+
+/* The K and V of page src[i] copied to page dst[i] in each of n_caches caches
+ * (host array; of one shape, strides and type), for every i < n with both not
+ * negative (device int32).  Destinations are distinct and no sources, or what
+ * they hold is unspecified.  Pages past the cache are passed over (DFC_ECORRUPT
+ * in the status).  Errors: DFC_EINVAL (null pointers, caches that differ),
+ * DFC_EUNSUPPORTED, DFC_EHIP. */
+dfc_status dfc_paged_copy(const dfc_paged_cache *caches, uint32_t n_caches, const int32_t *src, const int32_t *dst,
+                          uint32_t n, uint32_t *status_dev, void *stream);
+
+/* ------------------------------------------------------------------------
+ * The next tokens of a step from its logits (dfc_decode_gemm's of the
+ * vocabulary's matrix, among others). */
+typedef struct {
+    uint32_t n_requests, vocab;     /* at most 65536 requests; vocab 1 .. 2^30 */
+    uint64_t rows;
+    uint32_t dtype;                 /* of the logits, the drafter's too: DFC_F32, DFC_BF16 or DFC_F16 */
+    const void *logits_dev;         /* rows x vocab */
+    int64_t logits_stride;          /* elements from a row to the next, not below vocab */
+    const void *draft_logits_dev;   /* NULL, or rows x vocab: row i what draft i was drawn from */
+    int64_t draft_stride;
+    const int32_t *cu_rows;         /* request r's rows: cu_rows[r] .. cu_rows[r + 1] - 1 */
+    const int64_t *drafts;          /* rows: the token drafted to follow row i (a request's last entry is not read) */
+    const float *uniforms;          /* rows: random numbers in [0, 1) */
+    const float *temperature;       /* n_requests, or NULL: 1 */
+    int32_t *accepted;              /* out (n_requests): drafts that hold */
+    int64_t *tokens;                /* out (n_requests): the token that follows them, -1: none */
+    void *workspace_dev;            /* dfc_verify_workspace bytes, 256-byte aligned */
+    uint64_t workspace_bytes;
+    uint32_t *status_dev;
+} dfc_verify_args;
+
+/* Drafted tokens checked against the model's probabilities, so that what is
+ * answered is distributed as if each token had been drawn from the model.
+ * Request r has n rows of logits z and n - 1 drafts x: row i is the model's
+ * answer to the token before draft i.  With temperature T, p_i = softmax(z_i / T)
+ * and q_i = softmax(drafter's z_i / T), or without its logits 1 at x_i and 0
+ * elsewhere.  Draft i holds if all before it hold and u_i q_i(x_i) < p_i(x_i),
+ * u_i = uniforms[row i].  The token that follows the a drafts that hold is the
+ * first j with w_0 + ... + w_j > u (w_0 + w_1 + ...), u the uniform of the
+ * request's last row, w = max(p_a - q_a, 0) if draft a was refused (p_a where
+ * that is 0 everywhere) and p_a if there are no more.  One row and no draft: a
+ * token drawn from the logits.  T = 0: p is 1 at the lowest index of the
+ * largest logit, so a draft holds if it is that.  Logits of -inf have
+ * probability 0.  Exponentials, sums and comparisons are in 64 bits, whose
+ * roundings move the border between two tokens by some 1e-14.  A row that holds
+ * NaN or +inf or nothing above -inf, and a temperature that is negative or not
+ * finite, give no probabilities: no draft holds there and the token is -1
+ * (DFC_ECORRUPT in the status).  A draft outside the vocabulary does not hold
+ * (DFC_ECORRUPT).  Uniforms outside [0, 1) count as the nearest value in it, NaN
+ * as 0 for the token and as not holding for a draft.  A request without rows:
+ * 0 and -1.  Errors: DFC_EINVAL, DFC_ESIZE (workspace), DFC_EUNSUPPORTED
+ * (types, sizes), DFC_EHIP. */
+dfc_status dfc_verify_drafts(const dfc_verify_args *args, void *stream);
+
+/* Bytes of the workspace for those sizes (host; rows, vocab and n_requests
+ * and whether there are drafter's logits are read). */
+dfc_status dfc_verify_workspace(const dfc_verify_args *args, uint64_t *bytes);
+
 /* Human-readable name of a status code. */
 const char *dfc_status_str(dfc_status s);
 

@@ -24,6 +24,8 @@ __all__ = [
     "STORES_AUTO", "STORES_DEFERRED", "STORES_IMMEDIATE",
     "status_str", "MAX_BATCH", "derived_tables_bytes", "derive_tables",
     "PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace",
+    "PagedFork", "PagedMoves", "paged_release", "paged_fork", "paged_compact", "paged_copy",
+    "Verified", "verify_drafts", "verify_drafts_workspace",
 ]
 
 MAX_BATCH = 32
@@ -92,8 +94,10 @@ class BatchItem(ctypes.Structure):
 
 
 def __getattr__(name):
-    # the paged cache's entry points need torch, which the codec does not
-    if name in ("PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace"):
+    # the serving entry points need torch, which the codec does not
+    if name in ("PagedPlan", "paged_plan", "paged_append", "paged_attention", "paged_attention_workspace", "PagedFork",
+                "PagedMoves", "paged_release", "paged_fork", "paged_compact", "paged_copy", "Verified", "verify_drafts",
+                "verify_drafts_workspace"):
         from . import paged
         for entry in paged.__all__:
             globals()[entry] = getattr(paged, entry)

@@ -87,7 +87,7 @@ def build(verbose: bool = False, out: str = OUT) -> str:
         _run(["g++", *CXX_FLAGS, *inc, "-c", os.path.join(HERE, name + ".cpp"), "-o", obj], verbose)
         host_objs.append(obj)
     dev_objs = []
-    for name in ("dfc_decode", "dfc_ans", "dfc_gemm", "dfc_encode_gpu", "dfc_paged", "dfc_attention"):
+    for name in ("dfc_decode", "dfc_ans", "dfc_gemm", "dfc_encode_gpu", "dfc_paged", "dfc_attention", "dfc_pages", "dfc_verify"):
         obj = os.path.join(objdir, name + ".o")
         _run([hipcc, *HIP_FLAGS, *inc, "-c", os.path.join(HERE, name + ".hip"), "-o", obj], verbose)
         dev_objs.append(obj)

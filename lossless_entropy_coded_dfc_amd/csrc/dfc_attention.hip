@@ -2,7 +2,7 @@
 //
 // Token i of request r (n_r new tokens, s_r tokens in all) stands at position
 // p = s_r - n_r + i and sees the keys j < s_r with j <= p (causal) and
-// j > p - window.  For each of its heads, which share the keys and values of
+// j > p - window or j < sinks.  For each of its heads, which share the keys and values of
 // one cache head in groups of G = heads / kv_heads,
 //     o = sum_j exp(z_j - m) v_j / sum_j exp(z_j - m),  z_j = scale q . k_j,
 // in one pass over the keys: m is a running reference no smaller than the
@@ -105,7 +105,7 @@ __device__ __forceinline__ float other_half(float x) {
 // these take long: one infinite value at token 1000 of a prompt of 2048 makes
 // 10 ms of 0.08, at token 4000 of 8192 42 ms of 0.6 (bfloat16, heads of 128),
 // before a window of 100,000 keys of a single token 0.75 ms of 0.11.
-template <typename E, int DP>
+template <typename E, int DP, bool Sinks>
 __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t row_base,
                                                 uint32_t first, uint32_t stride, int kt, float *own, float *ml) {
     using V8 = __attribute__((ext_vector_type(8))) E;
@@ -121,17 +121,18 @@ __device__ __forceinline__ void rows_one_by_one(const AttnArgs &a, const Piece &
         if (row >= w.q_len * int32_t(a.group)) break;
         const int32_t tok = row / int32_t(a.group), g = row - tok * int32_t(a.group);
         const int32_t pos = w.kv_len - w.q_len + tok;
-        const int32_t see_hi = a.causal ? min(pos + 1, w.hi) : w.hi;
+        const int32_t end = end_of<Sinks>(a, w), see_hi = a.causal ? min(pos + 1, end) : end;
         const int32_t see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
         const E *qp = static_cast<const E *>(a.q) + int64_t(w.q_start + tok) * a.q_stride[0] +
                       int64_t(kvh * a.group + uint32_t(g)) * a.q_stride[1];
         float m = -INFINITY, l = 0.0f, o[NO] = {};
 #pragma unroll 1
-        for (int32_t start = w.lo + int32_t(first); start < w.hi; start += int32_t(stride)) {
-            const int32_t key = start + int32_t(lane);
+        for (int32_t at = w.lo + int32_t(first); at < w.hi; at += int32_t(stride)) {
+            const int32_t start = key_at<Sinks>(a, w, at), key = start + int32_t(lane);
+            const bool behind = key < see_lo && !(Sinks && key < a.sinks);
             int32_t page = -1;
-            if (int32_t(lane) < kt && key >= see_lo && key < see_hi) page = table[key >> a.page_shift];
-            const bool seen = int32_t(lane) < kt && key >= see_lo && key < see_hi;
+            if (int32_t(lane) < kt && !behind && key < see_hi) page = table[key >> a.page_shift];
+            const bool seen = int32_t(lane) < kt && !behind && key < see_hi;
             if (uint32_t(page) >= a.n_pages) page = -1;  // counts as zeros
             const uint32_t in_page = uint32_t(key & page_mask);
             float z = 0.0f;
@@ -197,7 +198,7 @@ constexpr auto nothing = [](int) {};  // no work beside the products
 
 // A wavefront's 32 rows: their queries, limits and running sums.  Lane l has
 // row l mod 32 (half l / 32 of its keys and columns).
-template <typename E, int DP, int KT>
+template <typename E, int DP, int KT, bool Sinks>
 struct Rows {
     using T = Type<E>;
     using V8 = typename T::V8;
@@ -206,7 +207,8 @@ struct Rows {
     V8 qf[NQ];
     f32x16 acc[ND];
     float m, l, slack;              // reference (raw scores); this lane's share of the sum
-    int32_t see_lo, see_hi;         // the keys of the row
+    int32_t see_lo, see_hi;         // the keys of the row,
+    int32_t sinks, see_sinks;       // and the first so many; those before see_hi
     int32_t hi_min, hi_max, lo_min, lo_max;  // over the wavefront's rows
     bool idle;                      // no rows
     uint32_t odd;                   // a tile with masked keys held a value that is not finite
@@ -219,7 +221,12 @@ struct Rows {
         const int32_t row_c = min(row, n_rows - 1);
         const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
         const int32_t pos = w.kv_len - w.q_len + tok;
-        see_hi = a.causal ? min(pos + 1, w.hi) : w.hi;
+        const int32_t end = end_of<Sinks>(a, w);
+        see_hi = a.causal ? min(pos + 1, end) : end;
+        if constexpr (Sinks) {
+            sinks = a.sinks;
+            see_sinks = max(min(sinks, see_hi), 0);
+        }
         see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
         // positions ascend with the row
         hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
@@ -259,9 +266,11 @@ struct Rows {
 
     // No row sees a key of the tile; some row does not see all of them.
     __device__ __forceinline__ bool skips(int32_t start) const {
-        return idle || start >= hi_max || start + KT <= lo_min;
+        return idle || start >= hi_max || (start + KT <= lo_min && !(Sinks && start < sinks));
     }
-    __device__ __forceinline__ bool masks(int32_t start) const { return start + KT > hi_min || start < lo_max; }
+    __device__ __forceinline__ bool masks(int32_t start) const {
+        return start + KT > hi_min || (start < lo_max && !(Sinks && start + KT <= sinks));
+    }
 
     // O^T += V^T P^T (PV), S^T = K Q^T (QK), in groups of four products whose
     // operands are read kAhead groups before they are used: four wavefronts
@@ -342,8 +351,12 @@ struct Rows {
 #pragma unroll
             for (int b = 0; b < NB; ++b)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    if (first + uint32_t(32 * b + 8 * (r / 4) + r % 4) >= width) s[b][r] = -INFINITY;
+                for (int r = 0; r < 16; ++r) {
+                    const uint32_t at = uint32_t(32 * b + 8 * (r / 4) + r % 4);
+                    bool hidden = first + at >= width;
+                    if constexpr (Sinks) hidden = hidden && first + uint32_t(see_lo) + at >= uint32_t(see_sinks);
+                    if (hidden) s[b][r] = -INFINITY;
+                }
         }
         float top = s[0][0];
 #pragma unroll
@@ -403,7 +416,7 @@ struct Loader {
     bool absent, missing;                          // a page that is none of the cache's: under way, ever (wavefront)
     uint4 kr[NL], vr[NL];
 
-    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t rw) {
+    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, int32_t end, uint32_t kvh, uint32_t rw) {
         gtid = rw * 64u + threadIdx.x % kWave;
         row = gtid / CPR;
         chunk = gtid % CPR * 8u < a.dim ? gtid % CPR : 0u;
@@ -413,7 +426,7 @@ struct Loader {
         vbase = static_cast<const uint8_t *>(a.v) + uint64_t(kvh) * a.v_units[2] * 16u;
         k_page = a.k_units[0], k_slot = a.k_units[1], v_page = a.v_units[0], v_slot = a.v_units[1];
         same = k_page == v_page && k_slot == v_slot;
-        hi = w.hi;
+        hi = end;
         n_pages = a.n_pages;
         page_shift = a.page_shift;
         absent = missing = false;
@@ -479,14 +492,20 @@ struct Loader {
 // A page that is none of the cache's was read: told if a row sees a key of it.
 // The piece's first tile of keys may begin before every row's window, where a
 // request need not hold its pages any more.
+template <bool Sinks>
 __device__ __forceinline__ void tell_missing(const AttnArgs &a, const Piece &w) {
-    int32_t lo, hi, first;
-    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, first);
+    int32_t lo, hi, first, gap;
+    tile_keys<Sinks>(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, first, gap);
     const int32_t *table = a.table + int64_t(w.req) * a.table_stride;
     bool bad = false;
-    for (int32_t i = (max(first, w.lo) >> a.page_shift) + int32_t(threadIdx.x % kWave); i <= (w.hi - 1) >> a.page_shift;
-         i += int32_t(kWave))
-        bad |= uint32_t(table[i]) >= a.n_pages;
+    auto look = [&](int32_t from, int32_t to) {  // the keys from .. to - 1
+        if (from >= to) return;
+        for (int32_t i = (from >> a.page_shift) + int32_t(threadIdx.x % kWave); i <= (to - 1) >> a.page_shift;
+             i += int32_t(kWave))
+            bad |= uint32_t(table[i]) >= a.n_pages;
+    };
+    look(max(first, key_at<Sinks>(a, w, w.lo)), end_of<Sinks>(a, w));
+    if constexpr (Sinks) look(w.lo, min(w.hi, a.sinks));
     if (bad && a.status) atomicOr(a.status, kStatusCorrupt);
 }
 
@@ -497,9 +516,9 @@ __device__ __forceinline__ void tell_missing(const AttnArgs &a, const Piece &w) 
 template <int DP>
 constexpr uint32_t out_bytes() { return 32u * DP * 4u; }
 
-template <typename E, int DP, int KT, int RW, int KW>
+template <typename E, int DP, int KT, int RW, int KW, bool Sinks>
 __device__ __forceinline__ void store(const AttnArgs &a, const Piece &w, uint32_t kvh, uint8_t *lds, uint32_t ml_at,
-                                      Rows<E, DP, KT> &x, uint32_t wave) {
+                                      Rows<E, DP, KT, Sinks> &x, uint32_t wave) {
     using T = Type<E>;
     using V8 = typename T::V8;
     constexpr int CPR = DP / 8, ND = DP / 32;
@@ -520,7 +539,7 @@ __device__ __forceinline__ void store(const AttnArgs &a, const Piece &w, uint32_
                 own[place(c, 8u * uint32_t(d) + 2u * uint32_t(q4) + h)] = float4{
                     x.acc[d][4 * q4], x.acc[d][4 * q4 + 1], x.acc[d][4 * q4 + 2], x.acc[d][4 * q4 + 3]};
     } else {
-        rows_one_by_one<E, DP>(a, w, kvh, 32u * rw, kw * KT, uint32_t(KW * KT), KT, reinterpret_cast<float *>(own), ml);
+        rows_one_by_one<E, DP, Sinks>(a, w, kvh, 32u * rw, kw * KT, uint32_t(KW * KT), KT, reinterpret_cast<float *>(own), ml);
     }
     __syncthreads();
     auto weight = [&](float mk, float top) {
@@ -594,26 +613,27 @@ struct Shape {
     static constexpr uint32_t kLds = kMl + kWaves * 32 * 8;
 };
 
-template <typename E, int DP, int RW, int KT>
+template <typename E, int DP, int RW, int KT, bool Sinks>
 __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(AttnArgs a) {
     using Sh = Shape<DP, RW, KT>;
-    using R = Rows<E, DP, KT>;
+    using R = Rows<E, DP, KT, Sinks>;
     constexpr int KW = Sh::KW;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
     Piece w;
-    if (!find_piece<kThreads>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
+    if (!find_piece<kThreads, Sinks>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t rw = wave % RW, kw = wave / RW;
     Loader<E, DP, KT, 64 * RW, false> ld;
-    ld.init(a, w, kvh, rw);
+    ld.init(a, w, end_of<Sinks>(a, w), kvh, rw);
     const int32_t n_tiles = (w.hi - w.lo + KT - 1) / KT;
     const int32_t n_steps = (n_tiles + KW - 1) / KW;  // the same for every group: they meet at barriers
-    auto tile_start = [&](int32_t step) { return w.lo + (step * KW + int32_t(kw)) * KT; };
+    auto tile_key = [&](int32_t step) { return w.lo + (step * KW + int32_t(kw)) * KT; };
+    auto tile_start = [&](int32_t step) { return key_at<Sinks>(a, w, tile_key(step)); };
     R x;
     if (n_steps) ld.fetch_pages(tile_start(0));
     x.init(a, w, kvh, 32u * rw);
-    if (tile_start(0) < w.hi) {
+    if (tile_key(0) < w.hi) {
         ld.load(tile_start(0));
         ld.fetch_pages(tile_start(1));
     }
@@ -631,7 +651,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         else
             __syncthreads();
-        if (tile_start(step + 1) < w.hi) {
+        if (tile_key(step + 1) < w.hi) {
             ld.load(tile_start(step + 1));
             ld.fetch_pages(tile_start(step + 2));
         }
@@ -645,8 +665,8 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
         x.template products<true, false, 1>(vt, p, kt, s, nothing);
     }
     const AttnArgs &b = again(a);
-    if (ld.missing) tell_missing(b, w);
-    store<E, DP, KT, RW, KW>(b, w, kvh, lds, Sh::kMl, x, wave);
+    if (ld.missing) tell_missing<Sinks>(b, w);
+    store<E, DP, KT, RW, KW, Sinks>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 
 // Eight wavefronts of 32 rows each, for steps with tiles of 256 rows for
@@ -687,21 +707,21 @@ struct Shape8 {
     static constexpr uint32_t kLds = kMl + kWaves8 * 32 * 8;
 };
 
-template <typename E, int DP>
+template <typename E, int DP, bool Sinks>
 __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     using Sh = Shape8<DP>;
     constexpr int KT = Sh::KT;
-    using R = Rows<E, DP, KT>;
+    using R = Rows<E, DP, KT, Sinks>;
     extern __shared__ __attribute__((aligned(16))) uint8_t lds[];
     const uint32_t kvh = blockIdx.x % a.kv_heads, index = blockIdx.x / a.kv_heads;
     Piece w;
-    if (!find_piece<512>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
+    if (!find_piece<512, Sinks>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const bool second = wave >= 4u;
     Loader<E, DP, KT, 512, true> ld;  // (the launcher sees to it)
-    ld.init(a, w, kvh, wave);
+    ld.init(a, w, end_of<Sinks>(a, w), kvh, wave);
     const int32_t n = (w.hi - w.lo + KT - 1) / KT;
-    auto tile_start = [&](int32_t t) { return w.lo + t * KT; };
+    auto tile_start = [&](int32_t t) { return key_at<Sinks>(a, w, w.lo + t * KT); };
     auto k_tile = [&](int32_t t) { return lds + uint32_t(t & 1) * Sh::kTileBytes; };
     R x;
     if (n) ld.fetch_pages(tile_start(0));
@@ -733,8 +753,14 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     // the wavefront's own tiles: t0 .. t1 - 1
     int32_t t = 0, t0 = 0, t1 = 0;
     if (!x.idle) {
-        t0 = min(max((x.lo_min - w.lo) / KT, 0), n);
-        t1 = min(max((x.hi_max - w.lo + KT - 1) / KT, t0), n);
+        int32_t first = x.lo_min, end = x.hi_max;
+        if constexpr (Sinks) {
+            // from the sinks on, where the piece has them; else all of it is behind the gap
+            first = w.lo < a.sink_end ? w.lo : first - w.gap;
+            if (end > a.sink_end) end -= w.gap;
+        }
+        t0 = min(max((first - w.lo) / KT, 0), n);
+        t1 = min(max((end - w.lo + KT - 1) / KT, t0), n);
     }
     auto turn_without_rows = [&]() {
         load(t + lead);
@@ -777,8 +803,8 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     while (t < n) turn_without_rows();
     if (!second) __syncthreads();
     const AttnArgs &b = again(a);
-    if (ld.missing) tell_missing(b, w);
-    store<E, DP, KT, 8, 1>(b, w, kvh, lds, Sh::kMl, x, wave);
+    if (ld.missing) tell_missing<Sinks>(b, w);
+    store<E, DP, KT, 8, 1, Sinks>(b, w, kvh, lds, Sh::kMl, x, wave);
 }
 
 // The pieces of a split tile joined.  A wavefront takes a row (WPR = 1, for
@@ -896,12 +922,12 @@ uint32_t workgroups_at_once(int dp, int rw) { return dp > 128 || rw == 8 ? 256u 
 // device: under a table for 8192 tokens or more a prompt of 512 takes 28.4 and
 // not 16.1 us, of 200 16.7-19.5 and not 10.6, 64 single tokens over 700 49 and
 // not 40 (launch_plan leaves them to be split then).
-int tile_height(const dfc_attention_args &a) {
+int tile_height(const dfc_attention_args &a, uint32_t sinks) {
     const uint32_t group = a.heads / a.cache.kv_heads;
     const uint64_t most = most_rows(a);
     const int dp = padded_dim(a), fit = tallest(most);
     uint64_t keys = uint64_t(a.max_pages) * a.cache.page_size;
-    if (a.window) keys = std::min<uint64_t>(keys, uint64_t(a.window) + most / group);
+    if (a.window) keys = std::min<uint64_t>(keys, uint64_t(a.window) + most / group + sinks);
     // pairs of 32 rows and 64 keys there may be
     const double pairs = double(a.tokens * group) / 32.0 * a.cache.kv_heads * double(keys) / 64.0;
     int rw = 1;
@@ -912,7 +938,7 @@ int tile_height(const dfc_attention_args &a) {
     return rw == 8 && !same ? 4 : rw;
 }
 
-LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
+LaunchPlan launch_plan(const dfc_attention_args &a, uint32_t sinks, int rw) {
     LaunchPlan p;
     const uint32_t group = a.heads / a.cache.kv_heads;
     p.dp = padded_dim(a);
@@ -948,7 +974,8 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
     // 8191: 245 without, 216 with it): they are left to the device from 40 key
     // tiles on.
     if (a.window && a.causal)
-        longest = std::min<uint64_t>(longest, (uint64_t(a.window) + p.rows_per_tile / group) / p.kt + 3u);
+        longest = std::min<uint64_t>(longest, (uint64_t(a.window) + p.rows_per_tile / group) / p.kt + 3u +
+                                                  dfc::ceil_div(uint64_t(sinks), uint64_t(p.kt)));
     const double load = double(tiles) * a.cache.kv_heads / p.resident;
     const double rounds = a.n_requests == 1 ? std::ceil(load) : std::max(1.0, load);
     const double unsplit = rounds * (double(longest) + p.piece_cost);
@@ -967,12 +994,12 @@ LaunchPlan launch_plan(const dfc_attention_args &a, int rw) {
 }
 
 // What a call needs depends on the window, and by the tile height on the
-// layouts; one size has to serve every call of the same sizes.  A window never
-// needs more.
+// layouts; one size has to serve every call of the same sizes.  A window, with
+// sinks or without, never needs more.
 uint64_t workspace_bytes(dfc_attention_args a) {
     uint64_t bytes = 0;
     a.window = 0;
-    for (int rw = 1; rw <= tallest(most_rows(a)); rw *= 2) bytes = std::max(bytes, launch_plan(a, rw).bytes);
+    for (int rw = 1; rw <= tallest(most_rows(a)); rw *= 2) bytes = std::max(bytes, launch_plan(a, 0, rw).bytes);
     return bytes;
 }
 
@@ -991,14 +1018,14 @@ dfc_status check_attention(const dfc_attention_args &a) {
     return DFC_OK;
 }
 
-template <typename E, int DP, int RW, int KT>
+template <typename E, int DP, int RW, int KT, bool Sinks>
 dfc_status launch(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
     constexpr uint32_t kLds = RW == 8 ? Shape8<DP>::kLds : Shape<DP, RW == 8 ? 4 : RW, KT>::kLds;
     void (*kernel)(AttnArgs);
     if constexpr (RW == 8)
-        kernel = &attention8_kernel<E, DP>;
+        kernel = &attention8_kernel<E, DP, Sinks>;
     else
-        kernel = &attention_kernel<E, DP, RW, KT>;
+        kernel = &attention_kernel<E, DP, RW, KT, Sinks>;
     if (!allow_full_lds(reinterpret_cast<const void *>(kernel))) return DFC_EHIP;
     const uint64_t grid = (uint64_t(p.tile_cap) + p.extra) * a.kv_heads;
     if (grid > 0x7fffffffull) return DFC_EUNSUPPORTED;
@@ -1014,19 +1041,19 @@ dfc_status launch(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
     return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
 }
 
-template <typename E>
+template <typename E, bool Sinks>
 dfc_status launch_type(const AttnArgs &a, const LaunchPlan &p, hipStream_t st) {
     switch (p.dp * 16 + p.rw) {
-        case 64 * 16 + 1: return launch<E, 64, 1, 32>(a, p, st);
-        case 64 * 16 + 2: return launch<E, 64, 2, 32>(a, p, st);
-        case 64 * 16 + 4: return launch<E, 64, 4, 64>(a, p, st);
-        case 64 * 16 + 8: return launch<E, 64, 8, 64>(a, p, st);
-        case 128 * 16 + 1: return launch<E, 128, 1, 32>(a, p, st);
-        case 128 * 16 + 2: return launch<E, 128, 2, 32>(a, p, st);
-        case 128 * 16 + 4: return launch<E, 128, 4, 64>(a, p, st);
-        case 128 * 16 + 8: return launch<E, 128, 8, 64>(a, p, st);
-        case 256 * 16 + 2: return launch<E, 256, 2, 32>(a, p, st);
-        default: return launch<E, 256, 4, 32>(a, p, st);
+        case 64 * 16 + 1: return launch<E, 64, 1, 32, Sinks>(a, p, st);
+        case 64 * 16 + 2: return launch<E, 64, 2, 32, Sinks>(a, p, st);
+        case 64 * 16 + 4: return launch<E, 64, 4, 64, Sinks>(a, p, st);
+        case 64 * 16 + 8: return launch<E, 64, 8, 64, Sinks>(a, p, st);
+        case 128 * 16 + 1: return launch<E, 128, 1, 32, Sinks>(a, p, st);
+        case 128 * 16 + 2: return launch<E, 128, 2, 32, Sinks>(a, p, st);
+        case 128 * 16 + 4: return launch<E, 128, 4, 64, Sinks>(a, p, st);
+        case 128 * 16 + 8: return launch<E, 128, 8, 64, Sinks>(a, p, st);
+        case 256 * 16 + 2: return launch<E, 256, 2, 32, Sinks>(a, p, st);
+        default: return launch<E, 256, 4, 32, Sinks>(a, p, st);
     }
 }
 
@@ -1043,10 +1070,19 @@ dfc_status dfc_paged_attention_workspace(const dfc_attention_args *args, uint64_
 }
 
 dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
+    return dfc_paged_attention_sinks(args, 0, stream);
+}
+
+dfc_status dfc_paged_attention_sinks(const dfc_attention_args *args, uint32_t sinks, void *stream) {
     if (!args) return DFC_EINVAL;
     const dfc_attention_args &in = *args;
     const dfc_status s = check_attention(in);
     if (s != DFC_OK) return s;
+    if (sinks > 0x7fffffffu) return DFC_EINVAL;
+    // without a window every token is visible; there are no more tokens than
+    // the table has room for
+    if (!in.window) sinks = 0;
+    sinks = uint32_t(std::min<uint64_t>({sinks, uint64_t(in.max_pages) * in.cache.page_size, 0x7ffffe00u}));
     if (!in.tokens || !in.n_requests) return DFC_OK;
     if (!in.q_dev || !in.out_dev || !in.cu_q || !in.seq_lens || !in.workspace_dev) return DFC_EINVAL;
     if (in.max_pages && !in.block_table) return DFC_EINVAL;
@@ -1055,7 +1091,7 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     if (reinterpret_cast<uintptr_t>(in.workspace_dev) & 255u) return DFC_EINVAL;
     for (int i = 0; i < 2; ++i)
         if (in.q_stride[i] % 8 || in.out_stride[i] % 8) return DFC_EINVAL;
-    const LaunchPlan p = launch_plan(in, tile_height(in));
+    const LaunchPlan p = launch_plan(in, sinks, tile_height(in, sinks));
     if (in.workspace_bytes < workspace_bytes(in)) return DFC_ESIZE;
     AttnArgs a;
     std::memset(&a, 0, sizeof(a));
@@ -1107,8 +1143,12 @@ dfc_status dfc_paged_attention(const dfc_attention_args *args, void *stream) {
     a.part_ml = reinterpret_cast<float *>(ws + p.off_ml);
     a.part_o = reinterpret_cast<float *>(ws + p.off_o);
     a.status = in.status_dev;
+    a.sinks = int32_t(sinks);
+    a.sink_end = int32_t((sinks + uint32_t(p.kt) - 1u) / uint32_t(p.kt) * uint32_t(p.kt));
     hipStream_t st = static_cast<hipStream_t>(stream);
-    return in.cache.dtype == DFC_BF16 ? launch_type<__bf16>(a, p, st) : launch_type<_Float16>(a, p, st);
+    const bool bf = in.cache.dtype == DFC_BF16;
+    if (sinks) return bf ? launch_type<__bf16, true>(a, p, st) : launch_type<_Float16, true>(a, p, st);
+    return bf ? launch_type<__bf16, false>(a, p, st) : launch_type<_Float16, false>(a, p, st);
 }
 
 }  // extern "C"

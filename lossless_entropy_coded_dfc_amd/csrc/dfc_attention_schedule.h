@@ -15,11 +15,13 @@ constexpr uint32_t kThreads = 256;
 constexpr uint32_t kWaves = 4;
 
 // One piece of work: a tile of rows of one request and a range of keys, for
-// one cache head.
+// one cache head.  With sinks, keys are counted without those between the
+// sinks and the window, which no row of the tile sees: see key_at.
 struct Piece {
     uint32_t req, row0;     // request; first row of the tile
     int32_t q_start, q_len, kv_len;
     int32_t lo, hi;         // keys
+    int32_t gap;            // left out behind the sinks
     uint32_t split, splits; // which piece of the tile, of how many
     uint32_t slot;          // first partial result of the tile (splits > 1)
 };
@@ -56,7 +58,20 @@ struct AttnArgs {
     Tile *tiles;               // null: no tile can be split
     float *part_o, *part_ml;
     uint32_t *status;
+    int32_t sinks, sink_end;   // tokens that stay visible; the same up to a whole key tile
 };
+
+// The token of a piece's key.  Both ends of the gap are multiples of the key
+// tile, so a tile of keys is a tile of tokens.
+template <bool Sinks>
+__device__ __forceinline__ int32_t key_at(const AttnArgs &a, const Piece &w, int32_t key) {
+    return Sinks && key >= a.sink_end ? key + w.gap : key;
+}
+// The end of a piece's tokens.
+template <bool Sinks>
+__device__ __forceinline__ int32_t end_of(const AttnArgs &a, const Piece &w) {
+    return Sinks && w.hi > a.sink_end ? w.hi + w.gap : w.hi;
+}
 
 // -------------------------------------------------------------- schedule
 //
@@ -86,9 +101,12 @@ __device__ __forceinline__ Req request(const AttnArgs &a, uint32_t r, uint32_t &
 }
 
 // Keys [first, hi) that the rows row0 .. of a tile see between them, and lo,
-// first rounded down to a multiple of the key tile.
+// first rounded down to a multiple of the key tile.  With sinks, lo is 0, and
+// lo and hi leave out the `gap` keys between the sinks' last tile and the
+// window's first.
+template <bool Sinks>
 __device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint32_t row0, int32_t &lo, int32_t &hi,
-                                          int32_t &first) {
+                                          int32_t &first, int32_t &gap) {
     const int32_t t0 = int32_t(row0 / a.group);
     const int32_t rows = int32_t(min(a.rows_per_tile, uint32_t(q.q_len) * a.group - row0));
     const int32_t t1 = int32_t((row0 + uint32_t(rows) - 1) / a.group);
@@ -98,6 +116,12 @@ __device__ __forceinline__ void tile_keys(const AttnArgs &a, const Req &q, uint3
     hi = int32_t(max(end, int64_t(0)));
     first = int32_t(min(begin, int64_t(hi)));
     lo = first >> a.key_shift << a.key_shift;
+    gap = 0;
+    if constexpr (Sinks) {
+        gap = max(lo - a.sink_end, 0);
+        lo = 0;
+        hi -= gap;
+    }
 }
 
 __device__ __forceinline__ uint32_t key_tiles(const AttnArgs &a, int32_t lo, int32_t hi) {
@@ -108,12 +132,13 @@ __device__ __forceinline__ uint32_t ceil_of(uint32_t x, uint32_t y) { return (x 
 
 // Tiles of rows of a request, and the key tiles of its last one (the longest
 // but for a window's edge).
+template <bool Sinks>
 __device__ __forceinline__ void tiles_of(const AttnArgs &a, const Req &q, uint32_t &n, uint32_t &c) {
     n = (uint32_t(q.q_len) * a.group + a.rows_per_tile - 1u) >> a.rows_shift;
     c = 0;
     if (n) {
-        int32_t lo, hi, first;
-        tile_keys(a, q, (n - 1u) * a.rows_per_tile, lo, hi, first);
+        int32_t lo, hi, first, gap;
+        tile_keys<Sinks>(a, q, (n - 1u) * a.rows_per_tile, lo, hi, first, gap);
         c = key_tiles(a, lo, hi);
     }
 }
@@ -178,7 +203,7 @@ __device__ __forceinline__ uint32_t choose_piece(const AttnArgs &a, uint32_t n, 
 // none.  `scratch` is LDS that nothing else uses meanwhile.  Row ranges that
 // overlap could make more tiles than q has room for: then there are none.
 // Called by all NT threads of the workgroup.
-template <uint32_t NT>
+template <uint32_t NT, bool Sinks>
 __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bool first, uint32_t *scratch, Piece &w) {
     const uint32_t tid = threadIdx.x, lane = tid % kWave;
     uint32_t bad = 0;
@@ -187,7 +212,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
         Req q{0, 0, 0};
         if (lane < a.n_requests) q = request(a, lane, bad);
         uint32_t n, c;
-        tiles_of(a, q, n, c);
+        tiles_of<Sinks>(a, q, n, c);
         piece = a.extra ? choose_piece<NT>(a, n, c, scratch) : 1u << 30;
         const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u, z = s > 1u ? n : 0u;
         const uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), iz = wave_inclusive_scan(z);
@@ -214,7 +239,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
         uint64_t all = 0, tiles = 0;
         for (uint32_t r = tid; r < a.n_requests; r += NT) {
             uint32_t n, c;
-            tiles_of(a, request(a, r, bad), n, c);
+            tiles_of<Sinks>(a, request(a, r, bad), n, c);
             all += uint64_t(n) * c;
             tiles += n;
         }
@@ -244,7 +269,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
             Req q{0, 0, 0};
             uint32_t unused = 0, n, c;
             if (r0 + tid < a.n_requests) q = request(a, r0 + tid, unused);
-            tiles_of(a, q, n, c);
+            tiles_of<Sinks>(a, q, n, c);
             const uint32_t s = max(1u, ceil_of(c, piece)), x = n * s, y = s > 1u ? x : 0u, z = s > 1u ? n : 0u;
             uint32_t ix = wave_inclusive_scan(x), iy = wave_inclusive_scan(y), iz = wave_inclusive_scan(z);
             __syncthreads();  // part has been read
@@ -281,7 +306,7 @@ __device__ __forceinline__ bool find_piece(const AttnArgs &a, uint32_t index, bo
     w.split = within - tile * parts;
     w.row0 = (n_tiles - 1u - tile) * a.rows_per_tile;
     int32_t lo, hi, seen;
-    tile_keys(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, seen);
+    tile_keys<Sinks>(a, Req{w.q_start, w.q_len, w.kv_len}, w.row0, lo, hi, seen, w.gap);
     const uint32_t c = key_tiles(a, lo, hi);
     w.splits = min(parts, max(1u, ceil_of(c, piece)));
     w.slot = slot0 + tile * parts;

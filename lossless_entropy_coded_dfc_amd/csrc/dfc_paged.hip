@@ -15,7 +15,9 @@
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstdint>
+#include <cstring>
 
 #include "dfc.h"
 #include "dfc_decode_core.h"
@@ -192,9 +194,11 @@ __global__ __launch_bounds__(kPlanThreads) void plan_kernel(PlanArgs p) {
 struct AppendArgs {
     dfc_append_args a;
     uint32_t page_shift;
-    uint32_t chunks, units;      // 8-value chunks of a head; threads per head
+    uint32_t chunks, units;      // 8-value chunks of a head; pairs of them
+    uint32_t lanes;              // threads per head
     uint32_t per_token;          // threads per token
     uint64_t threads;
+    dfc_norm_args norms;
 };
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
@@ -249,6 +253,34 @@ __device__ __forceinline__ void store8(E *at, const E8 &v) {
         *to = __builtin_bit_cast(U4, v);
 }
 
+// The threads of a head norm it: x w / sqrt(mean(x^2) + eps).  The squares are
+// summed and the root applied in 64 bits, in which no value of 32 overflows.
+template <typename E>
+__device__ __forceinline__ void norm(const AppendArgs &p, const void *weights, uint32_t at0, uint32_t at1, bool two,
+                                     float (&x)[8], float (&y)[8]) {
+    double sum = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        sum += double(x[i]) * double(x[i]);
+        sum += double(y[i]) * double(y[i]);
+    }
+    for (uint32_t d = p.lanes / 2u; d; d /= 2u) sum += __shfl_xor(sum, int(d));
+    const double r = 1.0 / sqrt(sum / double(p.a.cache.head_dim) + double(p.norms.eps));
+    float w[8] = {}, z[8] = {};
+    if (p.norms.dtype == DFC_F32) {
+        load8(static_cast<const float *>(weights) + at0, w);
+        if (two) load8(static_cast<const float *>(weights) + at1, z);
+    } else {
+        load8(static_cast<const E *>(weights) + at0, w);
+        if (two) load8(static_cast<const E *>(weights) + at1, z);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        x[i] = float(double(x[i]) * r) * w[i];
+        y[i] = float(double(y[i]) * r) * z[i];
+    }
+}
+
 // One thread takes two chunks of 8 values of one head of one token: those that
 // pair up half a rotation apart, elsewhere two that lie as far from each other
 // as the head's other threads reach.  Every value is read and written once.
@@ -256,7 +288,9 @@ __device__ __forceinline__ void store8(E *at, const E8 &v) {
 // 35.5-39 us (5.3-5.8 TB/s; one chunk a thread, and with it every rotated value
 // read twice, took 52).  64 tokens from float32 take 6 us, a launch and one chain of
 // loads.
-template <typename S, typename E, bool Past>
+// With norms the threads of a head are a power of two side by side (those past
+// its chunks only lend a hand to the sum).
+template <typename S, typename E, bool Past, bool Norm>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     using E8 = __attribute__((ext_vector_type(8))) E;
     const dfc_append_args &a = p.a;
@@ -267,7 +301,8 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     const uint32_t rest = uint32_t(base - t_base * p.per_token) + threadIdx.x;
     const uint64_t t = t_base + rest / p.per_token;
     const uint32_t in_token = rest % p.per_token;
-    const uint32_t row = in_token / p.units, u = in_token % p.units;
+    const uint32_t lanes = Norm ? p.lanes : p.units;
+    const uint32_t row = in_token / lanes, u = in_token % lanes;
     const uint32_t nk = a.cache.kv_heads;
     // rows of a token: k heads, v heads, q heads
     const uint32_t which = row < nk ? 0u : row < 2u * nk ? 1u : 2u;
@@ -295,10 +330,15 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     const uint32_t turned = which == 1u ? 0u : a.rot_dim / 8u;  // chunks that are rotated, an even number
     const uint32_t c0 = u < turned / 2u ? u : u + turned / 2u;
     const uint32_t c1 = u < turned / 2u ? u + turned / 2u : c0 + p.units - turned / 2u;
-    const bool two = c1 < p.chunks;
-    float x[8], y[8] = {};
-    load8(src + 8u * c0, x);
+    const bool one = !Norm || u < p.units, two = one && c1 < p.chunks;
+    float x[8] = {}, y[8] = {};
+    if (one) load8(src + 8u * c0, x);
     if (two) load8(src + 8u * c1, y);
+    if constexpr (Norm) {
+        const void *weights = which == 0u ? p.norms.k_norm_dev : which == 2u ? p.norms.q_norm_dev : nullptr;
+        if (weights) norm<E>(p, weights, 8u * (one ? c0 : 0u), 8u * c1, two, x, y);
+        if (!one) return;
+    }
     if (c0 < turned) {
         int32_t pos = a.positions[t];
         if (pos < 0 || uint32_t(pos) >= a.max_positions) {
@@ -324,13 +364,21 @@ __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     }
 }
 
-template <typename S, typename E>
+template <typename S, typename E, bool Norm>
 void launch_append(const AppendArgs &p, uint32_t blocks, hipStream_t stream) {
     // 32 bytes a thread
     if (p.threads * 32u > (2u << 20))
-        hipLaunchKernelGGL((append_kernel<S, E, true>), dim3(blocks), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL((append_kernel<S, E, true, Norm>), dim3(blocks), dim3(256), 0, stream, p);
     else
-        hipLaunchKernelGGL((append_kernel<S, E, false>), dim3(blocks), dim3(256), 0, stream, p);
+        hipLaunchKernelGGL((append_kernel<S, E, false, Norm>), dim3(blocks), dim3(256), 0, stream, p);
+}
+
+template <typename S, typename E>
+void launch_append(const AppendArgs &p, uint32_t blocks, hipStream_t stream) {
+    if (p.norms.q_norm_dev || p.norms.k_norm_dev)
+        launch_append<S, E, true>(p, blocks, stream);
+    else
+        launch_append<S, E, false>(p, blocks, stream);
 }
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
@@ -361,6 +409,10 @@ dfc_status dfc_paged_plan(const dfc_plan_args *args, void *stream) {
 }
 
 dfc_status dfc_paged_append(const dfc_append_args *args, void *stream) {
+    return dfc_paged_append_normed(args, nullptr, stream);
+}
+
+dfc_status dfc_paged_append_normed(const dfc_append_args *args, const dfc_norm_args *norms, void *stream) {
     if (!args) return DFC_EINVAL;
     const dfc_append_args &a = *args;
     const dfc_status cs = dfc::check_cache(a.cache);
@@ -371,6 +423,12 @@ dfc_status dfc_paged_append(const dfc_append_args *args, void *stream) {
     if (a.rot_dim % 16u || a.rot_dim > a.cache.head_dim) return DFC_EINVAL;
     if (a.rot_dim && (!a.rotary_dev || !a.max_positions || !aligned16(a.rotary_dev))) return DFC_EINVAL;
     if (a.q_heads > 65536u) return DFC_EINVAL;
+    const bool q_normed = norms && norms->q_norm_dev, k_normed = norms && norms->k_norm_dev;
+    if (q_normed || k_normed) {
+        if (norms->dtype != DFC_F32 && norms->dtype != a.cache.dtype) return DFC_EUNSUPPORTED;
+        if (!aligned16(norms->q_norm_dev) || !aligned16(norms->k_norm_dev)) return DFC_EINVAL;
+        if (!(norms->eps > 0.0f) || !std::isfinite(norms->eps)) return DFC_EINVAL;
+    }
     if (!a.tokens) return DFC_OK;
     if (!a.k_dev || !a.v_dev || !a.slots || (a.rot_dim && !a.positions)) return DFC_EINVAL;
     if (a.q_heads && (!a.q_dev || !a.q_out_dev)) return DFC_EINVAL;
@@ -383,14 +441,20 @@ dfc_status dfc_paged_append(const dfc_append_args *args, void *stream) {
         if (!aligned16(a.q_dev) || !aligned16(a.q_out_dev)) return DFC_EINVAL;
         for (int i = 0; i < 2; ++i)
             if (a.q_stride[i] % unit || a.q_out_stride[i] % 8) return DFC_EINVAL;
-        if (a.q_dev == a.q_out_dev && (a.rot_dim || a.source_dtype == DFC_F32)) return DFC_EINVAL;
+        if (a.q_dev == a.q_out_dev && (a.rot_dim || q_normed || a.source_dtype == DFC_F32)) return DFC_EINVAL;
     }
     AppendArgs p;
     p.a = a;
     p.page_shift = dfc::log2_of(a.cache.page_size);
     p.chunks = a.cache.head_dim / 8u;
     p.units = (p.chunks + 1u) / 2u;
-    p.per_token = p.units * (a.q_heads + 2u * a.cache.kv_heads);
+    p.lanes = p.units;
+    std::memset(&p.norms, 0, sizeof(p.norms));
+    if (q_normed || k_normed) {
+        p.norms = *norms;
+        p.lanes = 1u << dfc::log2_of(p.units);  // (16 at most: head_dim is 256 at most)
+    }
+    p.per_token = p.lanes * (a.q_heads + 2u * a.cache.kv_heads);
     p.threads = uint64_t(p.per_token) * a.tokens;
     const uint64_t blocks = dfc::ceil_div(p.threads, uint64_t(256));
     if (blocks > 0x7fffffffull) return DFC_EUNSUPPORTED;

@@ -1,6 +1,6 @@
-// dfc_paged_bind.cpp - the paged cache's entry points for Python: checks of
-// tensors, allocation of what a call returns, and the argument structures of
-// dfc.h.
+// dfc_paged_bind.cpp - the entry points of the paged cache and of the drafts'
+// verification for Python: checks of tensors, allocation of what a call returns,
+// and the argument structures of dfc.h.
 //
 // The kernels of a decoding step run for 4 to 12 us.  Done in Python and ctypes
 // this took 9 to 11 us a call beside the launch's 3.6 (an append of 64 tokens
@@ -19,6 +19,7 @@
 #include <cstdint>
 #include <cstring>
 #include <exception>
+#include <vector>
 
 #include "dfc.h"
 
@@ -44,9 +45,16 @@ template <typename... A>
 
 PyObject *g_current_stream;  // torch's: device -> handle
 decltype(&dfc_paged_plan) g_plan;
-decltype(&dfc_paged_append) g_append;
-decltype(&dfc_paged_attention) g_attention;
+decltype(&dfc_paged_append_normed) g_append;
+decltype(&dfc_paged_attention_sinks) g_attention;
 decltype(&dfc_paged_attention_workspace) g_workspace;
+decltype(&dfc_paged_release) g_release;
+decltype(&dfc_paged_fork) g_fork;
+decltype(&dfc_paged_compact) g_compact;
+decltype(&dfc_paged_compact_workspace) g_compact_workspace;
+decltype(&dfc_paged_copy) g_copy;
+decltype(&dfc_verify_drafts) g_verify;
+decltype(&dfc_verify_workspace) g_verify_workspace;
 
 // None of the operators has a backward pass: a tensor that asks for one is
 // refused, or its gradient would be lost without a word.
@@ -54,7 +62,7 @@ const at::Tensor &tensor(PyObject *o, const char *name) {
     if (!THPVariable_Check(o)) type_error("%s must be a tensor", name);
     const at::Tensor &t = THPVariable_Unpack(o);
     if (t.requires_grad() && c10::GradMode::is_enabled())
-        value_error("%s requires a gradient, which the paged cache's operators do not compute: detach it, or call under "
+        value_error("%s requires a gradient, which the serving operators do not compute: detach it, or call under "
                     "torch.no_grad()",
                     name);
     return t;
@@ -85,6 +93,12 @@ uint32_t count(PyObject *o, const char *name) {
 uint32_t narrow(int64_t x, const char *name) {
     if (x < 0 || x >= int64_t(1) << 31) value_error("%s must be between 0 and 2^31 - 1", name);
     return uint32_t(x);
+}
+
+float real(PyObject *o) {
+    const double x = PyFloat_AsDouble(o);
+    if (x == -1.0 && PyErr_Occurred()) throw Failed();
+    return float(x);
 }
 
 bool truth(PyObject *o) {
@@ -163,6 +177,16 @@ int32_t *table_of(const at::Tensor &t, int64_t n, int64_t dev, int64_t &stride, 
     return static_cast<int32_t *>(t.data_ptr());
 }
 
+// Weights of a norm: head_dim values, float32 or of the cache's type.
+const void *norm_of(PyObject *o, const char *name, at::ScalarType type, int64_t dim, int64_t dev, uint32_t &dtype) {
+    if (o == Py_None) return nullptr;
+    const at::Tensor &t = tensor(o, name);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != type)
+        type_error("%s must be float32 or of the cache's type", name);
+    dtype = t.scalar_type() == at::kFloat ? DFC_F32 : type == at::kBFloat16 ? DFC_BF16 : DFC_F16;
+    return vector<const void>(t, t.scalar_type(), dim, dev, name);
+}
+
 uint32_t *status_of(PyObject *o, int64_t dev) {
     if (o == Py_None) return nullptr;
     const at::Tensor &t = tensor(o, "status");
@@ -186,11 +210,11 @@ void *stream_of(PyObject *o, int64_t dev) {
 }
 
 // A launch may wait for room in the queue: other threads run meanwhile.
-template <typename F, typename A>
-dfc_status call(F f, const A &args, void *stream) {
+template <typename F, typename... A>
+dfc_status call(F f, A... args) {
     dfc_status s;
     Py_BEGIN_ALLOW_THREADS
-    s = f(&args, stream);
+    s = f(args...);
     Py_END_ALLOW_THREADS
     return s;
 }
@@ -240,19 +264,31 @@ PyObject *answer(dfc_status s, const at::Tensor (&t)[N]) {
     return r;
 }
 
-// setup(current_stream, plan, append, attention, workspace): torch's function
-// for the current stream and the addresses of dfc.h's functions
+template <typename F>
+void address(F &f, PyObject *o) {
+    f = reinterpret_cast<F>(uintptr_t(integer(o, "address")));
+}
+
+// setup(current_stream, addresses ...): torch's function for the current
+// stream and where dfc.h's functions are, in the order below
 PyObject *setup(PyObject *, PyObject *const *a, Py_ssize_t n) {
     return guarded([&]() -> PyObject * {
-        want(n, 5);
+        want(n, 12);
         Py_INCREF(a[0]);
         PyObject *before = g_current_stream;
         g_current_stream = a[0];
         Py_XDECREF(before);
-        g_plan = reinterpret_cast<decltype(g_plan)>(uintptr_t(integer(a[1], "address")));
-        g_append = reinterpret_cast<decltype(g_append)>(uintptr_t(integer(a[2], "address")));
-        g_attention = reinterpret_cast<decltype(g_attention)>(uintptr_t(integer(a[3], "address")));
-        g_workspace = reinterpret_cast<decltype(g_workspace)>(uintptr_t(integer(a[4], "address")));
+        address(g_plan, a[1]);
+        address(g_append, a[2]);
+        address(g_attention, a[3]);
+        address(g_workspace, a[4]);
+        address(g_release, a[5]);
+        address(g_fork, a[6]);
+        address(g_compact, a[7]);
+        address(g_compact_workspace, a[8]);
+        address(g_copy, a[9]);
+        address(g_verify, a[10]);
+        address(g_verify_workspace, a[11]);
         Py_RETURN_NONE;
     });
 }
@@ -297,15 +333,16 @@ PyObject *plan(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         p.positions = vector<int32_t>(t[3], at::kInt, tokens, dev, "the plan's positions");
         p.cursor_out = vector<int64_t>(t[4], at::kLong, 2, dev, "the plan's cursor");
         written(table);
-        return answer(call(g_plan, p, stream_of(a[9], dev)), t);
+        return answer(call(g_plan, &p, stream_of(a[9], dev)), t);
     });
 }
 
 // append(k, v, k_cache, v_cache, slots, q or None, q_out or None, positions or
-//        None, rotary or None, interleaved, status or None, stream)
+//        None, rotary or None, interleaved, status or None, q_norm or None,
+//        k_norm or None, eps, stream)
 PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
-        want(n_args, 12);
+        want(n_args, 15);
         const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
         const at::Tensor &kc = tensor(a[2], "k_cache"), &vc = tensor(a[3], "v_cache");
         const int64_t dev = device_of(kc, "k_cache");
@@ -344,9 +381,19 @@ PyObject *append(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         }
         p.interleaved = truth(a[9]) ? 1u : 0u;
         p.status_dev = status_of(a[10], dev);
+        dfc_norm_args norms;
+        std::memset(&norms, 0, sizeof(norms));
+        if (a[11] != Py_None && a[5] == Py_None) value_error("q_norm needs q");
+        norms.q_norm_dev = norm_of(a[11], "q_norm", type, dim, dev, norms.dtype);
+        norms.k_norm_dev = norm_of(a[12], "k_norm", type, dim, dev, norms.dtype);
+        const bool both = norms.q_norm_dev && norms.k_norm_dev;
+        if (both && tensor(a[11], "q_norm").scalar_type() != tensor(a[12], "k_norm").scalar_type())
+            type_error("q_norm and k_norm must be of one type");
+        norms.eps = real(a[13]);
+        const bool normed = norms.q_norm_dev || norms.k_norm_dev;
         written(kc);
         written(vc);
-        return answer(call(g_append, p, stream_of(a[11], dev)), out);
+        return answer(call(g_append, &p, normed ? &norms : nullptr, stream_of(a[14], dev)), out);
     });
 }
 
@@ -360,10 +407,10 @@ void sizes_of(const at::Tensor &q, int64_t n, int64_t width, PyObject *max_q_len
 
 // attention(q, k_cache, v_cache, block_table, cu_q, seq_lens, scale or None,
 //           causal, window, max_q_len, out or None, lse: None, True or a
-//           tensor, workspace or None, status or None, stream)
+//           tensor, workspace or None, status or None, sinks, stream)
 PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     return guarded([&]() -> PyObject * {
-        want(n_args, 15);
+        want(n_args, 16);
         const at::Tensor &q = tensor(a[0], "q"), &kc = tensor(a[1], "k_cache"), &lens = tensor(a[5], "seq_lens");
         const int64_t dev = device_of(q, "q");
         dfc_attention_args p;
@@ -380,12 +427,11 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         sizes_of(q, n, p.max_pages, a[9], p);
         p.causal = truth(a[7]) ? 1u : 0u;
         p.window = count(a[8], "window");
+        const uint32_t sinks = count(a[14], "sinks");
         if (a[6] == Py_None) {
             p.scale = float(1.0 / std::sqrt(double(shape[2])));
         } else {
-            const double scale = PyFloat_AsDouble(a[6]);
-            if (scale == -1.0 && PyErr_Occurred()) throw Failed();
-            p.scale = float(scale);
+            p.scale = real(a[6]);
         }
         p.q_dev = rows(q, "q", type, shape, dev, p.q_stride);
         p.cu_q = vector<int32_t>(tensor(a[4], "cu_q"), at::kInt, n + 1, dev, "cu_q");
@@ -421,7 +467,7 @@ PyObject *attention(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
         p.workspace_dev = work.data_ptr();
         p.workspace_bytes = uint64_t(work.nbytes());
         p.status_dev = status_of(a[13], dev);
-        return answer(call(g_attention, p, stream_of(a[14], dev)), t);
+        return answer(call(g_attention, &p, sinks, stream_of(a[15], dev)), t);
     });
 }
 
@@ -445,13 +491,268 @@ PyObject *workspace(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
     });
 }
 
+// The cursor of a ring, the ring and the holders.
+template <typename A>
+void pool_of(PyObject *ring, PyObject *cursor, PyObject *shared, int64_t dev, A &p) {
+    const at::Tensor &r = tensor(ring, "free_pages"), &s = tensor(shared, "shared");
+    p.free_pages = vector<int32_t>(r, at::kInt, r.dim() == 1 ? r.size(0) : -1, dev, "free_pages");
+    p.n_ring = narrow(r.size(0), "the length of free_pages");
+    p.cursor = vector<int64_t>(tensor(cursor, "cursor"), at::kLong, 2, dev, "cursor");
+    p.shared = vector<int32_t>(s, at::kInt, s.dim() == 1 ? s.size(0) : -1, dev, "shared");
+    p.n_pages = narrow(s.size(0), "the length of shared");
+}
+
+// release(held_lens, keep_lens, block_table, free_pages, cursor, shared,
+//         page_size, window, sinks, out or None, status or None, stream)
+PyObject *release(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 12);
+        const at::Tensor &held = tensor(a[0], "held_lens"), &table = tensor(a[2], "block_table");
+        const int64_t dev = device_of(table, "block_table");
+        const int64_t n = held.dim() == 1 ? held.size(0) : -1;
+        dfc_release_args p;
+        std::memset(&p, 0, sizeof(p));
+        p.block_table = table_of(table, n, dev, p.table_stride, p.max_pages);
+        p.n_requests = narrow(n, "requests");
+        p.held_lens = vector<int32_t>(held, at::kInt, n, dev, "held_lens");
+        p.keep_lens = vector<int32_t>(tensor(a[1], "keep_lens"), at::kInt, n, dev, "keep_lens");
+        pool_of(a[3], a[4], a[5], dev, p);
+        p.page_size = count(a[6], "page_size");
+        p.window = count(a[7], "window");
+        p.sinks = count(a[8], "sinks");
+        p.status_dev = status_of(a[10], dev);
+        // the workspace, and the new cursor before it
+        const at::Tensor all = make({16 + DFC_RELEASE_WORKSPACE}, at::kByte, table);
+        at::Tensor t[1];
+        if (a[9] == Py_None)
+            t[0] = part(all, at::kLong, 0, 2);
+        else
+            written(t[0] = tensor(a[9], "out"));
+        p.cursor_out = vector<int64_t>(t[0], at::kLong, 2, dev, "out");
+        p.workspace_dev = reinterpret_cast<uint32_t *>(static_cast<uint8_t *>(all.data_ptr()) + 16);
+        written(table);
+        written(tensor(a[3], "free_pages"));
+        written(tensor(a[5], "shared"));
+        return answer(call(g_release, &p, stream_of(a[11], dev)), t);
+    });
+}
+
+// fork(context_lens, parents, block_table, free_pages, cursor, shared,
+//      page_size, fork_lens or None, out or None, status or None, stream)
+PyObject *fork(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 11);
+        const at::Tensor &context = tensor(a[0], "context_lens"), &table = tensor(a[2], "block_table");
+        const int64_t dev = device_of(table, "block_table");
+        const int64_t n = context.dim() == 1 ? context.size(0) : -1;
+        dfc_fork_args p;
+        std::memset(&p, 0, sizeof(p));
+        p.block_table = table_of(table, n, dev, p.table_stride, p.max_pages);
+        p.n_requests = narrow(n, "requests");
+        p.context_lens = vector<int32_t>(context, at::kInt, n, dev, "context_lens");
+        p.parents = vector<int32_t>(tensor(a[1], "parents"), at::kInt, n, dev, "parents");
+        pool_of(a[3], a[4], a[5], dev, p);
+        p.page_size = count(a[6], "page_size");
+        if (a[7] != Py_None) p.fork_lens = vector<int32_t>(tensor(a[7], "fork_lens"), at::kInt, n, dev, "fork_lens");
+        p.status_dev = status_of(a[9], dev);
+        at::Tensor t[4];  // context_lens, src, dst, cursor
+        if (a[8] == Py_None) {
+            const at::Tensor all = make({16 + 12 * n}, at::kByte, table);
+            t[3] = part(all, at::kLong, 0, 2);
+            for (int i = 0; i < 3; ++i) t[i] = part(all, at::kInt, 4 + i * n, n);
+        } else {
+            if (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 4) type_error("out must be a PagedFork");
+            for (int i = 0; i < 4; ++i) written(t[i] = tensor(PyTuple_GET_ITEM(a[8], i), "a field of out"));
+        }
+        p.context_out = vector<int32_t>(t[0], at::kInt, n, dev, "the fork's context_lens");
+        p.src = vector<int32_t>(t[1], at::kInt, n, dev, "the fork's src");
+        p.dst = vector<int32_t>(t[2], at::kInt, n, dev, "the fork's dst");
+        p.cursor_out = vector<int64_t>(t[3], at::kLong, 2, dev, "the fork's cursor");
+        written(table);
+        written(tensor(a[5], "shared"));
+        return answer(call(g_fork, &p, stream_of(a[10], dev)), t);
+    });
+}
+
+// compact(context_lens, block_table, free_pages, cursor, shared, page_size,
+//         out or None, status or None, stream)
+PyObject *compact(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 9);
+        const at::Tensor &context = tensor(a[0], "context_lens"), &table = tensor(a[1], "block_table");
+        const int64_t dev = device_of(table, "block_table");
+        const int64_t n = context.dim() == 1 ? context.size(0) : -1;
+        dfc_compact_args p;
+        std::memset(&p, 0, sizeof(p));
+        p.block_table = table_of(table, n, dev, p.table_stride, p.max_pages);
+        p.n_requests = narrow(n, "requests");
+        p.context_lens = vector<int32_t>(context, at::kInt, n, dev, "context_lens");
+        pool_of(a[2], a[3], a[4], dev, p);
+        p.page_size = count(a[5], "page_size");
+        p.status_dev = status_of(a[7], dev);
+        const int64_t half = p.n_pages / 2;
+        at::Tensor t[3];  // src, dst, used
+        if (a[6] == Py_None) {
+            const at::Tensor all = make({2 * half + 1}, at::kInt, table);
+            t[0] = part(all, at::kInt, 0, half);
+            t[1] = part(all, at::kInt, half, half);
+            t[2] = part(all, at::kInt, 2 * half, 1);
+        } else {
+            if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 3) type_error("out must be a PagedMoves");
+            for (int i = 0; i < 3; ++i) written(t[i] = tensor(PyTuple_GET_ITEM(a[6], i), "a field of out"));
+        }
+        p.src = vector<int32_t>(t[0], at::kInt, half, dev, "the moves' src");
+        p.dst = vector<int32_t>(t[1], at::kInt, half, dev, "the moves' dst");
+        p.used = vector<int32_t>(t[2], at::kInt, 1, dev, "the moves' used");
+        const at::Tensor work = make({int64_t(g_compact_workspace(p.n_pages))}, at::kByte, table);
+        p.workspace_dev = static_cast<uint32_t *>(work.data_ptr());
+        written(table);
+        written(tensor(a[2], "free_pages"));
+        written(tensor(a[4], "shared"));
+        return answer(call(g_compact, &p, stream_of(a[8], dev)), t);
+    });
+}
+
+// copy(caches, src, dst, status or None, stream): caches a sequence of pairs
+PyObject *copy(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 5);
+        const at::Tensor &src = tensor(a[1], "src");
+        const int64_t dev = device_of(src, "src");
+        const int64_t n = src.dim() == 1 ? src.size(0) : -1;
+        const int32_t *from = vector<int32_t>(src, at::kInt, n, dev, "src");
+        const int32_t *to = vector<int32_t>(tensor(a[2], "dst"), at::kInt, n, dev, "dst");
+        uint32_t *status = status_of(a[3], dev);
+        struct Items {  // released however the call ends
+            PyObject *of;
+            ~Items() { Py_XDECREF(of); }
+        };
+        const Items all{PySequence_Fast(a[0], "caches must be a sequence of pairs (k_cache, v_cache)")};
+        if (!all.of) throw Failed();
+        std::vector<dfc_paged_cache> caches(size_t(PySequence_Fast_GET_SIZE(all.of)));
+        std::vector<at::Tensor> tensors;
+        for (size_t i = 0; i < caches.size(); ++i) {
+            const Items pair{PySequence_Fast(PySequence_Fast_GET_ITEM(all.of, Py_ssize_t(i)),
+                                             "a cache must be a pair (k_cache, v_cache)")};
+            if (!pair.of) throw Failed();
+            if (PySequence_Fast_GET_SIZE(pair.of) != 2) type_error("a cache must be a pair (k_cache, v_cache)");
+            const at::Tensor &k = tensor(PySequence_Fast_GET_ITEM(pair.of, 0), "k_cache");
+            const at::Tensor &v = tensor(PySequence_Fast_GET_ITEM(pair.of, 1), "v_cache");
+            cache_of(k, v, dev, caches[i]);
+            tensors.push_back(k);
+            tensors.push_back(v);
+        }
+        for (const at::Tensor &t : tensors) written(t);
+        const at::Tensor none[1];
+        return answer(call(g_copy, caches.data(), uint32_t(caches.size()), from, to, narrow(n, "the length of src"), status,
+                           stream_of(a[4], dev)),
+                      none);
+    });
+}
+
+uint32_t type_of(const at::Tensor &t, const char *name) {
+    switch (t.scalar_type()) {
+        case at::kFloat: return DFC_F32;
+        case at::kBFloat16: return DFC_BF16;
+        case at::kHalf: return DFC_F16;
+        default: type_error("%s must be float32, bfloat16 or float16", name);
+    }
+}
+
+// Rows of logits.
+const void *logits_of(const at::Tensor &t, const char *name, int64_t dev, int64_t &stride) {
+    if (t.dim() != 2 || !on(t, dev)) type_error("%s must be a tensor of shape (rows, vocabulary) on the call's device", name);
+    if (t.stride(1) != 1 && t.size(1) > 1) value_error("the values of a row of %s must be contiguous", name);
+    stride = t.size(0) > 1 ? t.stride(0) : t.size(1);  // a single row's stride says nothing
+    return t.data_ptr();
+}
+
+void verify_sizes(const at::Tensor &logits, const at::Tensor &cu, dfc_verify_args &p) {
+    if (logits.dim() != 2) type_error("logits must be a tensor of shape (rows, vocabulary)");
+    if (cu.dim() != 1 || cu.size(0) < 1) type_error("cu_rows must be a one-dimensional tensor of requests + 1 elements");
+    p.rows = uint64_t(logits.size(0));
+    p.vocab = narrow(logits.size(1), "the vocabulary");
+    p.n_requests = narrow(cu.size(0) - 1, "requests");
+    p.dtype = type_of(logits, "logits");
+}
+
+// verify(logits, cu_rows, drafts, uniforms, draft_logits or None, temperature
+//        or None, out or None, workspace or None, status or None, stream)
+PyObject *verify(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 10);
+        const at::Tensor &logits = tensor(a[0], "logits"), &cu = tensor(a[1], "cu_rows");
+        const int64_t dev = device_of(logits, "logits");
+        dfc_verify_args p;
+        std::memset(&p, 0, sizeof(p));
+        verify_sizes(logits, cu, p);
+        const int64_t rows = logits.size(0), n = p.n_requests;
+        p.logits_dev = logits_of(logits, "logits", dev, p.logits_stride);
+        if (a[4] != Py_None) {
+            const at::Tensor &draft = tensor(a[4], "draft_logits");
+            if (draft.scalar_type() != logits.scalar_type()) type_error("draft_logits must be of the type of logits");
+            if (draft.dim() != 2 || draft.sizes() != logits.sizes()) value_error("draft_logits must have the shape of logits");
+            p.draft_logits_dev = logits_of(draft, "draft_logits", dev, p.draft_stride);
+        }
+        p.cu_rows = vector<int32_t>(cu, at::kInt, n + 1, dev, "cu_rows");
+        p.drafts = vector<int64_t>(tensor(a[2], "drafts"), at::kLong, rows, dev, "drafts");
+        p.uniforms = vector<float>(tensor(a[3], "uniforms"), at::kFloat, rows, dev, "uniforms");
+        if (a[5] != Py_None) p.temperature = vector<float>(tensor(a[5], "temperature"), at::kFloat, n, dev, "temperature");
+        at::Tensor t[2];  // accepted, tokens
+        if (a[6] == Py_None) {
+            const at::Tensor all = make({12 * n}, at::kByte, logits);
+            t[1] = part(all, at::kLong, 0, n);
+            t[0] = part(all, at::kInt, 2 * n, n);
+        } else {
+            if (!PyTuple_Check(a[6]) || PyTuple_GET_SIZE(a[6]) != 2) type_error("out must be a Verified");
+            for (int i = 0; i < 2; ++i) written(t[i] = tensor(PyTuple_GET_ITEM(a[6], i), "a field of out"));
+        }
+        p.accepted = vector<int32_t>(t[0], at::kInt, n, dev, "accepted");
+        p.tokens = vector<int64_t>(t[1], at::kLong, n, dev, "tokens");
+        at::Tensor work;
+        if (a[7] == Py_None) {
+            uint64_t bytes = 0;
+            const dfc_status s = g_verify_workspace(&p, &bytes);
+            if (s != DFC_OK) return answer(s, t);
+            work = make({int64_t(bytes)}, at::kByte, logits);
+        } else {
+            work = tensor(a[7], "workspace");
+            if (!on(work, dev) || !work.is_contiguous())
+                type_error("workspace must be a contiguous tensor on the call's device");
+            written(work);
+        }
+        p.workspace_dev = work.data_ptr();
+        p.workspace_bytes = uint64_t(work.nbytes());
+        p.status_dev = status_of(a[8], dev);
+        return answer(call(g_verify, &p, stream_of(a[9], dev)), t);
+    });
+}
+
+// verify_workspace(logits, cu_rows, draft_logits or None) -> (status, bytes)
+PyObject *verify_workspace(PyObject *, PyObject *const *a, Py_ssize_t n_args) {
+    return guarded([&]() -> PyObject * {
+        want(n_args, 3);
+        const at::Tensor &logits = tensor(a[0], "logits");
+        dfc_verify_args p;
+        std::memset(&p, 0, sizeof(p));
+        verify_sizes(logits, tensor(a[1], "cu_rows"), p);
+        if (a[2] != Py_None) p.draft_logits_dev = &p;  // (whether there are any)
+        uint64_t bytes = 0;
+        const dfc_status s = g_verify_workspace(&p, &bytes);
+        return Py_BuildValue("iK", int(s), static_cast<unsigned long long>(bytes));
+    });
+}
+
 template <PyObject *(*F)(PyObject *, PyObject *const *, Py_ssize_t)>
 PyMethodDef method(const char *name) {
     return {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(F)), METH_FASTCALL, nullptr};
 }
 
-PyMethodDef g_methods[] = {method<setup>("setup"),         method<plan>("plan"),           method<append>("append"),
-                           method<attention>("attention"), method<workspace>("workspace"), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef g_methods[] = {method<setup>("setup"),         method<plan>("plan"),       method<append>("append"),
+                           method<attention>("attention"), method<workspace>("workspace"), method<release>("release"),
+                           method<fork>("fork"),           method<compact>("compact"), method<copy>("copy"),
+                           method<verify>("verify"),       method<verify_workspace>("verify_workspace"),
+                           {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_paged", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,0 +1,720 @@
+// dfc_pages.hip - pages of the cache given back, shared, moved and copied.
+//
+// shared[p] is the number of requests that hold page p beyond the first.
+//
+// dfc_paged_release.  A request gives up entries of its row; every one takes a
+// holder off its page, and a page whose count passes below zero is free.  The
+// counts are atomic sums, so which pages are free does not depend on any
+// order; they go to the ring in ascending order of their numbers, so their
+// places do not either.
+//
+// dfc_paged_fork.  Full pages of the parent's first tokens gain a holder, the
+// one that the tokens fill in part gets a new page off the ring: the i-th such
+// copy of the call takes the i-th free page.
+//
+// dfc_paged_compact.  With the held and the free pages in ascending order
+// a_0 < a_1 < ..., U of them held, page a_i stays if i < U and is held, is a
+// place to move to if i < U and is free, and is on the ring afterwards if
+// i >= U: all of it prefix sums of two flags over the pages.
+#include <hip/hip_runtime.h>
+
+#include <algorithm>
+#include <cstdint>
+#include <cstring>
+
+#include "dfc.h"
+#include "dfc_decode_core.h"
+#include "dfc_paged.h"
+
+namespace {
+
+constexpr uint32_t kRowThreads = 256;    // of a workgroup that walks a request's row
+constexpr uint32_t kPageThreads = 1024;  // of one that walks a slab of pages
+constexpr uint32_t kPageWaves = kPageThreads / kWave;
+constexpr uint32_t kMostSlabs = DFC_RELEASE_WORKSPACE / 4;
+constexpr uint32_t kMostRequests = 65536;
+
+__device__ __forceinline__ void tell(uint32_t *status, uint32_t bad) {
+    if (bad && status) atomicOr(status, bad);
+}
+
+__device__ __forceinline__ uint64_t lanes_below() { return (uint64_t(1) << (threadIdx.x % kWave)) - 1u; }
+
+// A cursor's free entries; none where it does not fit the ring.
+struct Ring {
+    uint64_t head, size;
+    bool ok;
+};
+__device__ __forceinline__ Ring ring_of(const int64_t *cursor, uint32_t n_ring) {
+    const int64_t head = cursor[0], tail = cursor[1];
+    const bool ok = head >= 0 && tail >= head && uint64_t(tail - head) <= n_ring;
+    return Ring{ok ? uint64_t(head) : 0u, ok ? uint64_t(tail - head) : 0u, ok};
+}
+
+// The sum of a value over the workgroup, for every thread.  `part` is LDS for
+// one value a wavefront.
+template <uint32_t NT>
+__device__ __forceinline__ uint32_t sum_of(uint32_t x, uint32_t *part) {
+    const uint32_t w = __builtin_amdgcn_readlane(wave_inclusive_scan(x), kWave - 1);
+    __syncthreads();  // the part before has been read
+    if (threadIdx.x % kWave == 0) part[threadIdx.x / kWave] = w;
+    __syncthreads();
+    uint32_t all = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < NT / kWave; ++k) all += part[k];
+    return all;
+}
+
+// ------------------------------------------------------- slabs of pages
+
+// The pages are cut into equal slabs, one a workgroup, and those into equal
+// runs, one a wavefront: consecutive lanes have consecutive pages, kAtOnce
+// loads are under way together.
+constexpr uint32_t kAtOnce = 8;
+constexpr uint32_t kSlab = kPageThreads * kAtOnce;
+
+struct Slabs {
+    uint32_t count, rounds;  // slabs; rounds of kSlab pages in each
+};
+Slabs slabs_of(uint32_t n_pages) {
+    const uint32_t least = uint32_t(dfc::ceil_div(uint64_t(n_pages), uint64_t(kSlab)));
+    const uint32_t rounds = uint32_t(dfc::ceil_div(uint64_t(least), uint64_t(kMostSlabs)));
+    return Slabs{uint32_t(dfc::ceil_div(uint64_t(least), uint64_t(std::max(rounds, 1u)))), std::max(rounds, 1u)};
+}
+
+// f(page, there, value of the page) for the pages of the calling wavefront's
+// run, in order, all lanes at a time.
+template <typename F>
+__device__ __forceinline__ void each_page(const int32_t *of, uint32_t n_pages, uint32_t rounds, F &&f) {
+    const uint32_t run = rounds * kAtOnce * kWave;
+    const uint64_t first = (uint64_t(blockIdx.x) * kPageWaves + threadIdx.x / kWave) * run + threadIdx.x % kWave;
+    for (uint32_t r = 0; r < rounds; ++r) {
+        int32_t v[kAtOnce];
+        const uint64_t base = first + uint64_t(r) * kAtOnce * kWave;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) v[i] = base + i * kWave < n_pages ? of[base + i * kWave] : 0;
+#pragma unroll
+        for (uint32_t i = 0; i < kAtOnce; ++i) f(uint32_t(base + i * kWave), base + i * kWave < n_pages, v[i]);
+    }
+}
+
+// ---------------------------------------------------------------- release
+
+struct ReleaseArgs {
+    dfc_release_args a;
+    uint32_t shift, slabs, rounds;
+};
+
+// A workgroup takes a request at a time and its lanes the entries that it
+// gives up.
+__global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
+    const dfc_release_args &a = p.a;
+    const uint32_t P = a.page_size;
+    uint32_t bad = 0;
+    for (uint32_t r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
+        const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
+        if (held < 0 || keep < 0 || keep > held) {
+            bad |= kStatusCorrupt;
+            continue;
+        }
+        uint32_t end = (uint32_t(held) + P - 1u) >> p.shift;
+        if (end > a.max_pages) {
+            bad |= uint32_t(DFC_ESIZE);
+            end = a.max_pages;
+        }
+        const uint32_t begin = min((uint32_t(keep) + P - 1u) >> p.shift, end);
+        // behind the window: [hole, hole + n_hole)
+        const uint32_t hole = uint32_t((uint64_t(a.sinks) + P - 1u) >> p.shift);
+        uint32_t n_hole = 0;
+        if (a.window && uint32_t(keep) + 1u > a.window) {
+            const uint32_t passed = min((uint32_t(keep) + 1u - a.window) >> p.shift, begin);
+            n_hole = passed > hole ? passed - hole : 0u;
+        }
+        int32_t *row = a.block_table + int64_t(r) * a.table_stride;
+        for (uint32_t j = threadIdx.x; j < n_hole + (end - begin); j += kRowThreads) {
+            const uint32_t i = j < n_hole ? hole + j : begin + (j - n_hole);
+            const int32_t page = row[i];
+            if (page < 0) continue;
+            row[i] = -1;
+            if (uint32_t(page) >= a.n_pages)
+                bad |= kStatusCorrupt;
+            else if (atomicSub(a.shared + page, 1) < 0)
+                bad |= kStatusCorrupt;  // given up more often than held
+        }
+    }
+    tell(a.status_dev, bad);
+}
+
+// Free pages of every slab.
+__global__ __launch_bounds__(kPageThreads) void freed_count_kernel(ReleaseArgs p) {
+    __shared__ uint32_t part[kPageWaves];
+    uint32_t n = 0;
+    each_page(p.a.shared, p.a.n_pages, p.rounds, [&](uint32_t, bool, int32_t v) { n += v < 0; });
+    const uint32_t all = sum_of<kPageThreads>(n, part);
+    if (threadIdx.x == 0) p.a.workspace_dev[blockIdx.x] = all;
+}
+
+// The free pages to the ring, their counts to 0, and the cursor.  One slab
+// counts its pages itself.
+__global__ __launch_bounds__(kPageThreads) void freed_write_kernel(ReleaseArgs p) {
+    __shared__ uint32_t part[kPageWaves], of_wave[kPageWaves];
+    const dfc_release_args &a = p.a;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave;
+    uint32_t bad = 0;
+    uint32_t before = 0, total = 0;
+    if (p.slabs > 1) {
+        uint32_t mine = 0, all = 0;
+        for (uint32_t k = tid; k < p.slabs; k += kPageThreads) {
+            const uint32_t n = a.workspace_dev[k];
+            all += n;
+            if (k < blockIdx.x) mine += n;
+        }
+        before = sum_of<kPageThreads>(mine, part);
+        total = sum_of<kPageThreads>(all, part);
+    }
+    uint32_t n = 0;
+    each_page(a.shared, a.n_pages, p.rounds, [&](uint32_t, bool, int32_t v) { n += uint32_t(__popcll(__ballot(v < 0))); });
+    if (tid % kWave == 0) of_wave[wave] = n;
+    __syncthreads();
+    uint32_t here = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kPageWaves; ++k) {
+        if (k < wave) before += of_wave[k];
+        here += of_wave[k];
+    }
+    if (p.slabs == 1) total = here;
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    const bool fits = ring.ok && total <= a.n_ring - ring.size;
+    if (!fits) bad |= kStatusCorrupt;
+    if (n) {  // (of the wavefront)
+        // the place of the wavefront's next page
+        uint64_t to = (ring.head + ring.size + before) % a.n_ring;
+        each_page(a.shared, a.n_pages, p.rounds, [&](uint32_t page, bool, int32_t v) {
+            const uint64_t who = __ballot(v < 0);
+            if (v < 0) {
+                uint64_t at = to + uint32_t(__popcll(who & lanes_below()));
+                if (at >= a.n_ring) at %= a.n_ring;
+                if (fits) a.free_pages[at] = int32_t(page);
+                a.shared[page] = 0;
+            }
+            to += uint32_t(__popcll(who));
+        });
+    }
+    // requests cut inside a page that others hold
+    for (uint32_t r = blockIdx.x * kPageThreads + tid; r < a.n_requests; r += gridDim.x * kPageThreads) {
+        const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
+        if (keep <= 0 || keep >= held || !(uint32_t(keep) & (a.page_size - 1u))) continue;
+        const uint32_t i = uint32_t(keep) >> p.shift;
+        if (i >= a.max_pages) continue;
+        const int32_t page = a.block_table[int64_t(r) * a.table_stride + i];
+        if (page >= 0 && uint32_t(page) < a.n_pages && a.shared[page] > 0) bad |= uint32_t(DFC_EUNSUPPORTED);
+    }
+    if (blockIdx.x == 0 && tid == 0) {
+        const int64_t head = a.cursor[0], tail = a.cursor[1];
+        a.cursor_out[0] = head;
+        a.cursor_out[1] = fits ? tail + int64_t(total) : tail;
+    }
+    tell(a.status_dev, bad);
+}
+
+// ------------------------------------------------------------------- fork
+
+struct ForkArgs {
+    dfc_fork_args a;
+    uint32_t shift;
+};
+
+// What becomes of request r: whether it is forked (if the ring has its page),
+// how many tokens it gets, and the page to copy (-1: none).
+struct Child {
+    int32_t parent, tokens, page;
+    bool forked;
+};
+__device__ __forceinline__ Child child_of(const dfc_fork_args &a, uint32_t shift, uint32_t r, uint32_t &bad) {
+    Child c{a.parents[r], 0, -1, false};
+    if (c.parent == -1) return c;
+    if (c.parent < 0 || uint32_t(c.parent) >= a.n_requests || a.parents[c.parent] != -1 || a.context_lens[r] != 0) {
+        bad |= kStatusCorrupt;
+        return c;
+    }
+    const int32_t has = a.context_lens[c.parent];
+    c.tokens = a.fork_lens ? a.fork_lens[r] : has;
+    if (c.tokens < 0 || c.tokens > has) {
+        bad |= kStatusCorrupt;
+        return c;
+    }
+    const uint32_t full = uint32_t(c.tokens) >> shift;
+    const bool ends = uint32_t(c.tokens) & (a.page_size - 1u);
+    if (full + ends > a.max_pages) {
+        bad |= uint32_t(DFC_ESIZE);
+        return c;
+    }
+    if (ends) {
+        c.page = a.block_table[int64_t(c.parent) * a.table_stride + full];
+        if (c.page < 0 || uint32_t(c.page) >= a.n_pages) {
+            bad |= kStatusCorrupt;
+            return c;
+        }
+    }
+    c.forked = true;
+    return c;
+}
+
+// A workgroup a request.  Those that are forked, and the last one for the
+// cursor, count the pages that the requests before them take.
+__global__ __launch_bounds__(kRowThreads) void fork_kernel(ForkArgs p) {
+    __shared__ uint32_t part[kRowThreads / kWave];
+    const dfc_fork_args &a = p.a;
+    const uint32_t r = blockIdx.x, tid = threadIdx.x;
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    uint32_t bad = ring.ok ? 0u : kStatusCorrupt, unused = 0;
+    if (!a.n_requests) {
+        if (tid == 0) a.cursor_out[0] = a.cursor[0], a.cursor_out[1] = a.cursor[1], tell(a.status_dev, bad);
+        return;
+    }
+    Child c = child_of(a, p.shift, r, bad);
+    const bool last = r == a.n_requests - 1u;
+    uint32_t before = 0;
+    if (last || (c.forked && c.page >= 0)) {
+        for (uint32_t k = tid; k < r; k += kRowThreads) {
+            const Child o = child_of(a, p.shift, k, unused);
+            before += o.forked && o.page >= 0;
+        }
+        before = sum_of<kRowThreads>(before, part);
+    }
+    if (last && tid == 0) {
+        const uint64_t taken = min(uint64_t(before) + (c.forked && c.page >= 0), ring.size);
+        a.cursor_out[0] = a.cursor[0] + int64_t(taken);
+        a.cursor_out[1] = a.cursor[1];
+    }
+    int32_t page = -1;
+    if (c.forked && c.page >= 0) {
+        if (before >= ring.size) {
+            bad |= uint32_t(DFC_ESIZE);
+            c.forked = false;
+        } else {
+            page = a.free_pages[(ring.head + before) % a.n_ring];
+            if (page < 0 || uint32_t(page) >= a.n_pages) {
+                bad |= kStatusCorrupt;
+                c.forked = false;
+            }
+        }
+    }
+    if (tid == 0) {
+        a.context_out[r] = c.parent == -1 ? a.context_lens[r] : c.forked ? c.tokens : max(a.context_lens[r], 0);
+        a.src[r] = c.forked ? c.page : -1;
+        a.dst[r] = c.forked ? page : -1;
+    }
+    if (c.forked) {
+        const int32_t *from = a.block_table + int64_t(c.parent) * a.table_stride;
+        int32_t *to = a.block_table + int64_t(r) * a.table_stride;
+        const uint32_t full = uint32_t(c.tokens) >> p.shift;
+        for (uint32_t i = tid; i < full; i += kRowThreads) {
+            int32_t x = from[i];
+            if (x >= 0 && uint32_t(x) >= a.n_pages) {
+                bad |= kStatusCorrupt;
+                x = -1;
+            }
+            to[i] = x;
+            if (x >= 0) atomicAdd(a.shared + x, 1);
+        }
+        if (tid == 0 && page >= 0) to[full] = page;
+    }
+    tell(a.status_dev, bad);
+}
+
+// ---------------------------------------------------------------- compact
+
+constexpr int32_t kHeld = 1, kFree = 2;
+
+struct CompactArgs {
+    dfc_compact_args a;
+    uint32_t shift, slabs, rounds;
+    int32_t *flags;              // per page: kHeld | kFree
+    int32_t *place;              // its own number, -1 if it is not held, -2 - k if it is the k-th held one and moves
+    uint32_t *held, *either;     // per slab
+    uint32_t *wrong;             // ring and tables contradict each other
+    uint32_t *stay;              // held pages that do not move
+};
+
+__global__ __launch_bounds__(kRowThreads) void compact_clear_kernel(CompactArgs p) {
+    const dfc_compact_args &a = p.a;
+    for (uint32_t i = blockIdx.x * kRowThreads + threadIdx.x; i < a.n_pages; i += gridDim.x * kRowThreads) {
+        p.flags[i] = 0;
+        if (i < a.n_pages / 2u) a.src[i] = a.dst[i] = -1;
+    }
+    if (blockIdx.x == 0 && threadIdx.x == 0) *p.wrong = *p.stay = 0;
+}
+
+// Workgroups go through the requests' rows, then through the ring.
+__global__ __launch_bounds__(kRowThreads) void compact_mark_kernel(CompactArgs p) {
+    const dfc_compact_args &a = p.a;
+    uint32_t bad = 0;
+    bool wrong = false;
+    for (uint32_t r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
+        const int32_t n = a.context_lens[r];
+        if (n < 0) {
+            bad |= kStatusCorrupt;
+            continue;
+        }
+        uint32_t end = (uint32_t(n) + a.page_size - 1u) >> p.shift;
+        if (end > a.max_pages) {
+            bad |= uint32_t(DFC_ESIZE);
+            end = a.max_pages;
+        }
+        const int32_t *row = a.block_table + int64_t(r) * a.table_stride;
+        for (uint32_t i = threadIdx.x; i < end; i += kRowThreads) {
+            const int32_t page = row[i];
+            if (page < 0) continue;
+            if (uint32_t(page) < a.n_pages)
+                atomicOr(p.flags + page, kHeld);
+            else
+                wrong = true;
+        }
+    }
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    wrong |= !ring.ok;
+    for (uint64_t i = uint64_t(blockIdx.x) * kRowThreads + threadIdx.x; i < ring.size; i += uint64_t(gridDim.x) * kRowThreads) {
+        const int32_t page = a.free_pages[(ring.head + i) % a.n_ring];
+        if (page >= 0 && uint32_t(page) < a.n_pages)
+            wrong |= (atomicOr(p.flags + page, kFree) & kFree) != 0;  // twice on the ring
+        else
+            wrong = true;
+    }
+    if (wrong) atomicOr(p.wrong, 1u);
+    tell(a.status_dev, bad | (wrong ? kStatusCorrupt : 0u));
+}
+
+__global__ __launch_bounds__(kPageThreads) void compact_count_kernel(CompactArgs p) {
+    __shared__ uint32_t part[kPageWaves];
+    uint32_t held = 0, either = 0;
+    bool both = false;
+    each_page(p.flags, p.a.n_pages, p.rounds, [&](uint32_t, bool, int32_t v) {
+        held += (v & kHeld) != 0;
+        either += v != 0;
+        both |= v == (kHeld | kFree);
+    });
+    held = sum_of<kPageThreads>(held, part);
+    either = sum_of<kPageThreads>(either, part);
+    if (threadIdx.x == 0) p.held[blockIdx.x] = held, p.either[blockIdx.x] = either;
+    if (both) atomicOr(p.wrong, 1u);
+    tell(p.a.status_dev, both ? kStatusCorrupt : 0u);
+}
+
+__global__ __launch_bounds__(kPageThreads) void compact_place_kernel(CompactArgs p) {
+    __shared__ uint32_t part[kPageWaves], held_of[kPageWaves], either_of[kPageWaves];
+    const dfc_compact_args &a = p.a;
+    const uint32_t tid = threadIdx.x, wave = tid / kWave;
+    uint32_t held = 0, h = 0, e = 0;  // held pages; held, and either, in the slabs before this one
+    {
+        uint32_t all = 0, mh = 0, me = 0;
+        for (uint32_t k = tid; k < p.slabs; k += kPageThreads) {
+            const uint32_t x = p.held[k], y = p.either[k];
+            all += x;
+            if (k < blockIdx.x) mh += x, me += y;
+        }
+        held = sum_of<kPageThreads>(all, part);
+        h = sum_of<kPageThreads>(mh, part);
+        e = sum_of<kPageThreads>(me, part);
+    }
+    if (blockIdx.x == 0 && tid == 0) *a.used = int32_t(held);
+    if (*p.wrong) {
+        each_page(p.flags, a.n_pages, p.rounds, [&](uint32_t page, bool there, int32_t) {
+            if (there) p.place[page] = int32_t(page);
+        });
+        return;
+    }
+    uint32_t nh = 0, ne = 0;
+    each_page(p.flags, a.n_pages, p.rounds, [&](uint32_t, bool, int32_t v) {
+        nh += uint32_t(__popcll(__ballot(v & kHeld)));
+        ne += uint32_t(__popcll(__ballot(v != 0)));
+    });
+    if (tid % kWave == 0) held_of[wave] = nh, either_of[wave] = ne;
+    __syncthreads();
+    for (uint32_t k = 0; k < wave; ++k) h += held_of[k], e += either_of[k];
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    const uint64_t below = lanes_below();
+    each_page(p.flags, a.n_pages, p.rounds, [&](uint32_t page, bool there, int32_t v) {
+        const uint64_t hs = __ballot(v & kHeld), es = __ballot(v != 0);
+        const uint32_t rank = e + uint32_t(__popcll(es & below)), before = h + uint32_t(__popcll(hs & below));
+        if (there) {
+            int32_t to = -1;
+            if (v == kHeld) to = rank < held ? int32_t(page) : -2 - int32_t(before);
+            p.place[page] = to;
+            if (v == kFree && rank < held) a.dst[rank - before] = int32_t(page);
+            // (the first `stay` held pages are those up to a_{U-1})
+            if (v && rank + 1u == held) *p.stay = before + (v == kHeld);
+            if (v && rank >= held) a.free_pages[(ring.head + (rank - held)) % a.n_ring] = int32_t(page);
+        }
+        h += uint32_t(__popcll(hs));
+        e += uint32_t(__popcll(es));
+    });
+}
+
+// The pages that move: the lists and their holders; and the rows.
+__global__ __launch_bounds__(kRowThreads) void compact_finish_kernel(CompactArgs p) {
+    const dfc_compact_args &a = p.a;
+    if (*p.wrong) return;
+    const uint32_t stay = *p.stay;
+    for (uint32_t i = blockIdx.x * kRowThreads + threadIdx.x; i < a.n_pages; i += gridDim.x * kRowThreads) {
+        const int32_t k = p.place[i];
+        if (k > -2) continue;
+        const uint32_t move = uint32_t(-2 - k) - stay;
+        const int32_t to = a.dst[move];
+        a.src[move] = int32_t(i);
+        a.shared[to] = a.shared[i];
+        a.shared[i] = 0;
+    }
+    for (uint32_t r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
+        const int32_t n = a.context_lens[r];
+        if (n < 0) continue;
+        const uint32_t end = min((uint32_t(n) + a.page_size - 1u) >> p.shift, a.max_pages);
+        int32_t *row = a.block_table + int64_t(r) * a.table_stride;
+        for (uint32_t i = threadIdx.x; i < end; i += kRowThreads) {
+            const int32_t page = row[i];
+            if (page < 0 || uint32_t(page) >= a.n_pages) continue;
+            const int32_t k = p.place[page];
+            if (k <= -2) row[i] = a.dst[uint32_t(-2 - k) - stay];
+        }
+    }
+}
+
+// ------------------------------------------------------------------- copy
+
+using U4 = __attribute__((ext_vector_type(4))) uint32_t;
+constexpr uint32_t kCopyThreads = 256, kCopyCaches = 64, kCopyList = 1024;
+
+struct CopyArgs {
+    U4 *base[2 * kCopyCaches];  // K and V of every cache
+    const int32_t *src, *dst;
+    uint32_t *status;
+    uint32_t n, n_pages;
+    uint32_t parts;                // bases
+    uint32_t groups;               // pair i belongs to group i mod groups
+    uint32_t pieces;               // 16-byte pieces of a page
+    uint32_t step_pairs, step_pieces;  // kCopyThreads = step_pairs pieces + step_pieces
+    uint32_t heads, row;           // for pages that are not one run: heads; pieces of a head
+    uint32_t k_stride[3], v_stride[3];  // in pieces
+};
+
+// A workgroup copies the pages of one group of pairs in one K or V: the pairs
+// that are none are passed over first, and the threads then go through the
+// others' pieces.  Consecutive pairs are dealt out to different groups, since
+// a list is often filled in front only.
+template <bool Run>
+__global__ __launch_bounds__(kCopyThreads) void copy_kernel(CopyArgs a) {
+    __shared__ int2 list[kCopyList];
+    __shared__ uint32_t filled;
+    const uint32_t part = blockIdx.x % a.parts, group = blockIdx.x / a.parts, tid = threadIdx.x;
+    if (tid == 0) filled = 0;
+    __syncthreads();
+    bool bad = false;
+    for (uint64_t i = group + uint64_t(tid) * a.groups; i < a.n; i += uint64_t(kCopyThreads) * a.groups) {
+        const int32_t from = a.src[i], to = a.dst[i];
+        if (from < 0 || to < 0) continue;
+        if (uint32_t(from) >= a.n_pages || uint32_t(to) >= a.n_pages) {
+            bad = true;
+            continue;
+        }
+        list[atomicAdd(&filled, 1u)] = int2{from, to};
+    }
+    __syncthreads();
+    tell(a.status, bad ? kStatusCorrupt : 0u);
+    const uint32_t n = filled;
+    U4 *base = a.base[part];
+    const uint32_t page_stride = part & 1u ? a.v_stride[0] : a.k_stride[0];
+    const uint32_t place_stride = part & 1u ? a.v_stride[1] : a.k_stride[1];
+    const uint32_t head_stride = part & 1u ? a.v_stride[2] : a.k_stride[2];
+    uint32_t pair = tid / a.pieces, piece = tid % a.pieces;
+    auto next = [&]() {
+        pair += a.step_pairs;
+        piece += a.step_pieces;
+        if (piece >= a.pieces) piece -= a.pieces, ++pair;
+    };
+    while (pair < n) {
+        constexpr uint32_t kLoads = 8;
+        U4 x[kLoads];
+        uint64_t to[kLoads];
+        bool there[kLoads];
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; ++i) {
+            // (past the last pair, its piece again, not stored)
+            there[i] = pair < n;
+            const int2 l = list[min(pair, n - 1u)];
+            uint32_t in_page = piece;
+            if constexpr (!Run) {
+                const uint32_t head = piece / a.row;
+                in_page = head / a.heads * place_stride + head % a.heads * head_stride + piece % a.row;
+            }
+            x[i] = base[uint64_t(uint32_t(l.x)) * page_stride + in_page];
+            to[i] = uint64_t(uint32_t(l.y)) * page_stride + in_page;
+            next();
+        }
+#pragma unroll
+        for (uint32_t i = 0; i < kLoads; ++i)
+            if (there[i]) base[to[i]] = x[i];
+    }
+}
+
+// ----------------------------------------------------------------- launch
+
+bool pool_ok(uint32_t n_requests, uint32_t max_pages, uint32_t page_size, uint32_t n_ring, uint32_t n_pages,
+             const void *table, int64_t stride, const void *lens, const void *ring, const void *cursor,
+             const void *shared) {
+    if (!dfc::is_pow2(page_size) || !n_ring || n_ring > 0x7fffffffu || !n_pages || n_pages > (1u << 30)) return false;
+    if (!ring || !cursor || !shared) return false;
+    return !n_requests || (table && lens && max_pages && max_pages <= 0x7fffffffu && stride >= int64_t(max_pages));
+}
+
+bool aligned(const void *p, uintptr_t to) { return (reinterpret_cast<uintptr_t>(p) & (to - 1u)) == 0; }
+
+dfc_status launched() { return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP; }
+
+}  // namespace
+
+extern "C" {
+
+dfc_status dfc_paged_release(const dfc_release_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_release_args &a = *args;
+    if (!pool_ok(a.n_requests, a.max_pages, a.page_size, a.n_ring, a.n_pages, a.block_table, a.table_stride, a.held_lens,
+                 a.free_pages, a.cursor, a.shared))
+        return DFC_EINVAL;
+    if ((a.n_requests && !a.keep_lens) || !a.cursor_out || a.cursor_out == a.cursor) return DFC_EINVAL;
+    if (!a.workspace_dev || !aligned(a.workspace_dev, 16)) return DFC_EINVAL;
+    if (a.window > 0x7fffffffu || a.sinks > 0x7fffffffu) return DFC_EINVAL;
+    if (a.n_requests > kMostRequests) return DFC_EUNSUPPORTED;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Slabs s = slabs_of(a.n_pages);
+    const ReleaseArgs p{a, dfc::log2_of(a.page_size), s.count, s.rounds};
+    if (a.n_requests) hipLaunchKernelGGL(release_kernel, dim3(std::min(a.n_requests, 4096u)), dim3(kRowThreads), 0, st, p);
+    if (s.count > 1) hipLaunchKernelGGL(freed_count_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
+    hipLaunchKernelGGL(freed_write_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
+    return launched();
+}
+
+dfc_status dfc_paged_fork(const dfc_fork_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_fork_args &a = *args;
+    if (!pool_ok(a.n_requests, a.max_pages, a.page_size, a.n_ring, a.n_pages, a.block_table, a.table_stride, a.context_lens,
+                 a.free_pages, a.cursor, a.shared))
+        return DFC_EINVAL;
+    if (!a.cursor_out || a.cursor_out == a.cursor) return DFC_EINVAL;
+    // every workgroup reads the lengths and the parents while others write
+    if (a.n_requests && (!a.parents || !a.context_out || !a.src || !a.dst || a.src == a.dst)) return DFC_EINVAL;
+    for (const int32_t *out : {a.context_out, a.src, a.dst})
+        if (a.n_requests && (out == a.context_lens || out == a.parents || out == a.fork_lens)) return DFC_EINVAL;
+    if (a.n_requests > kMostRequests) return DFC_EUNSUPPORTED;
+    const ForkArgs p{a, dfc::log2_of(a.page_size)};
+    hipLaunchKernelGGL(fork_kernel, dim3(std::max(a.n_requests, 1u)), dim3(kRowThreads), 0, static_cast<hipStream_t>(stream),
+                       p);
+    return launched();
+}
+
+uint64_t dfc_paged_compact_workspace(uint32_t n_pages) {
+    return uint64_t(n_pages) * 8u + 2u * kMostSlabs * 4u + 16u;
+}
+
+dfc_status dfc_paged_compact(const dfc_compact_args *args, void *stream) {
+    if (!args) return DFC_EINVAL;
+    const dfc_compact_args &a = *args;
+    if (!pool_ok(a.n_requests, a.max_pages, a.page_size, a.n_ring, a.n_pages, a.block_table, a.table_stride, a.context_lens,
+                 a.free_pages, a.cursor, a.shared))
+        return DFC_EINVAL;
+    if (!a.used || (a.n_pages > 1 && (!a.src || !a.dst || a.src == a.dst))) return DFC_EINVAL;
+    if (!a.workspace_dev || !aligned(a.workspace_dev, 16)) return DFC_EINVAL;
+    if (a.n_requests > kMostRequests) return DFC_EUNSUPPORTED;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    const Slabs s = slabs_of(a.n_pages);
+    CompactArgs p;
+    std::memset(&p, 0, sizeof(p));
+    p.a = a;
+    p.shift = dfc::log2_of(a.page_size);
+    p.slabs = s.count;
+    p.rounds = s.rounds;
+    uint32_t *work = a.workspace_dev;
+    p.wrong = work;
+    p.stay = work + 1;
+    p.held = work + 4;
+    p.either = p.held + kMostSlabs;
+    p.flags = reinterpret_cast<int32_t *>(p.either + kMostSlabs);
+    p.place = p.flags + a.n_pages;
+    const uint32_t pages = std::min(uint32_t(dfc::ceil_div(uint64_t(a.n_pages), uint64_t(kRowThreads))), 2048u);
+    const uint32_t ring = std::min(uint32_t(dfc::ceil_div(uint64_t(a.n_ring), uint64_t(kRowThreads))), 2048u);
+    const uint32_t rows = std::min(a.n_requests, 4096u);
+    hipLaunchKernelGGL(compact_clear_kernel, dim3(pages), dim3(kRowThreads), 0, st, p);
+    hipLaunchKernelGGL(compact_mark_kernel, dim3(std::max(rows, ring)), dim3(kRowThreads), 0, st, p);
+    hipLaunchKernelGGL(compact_count_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
+    hipLaunchKernelGGL(compact_place_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
+    hipLaunchKernelGGL(compact_finish_kernel, dim3(std::max(rows, pages)), dim3(kRowThreads), 0, st, p);
+    return launched();
+}
+
+dfc_status dfc_paged_copy(const dfc_paged_cache *caches, uint32_t n_caches, const int32_t *src, const int32_t *dst,
+                          uint32_t n, uint32_t *status_dev, void *stream) {
+    if (n_caches && !caches) return DFC_EINVAL;
+    for (uint32_t i = 0; i < n_caches; ++i) {
+        const dfc_paged_cache &c = caches[i], &first = caches[0];
+        const dfc_status cs = dfc::check_cache(c);
+        if (cs != DFC_OK) return cs;
+        if (c.n_pages != first.n_pages || c.page_size != first.page_size || c.kv_heads != first.kv_heads ||
+            c.head_dim != first.head_dim || c.dtype != first.dtype)
+            return DFC_EINVAL;
+        for (int k = 0; k < 3; ++k) {
+            if (c.k_stride[k] != first.k_stride[k] || c.v_stride[k] != first.v_stride[k]) return DFC_EINVAL;
+            if (c.k_stride[k] >> 34 || c.v_stride[k] >> 34) return DFC_EUNSUPPORTED;
+        }
+    }
+    if (!n || !n_caches) return DFC_OK;
+    if (!src || !dst || src == dst || n > 0x7fffffffu) return DFC_EINVAL;
+    const dfc_paged_cache &c = caches[0];
+    CopyArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.src = src;
+    a.dst = dst;
+    a.status = status_dev;
+    a.n = n;
+    a.n_pages = c.n_pages;
+    a.row = c.head_dim / 8u;
+    a.heads = c.kv_heads;
+    const uint64_t pieces = uint64_t(c.page_size) * c.kv_heads * a.row;
+    if (pieces > 0x3fffffffull) return DFC_EUNSUPPORTED;
+    a.pieces = uint32_t(pieces);
+    a.step_pairs = kCopyThreads / a.pieces;
+    a.step_pieces = kCopyThreads % a.pieces;
+    for (int k = 0; k < 3; ++k) {
+        a.k_stride[k] = uint32_t(c.k_stride[k] / 8);
+        a.v_stride[k] = uint32_t(c.v_stride[k] / 8);
+    }
+    // a page is one run of memory, in whichever order
+    auto run = [&](const int64_t (&s)[3]) {
+        const int64_t dim = c.head_dim, heads = c.kv_heads, places = c.page_size;
+        return (s[2] == dim && s[1] == heads * dim) || (s[1] == dim && s[2] == places * dim) ||
+               (heads == 1 && s[1] == dim) || (places == 1 && s[2] == dim);
+    };
+    const bool whole = run(c.k_stride) && run(c.v_stride);
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    for (uint32_t first = 0; first < n_caches; first += kCopyCaches) {
+        const uint32_t here = std::min(n_caches - first, kCopyCaches);
+        a.parts = 2u * here;
+        for (uint32_t i = 0; i < here; ++i) {
+            a.base[2 * i] = static_cast<U4 *>(caches[first + i].k_dev);
+            a.base[2 * i + 1] = static_cast<U4 *>(caches[first + i].v_dev);
+        }
+        // pairs of a group: a workgroup's loads at least, no more than 16,384
+        // workgroups, and no more pairs than its list holds
+        const uint64_t fill = dfc::ceil_div(uint64_t(8u * kCopyThreads), uint64_t(a.pieces));
+        const uint64_t few = dfc::ceil_div(uint64_t(n) * a.parts, uint64_t(16384));
+        const uint64_t pairs = std::min<uint64_t>(std::max(fill, few), kCopyList);
+        a.groups = uint32_t(dfc::ceil_div(uint64_t(n), pairs));
+        const uint64_t blocks = uint64_t(a.groups) * a.parts;
+        if (blocks > 0x7fffffffull) return DFC_EUNSUPPORTED;
+        if (whole)
+            hipLaunchKernelGGL((copy_kernel<true>), dim3(uint32_t(blocks)), dim3(kCopyThreads), 0, st, a);
+        else
+            hipLaunchKernelGGL((copy_kernel<false>), dim3(uint32_t(blocks)), dim3(kCopyThreads), 0, st, a);
+    }
+    return launched();
+}
+
+}  // extern "C"
