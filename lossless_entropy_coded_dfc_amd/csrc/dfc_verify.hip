@@ -63,24 +63,85 @@ struct VerifyArgs {
     Found *found;
 };
 
-template <typename F>
-__device__ __forceinline__ auto over_wave(decltype(F::id()) x) {
-#pragma unroll
-    for (int d = 32; d; d /= 2) x = F::of(x, __shfl_xor(x, d));
-    return x;
-}
+// Inclusive prefix of an operation over the wavefront (DPP row shifts, then row
+// broadcasts 15 and 31), and its last value, for every lane.
+struct Sum {
+    static constexpr double kNone = 0.0;
+    static __device__ __forceinline__ double of(double a, double b) { return a + b; }
+};
 struct Largest {
-    static __device__ float id() { return 0.0f; }
-    static __device__ float of(float a, float b) { return fmaxf(a, b); }
+    static constexpr float kNone = -INFINITY;
+    static __device__ __forceinline__ float of(float a, float b) { return fmaxf(a, b); }
 };
 struct Least {
-    static __device__ uint32_t id() { return 0u; }
-    static __device__ uint32_t of(uint32_t a, uint32_t b) { return min(a, b); }
+    static constexpr uint32_t kNone = ~0u;
+    static __device__ __forceinline__ uint32_t of(uint32_t a, uint32_t b) { return min(a, b); }
 };
-struct Sum {
-    static __device__ double id() { return 0.0; }
-    static __device__ double of(double a, double b) { return a + b; }
-};
+
+template <int Ctrl, int Rows, typename T>
+__device__ __forceinline__ T shifted(T x, T none) {
+    if constexpr (sizeof(T) == 8) {
+        using Two = __attribute__((ext_vector_type(2))) int;
+        const Two v = __builtin_bit_cast(Two, x), o = __builtin_bit_cast(Two, none);
+        return __builtin_bit_cast(T, Two{__builtin_amdgcn_update_dpp(o.x, v.x, Ctrl, Rows, 0xf, false),
+                                         __builtin_amdgcn_update_dpp(o.y, v.y, Ctrl, Rows, 0xf, false)});
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_update_dpp(__builtin_bit_cast(int, none), __builtin_bit_cast(int, x),
+                                                                 Ctrl, Rows, 0xf, false));
+    }
+}
+template <typename F, typename T>
+__device__ __forceinline__ T scan_of(T x) {
+    x = F::of(x, shifted<0x111, 0xf>(x, F::kNone));
+    x = F::of(x, shifted<0x112, 0xf>(x, F::kNone));
+    x = F::of(x, shifted<0x114, 0xf>(x, F::kNone));
+    x = F::of(x, shifted<0x118, 0xf>(x, F::kNone));
+    x = F::of(x, shifted<0x142, 0xa>(x, F::kNone));
+    return F::of(x, shifted<0x143, 0xc>(x, F::kNone));
+}
+template <typename T>
+__device__ __forceinline__ T of_lane(T x, uint32_t lane) {
+    if constexpr (sizeof(T) == 8) {
+        using Two = __attribute__((ext_vector_type(2))) int;
+        const Two v = __builtin_bit_cast(Two, x);
+        return __builtin_bit_cast(T, Two{__builtin_amdgcn_readlane(v.x, lane), __builtin_amdgcn_readlane(v.y, lane)});
+    } else {
+        return __builtin_bit_cast(T, __builtin_amdgcn_readlane(__builtin_bit_cast(int, x), lane));
+    }
+}
+template <typename F, typename T>
+__device__ __forceinline__ T over_wave(T x) {
+    return of_lane(scan_of<F>(x), kWave - 1);
+}
+
+// 2^t for t <= 0, within 5e-16 of it: t = n + f with |f| <= 1/2 by adding and
+// taking off a number whose last bit is 1, and 2^f by the polynomial of degree 10
+// through its values at the Chebyshev nodes of [-1/2, 1/2].  A library's
+// exponential has twice the instructions, which decide: 64 requests of five drafts
+// 129 us with it and 106 with this.  (With a table of 64 roots and degree 4, a
+// quarter fewer, it took the same.)
+__device__ __forceinline__ double exp2_of(double t) {
+    t = fmax(t, -1100.0);  // (2^-1100 is 0)
+    const double whole = t + 0x1.8p52, f = t - (whole - 0x1.8p52);
+    double y = 0x1.e6063f7217bc6p-28;
+    y = fma(y, f, 0x1.b675bca4eeebbp-24);
+    y = fma(y, f, 0x1.62bfd47773353p-20);
+    y = fma(y, f, 0x1.ffcb54062e698p-17);
+    y = fma(y, f, 0x1.430913096fd9fp-13);
+    y = fma(y, f, 0x1.5d87fe9d7a584p-10);
+    y = fma(y, f, 0x1.3b2ab6fba1ddap-7);
+    y = fma(y, f, 0x1.c6b08d703ce49p-5);
+    y = fma(y, f, 0x1.ebfbdff82c598p-3);
+    y = fma(y, f, 0x1.62e42fefa3a19p-1);
+    y = fma(y, f, 1.0);
+    return __builtin_ldexp(y, int(uint32_t(__builtin_bit_cast(uint64_t, whole))));
+}
+
+// exp((z - top) / T) for z <= top, `rate` = log2(e) / T.
+__device__ __forceinline__ double weight_of(float z, float top, double rate) {
+    return exp2_of((double(z) - double(top)) * rate);
+}
+__device__ __forceinline__ double rate_of(float t) { return t > 0.0f ? 1.4426950408889634 / double(t) : 0.0; }
 
 // The request of a row: the number of requests that end at or before it.
 __device__ __forceinline__ uint32_t request_of(const dfc_verify_args &a, uint32_t row) {
@@ -112,7 +173,9 @@ __device__ __forceinline__ uint32_t index_of(uint32_t piece, uint32_t i) {
     return piece * kPiece + (i / W * kWave + threadIdx.x % kWave) * W + i % W;
 }
 
-// A lane's 16 values of a piece of a row; -inf past the row.
+// A lane's 16 values of a piece of a row; -inf past the row.  Loads pass the
+// caches by: most logits are read once (64 requests of five drafts 101 us and not
+// 104, one row the same).
 template <typename E>
 __device__ __forceinline__ void load_piece(const E *row, uint32_t vocab, uint32_t piece, float (&x)[kPerLane]) {
     constexpr uint32_t W = 16u / sizeof(E);
@@ -121,7 +184,7 @@ __device__ __forceinline__ void load_piece(const E *row, uint32_t vocab, uint32_
     if (whole && (reinterpret_cast<uintptr_t>(row) & 15u) == 0) {
 #pragma unroll
         for (uint32_t k = 0; k < kPerLane / W; ++k) {
-            const V v = *reinterpret_cast<const V *>(row + index_of<W>(piece, k * W));
+            const V v = __builtin_nontemporal_load(reinterpret_cast<const V *>(row + index_of<W>(piece, k * W)));
 #pragma unroll
             for (uint32_t j = 0; j < W; ++j) x[k * W + j] = float(v[j]);
         }
@@ -140,13 +203,13 @@ __device__ __forceinline__ Part part_of(const float (&x)[kPerLane], uint32_t pie
     float top = -INFINITY;
     bool odd = false;
 #pragma unroll
-    for (uint32_t i = 0; i < kPerLane; ++i) {
-        top = fmaxf(top, x[i]);
-        odd |= !(x[i] < INFINITY);
+    for (uint32_t i = 0; i < kPerLane; i += 2) {
+        top = fmaxf(top, fmaxf(x[i], x[i + 1]));
+        odd |= __builtin_isunordered(x[i], x[i + 1]);
     }
     top = over_wave<Largest>(top);
     Part p{top, 0u, 0.0};
-    if (__any(odd)) {
+    if (__any(odd) || top == INFINITY) {
         p.top = __builtin_nanf("");
     } else if (t == 0.0f) {
         uint32_t at = ~0u;
@@ -155,10 +218,10 @@ __device__ __forceinline__ Part part_of(const float (&x)[kPerLane], uint32_t pie
             if (x[i] == top) at = index_of<W>(piece, i);
         p.at = over_wave<Least>(at);
     } else if (top > -INFINITY) {
-        const double inv = 1.0 / double(t);
+        const double rate = rate_of(t);
         double s = 0.0;
 #pragma unroll
-        for (uint32_t i = 0; i < kPerLane; ++i) s += exp((double(x[i]) - double(top)) * inv);
+        for (uint32_t i = 0; i < kPerLane; ++i) s += weight_of(x[i], top, rate);
         p.sum = over_wave<Sum>(s);
     }
     return p;
@@ -194,14 +257,15 @@ __global__ __launch_bounds__(kVThreads) void parts_kernel(VerifyArgs p) {
 
 // A row's pieces joined by a wavefront.
 struct Whole {
+    double sum;  // of exp((z - top) / T)
     float top;
     uint32_t at;
-    double sum;  // of exp((z - top) / T)
-    bool ok;     // the row has probabilities
+    uint32_t ok;  // the row has probabilities
+    uint32_t pad;
 };
 __device__ __forceinline__ Whole whole_of(const Part *parts, uint32_t pieces, float t) {
     const uint32_t lane = threadIdx.x % kWave;
-    const double inv = t > 0.0f ? 1.0 / double(t) : 0.0;
+    const double rate = rate_of(t);
     float top = -INFINITY;
     uint32_t at = ~0u;
     double sum = 0.0;
@@ -211,31 +275,33 @@ __device__ __forceinline__ Whole whole_of(const Part *parts, uint32_t pieces, fl
         odd |= !(x.top < INFINITY);
         // pieces come in the order of their indexes: a later one has to be larger
         if (x.top > top) {
-            sum = sum > 0.0 ? sum * exp((double(top) - double(x.top)) * inv) : 0.0;
+            sum = sum > 0.0 ? sum * weight_of(top, x.top, rate) : 0.0;
             top = x.top;
             at = x.at;
         }
-        if (x.sum > 0.0) sum += x.sum * exp((double(x.top) - double(top)) * inv);
+        if (x.sum > 0.0) sum += x.sum * weight_of(x.top, top, rate);
     }
     Whole w;
     w.top = over_wave<Largest>(top);
     w.at = over_wave<Least>(top == w.top ? at : ~0u);
-    w.sum = over_wave<Sum>(sum > 0.0 ? sum * exp((double(top) - double(w.top)) * inv) : 0.0);
+    w.sum = over_wave<Sum>(sum > 0.0 ? sum * weight_of(top, w.top, rate) : 0.0);
     w.ok = !__any(odd) && w.top > -INFINITY;
+    w.pad = 0;
     return w;
 }
 
 // The drafts of a request that hold, and where its next token comes from.
-// Called by all wavefronts of a workgroup, which take a row each; `lds` is one
-// Found and a word a wavefront.
+// Called by all wavefronts of a workgroup: each joins the pieces of a row at a
+// time, and then the lanes of all of them look at a draft each.
+constexpr uint32_t kDecideThreads = 1024, kDecideWaves = kDecideThreads / kWave;
 struct Decision {
+    Whole target[kDecideWaves], draft[kDecideWaves];
     Found f;
-    uint32_t refused[kVWaves];
 };
 template <typename E>
 __device__ __forceinline__ Found decide(const VerifyArgs &p, uint32_t r, Decision &lds) {
     const dfc_verify_args &a = p.a;
-    const uint32_t lane = threadIdx.x % kWave, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave), lane = threadIdx.x % kWave;
     Found none{};
     const Rows rows = rows_of(a, r, none.bad);
     const float t = temperature_of(a, r);
@@ -246,45 +312,55 @@ __device__ __forceinline__ Found decide(const VerifyArgs &p, uint32_t r, Decisio
         none.bad = kStatusCorrupt;
         return none;
     }
-    const double inv = t > 0.0f ? 1.0 / double(t) : 0.0;
-    for (uint32_t i0 = 0; i0 < rows.count; i0 += kVWaves) {
-        const uint32_t i = i0 + wave, row = rows.first + i;
+    const double rate = rate_of(t);
+    const bool against = a.draft_logits_dev && t > 0.0f;
+    for (uint32_t i0 = 0; i0 < rows.count; i0 += kDecideWaves) {
+        const uint32_t here = min(rows.count - i0, kDecideWaves);
+        // the model's rows, then the drafter's but for the last
+        for (uint32_t j = wave; j < (against ? 2u * here : here); j += kDecideWaves) {
+            const bool model = j < here;
+            const uint32_t i = model ? j : j - here;
+            if (!model && i0 + i + 1u == rows.count) continue;
+            const Whole w = whole_of((model ? p.target : p.draft) + uint64_t(rows.first + i0 + i) * p.pieces, p.pieces, t);
+            if (lane == 0) (model ? lds.target : lds.draft)[i] = w;
+        }
+        __syncthreads();
         bool stops = false;
         Found f = none;
-        if (i < rows.count) {
-            f.row = row;
-            f.accepted = i;
-            const Whole w = whole_of(p.target + uint64_t(row) * p.pieces, p.pieces, t);
+        if (lane < here) {
+            const uint32_t i = i0 + lane, row = rows.first + i;
             const bool last = i + 1u == rows.count;
             const int64_t x = last ? 0 : a.drafts[row];
             const bool there = x >= 0 && x < int64_t(a.vocab);
-            stops = last;
-            if (!w.ok) {
-                stops = true;
-            } else if (t == 0.0f) {
+            const Whole w = lds.target[lane];
+            f.row = row;
+            f.accepted = i;
+            stops = last || !w.ok;
+            if (w.ok && t == 0.0f) {
                 f.mode = kGreedy;
                 f.drafted = int32_t(w.at);
-                if (!last) stops = x != int64_t(w.at);
-            } else {
+                stops = last || x != int64_t(w.at);
+            } else if (w.ok) {
                 f.mode = kPlain;
                 f.p_top = w.top;
                 f.p_scale = 1.0 / w.sum;
                 if (!last) {
-                    auto value = [&](const void *logits, int64_t stride) {
-                        return double(float(static_cast<const E *>(logits)[int64_t(row) * stride + (there ? x : 0)]));
+                    auto share = [&](const void *logits, int64_t stride, const Whole &of) {
+                        const E z = static_cast<const E *>(logits)[int64_t(row) * stride + (there ? x : 0)];
+                        return weight_of(float(z), of.top, rate) / of.sum;
                     };
-                    const double px = there ? exp((value(a.logits_dev, a.logits_stride) - double(w.top)) * inv) / w.sum : 0.0;
+                    const double px = there ? share(a.logits_dev, a.logits_stride, w) : 0.0;
                     double qx = 1.0;
-                    if (a.draft_logits_dev) {
-                        const Whole v = whole_of(p.draft + uint64_t(row) * p.pieces, p.pieces, t);
+                    if (against) {
+                        const Whole v = lds.draft[lane];
                         f.q_top = v.top;
                         f.q_scale = 1.0 / v.sum;
                         if (!v.ok) f.mode = kNone;  // nothing can be drawn against what is not known
-                        if (there) qx = exp((value(a.draft_logits_dev, a.draft_stride) - double(v.top)) * inv) / v.sum;
+                        if (there) qx = share(a.draft_logits_dev, a.draft_stride, v);
                     }
                     stops = f.mode == kNone || !(double(a.uniforms[row]) * qx < px);
                     if (stops && f.mode == kPlain) {
-                        if (a.draft_logits_dev)
+                        if (against)
                             f.mode = kRest;
                         else if (there)
                             f.drafted = int32_t(x);
@@ -293,17 +369,10 @@ __device__ __forceinline__ Found decide(const VerifyArgs &p, uint32_t r, Decisio
             }
             if (f.mode == kNone || !(last || there)) f.bad |= kStatusCorrupt;
         }
-        __syncthreads();  // the ones before have been read
-        if (lane == 0) lds.refused[wave] = stops;
+        const uint64_t who = __ballot(stops);  // the same for every wavefront
+        if (who && wave == 0 && lane == uint32_t(__builtin_ctzll(who))) lds.f = f;
         __syncthreads();
-        uint32_t who = kVWaves;
-#pragma unroll
-        for (uint32_t k = kVWaves; k-- > 0;)
-            if (lds.refused[k]) who = k;
-        if (who == kVWaves) continue;
-        if (wave == who && lane == 0) lds.f = f;
-        __syncthreads();
-        return lds.f;
+        if (who) return lds.f;
     }
     return none;
 }
@@ -314,7 +383,7 @@ __device__ __forceinline__ void weights_of(const VerifyArgs &p, const Found &f, 
                                            double (&w)[kPerLane]) {
     constexpr uint32_t W = 16u / sizeof(E);
     const dfc_verify_args &a = p.a;
-    const double inv = 1.0 / double(t);
+    const double rate = rate_of(t);
     float x[kPerLane];
     load_piece(static_cast<const E *>(a.logits_dev) + int64_t(f.row) * a.logits_stride, a.vocab, piece, x);
     if (f.mode == kRest) {
@@ -322,30 +391,33 @@ __device__ __forceinline__ void weights_of(const VerifyArgs &p, const Found &f, 
         load_piece(static_cast<const E *>(a.draft_logits_dev) + int64_t(f.row) * a.draft_stride, a.vocab, piece, y);
 #pragma unroll
         for (uint32_t i = 0; i < kPerLane; ++i) {
-            const double px = f.p_scale * exp((double(x[i]) - double(f.p_top)) * inv);
-            const double qx = f.q_scale * exp((double(y[i]) - double(f.q_top)) * inv);
+            const double px = f.p_scale * weight_of(x[i], f.p_top, rate), qx = f.q_scale * weight_of(y[i], f.q_top, rate);
             w[i] = px > qx ? px - qx : 0.0;
         }
     } else {
 #pragma unroll
         for (uint32_t i = 0; i < kPerLane; ++i)
-            w[i] = int32_t(index_of<W>(piece, i)) == f.drafted ? 0.0 : exp((double(x[i]) - double(f.p_top)) * inv);
+            w[i] = int32_t(index_of<W>(piece, i)) == f.drafted ? 0.0 : weight_of(x[i], f.p_top, rate);
     }
 }
 
+template <typename E>
+__global__ __launch_bounds__(kDecideThreads) void decide_kernel(VerifyArgs p) {
+    __shared__ Decision lds;
+    const Found f = decide<E>(p, blockIdx.x, lds);
+    if (threadIdx.x == 0) p.found[blockIdx.x] = f;
+}
+
 // What is left of p where a draft was refused against a drafter's q, summed
-// over each piece.  Every workgroup finds out for itself which drafts hold.
+// over each piece.
 template <typename E>
 __global__ __launch_bounds__(kVThreads) void rest_kernel(VerifyArgs p) {
-    __shared__ Decision lds;
-    const dfc_verify_args &a = p.a;
-    const uint32_t r = blockIdx.x / p.groups, group = blockIdx.x % p.groups;
-    const Found f = decide<E>(p, r, lds);
-    if (group == 0 && threadIdx.x == 0) p.found[r] = f;
-    const uint32_t piece = group * kVWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const uint32_t r = blockIdx.x / p.groups;
+    const uint32_t piece = blockIdx.x % p.groups * kVWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Found f = p.found[r];
     if (f.mode != kRest || piece >= p.pieces) return;
     double w[kPerLane];
-    weights_of<E>(p, f, temperature_of(a, r), piece, w);
+    weights_of<E>(p, f, temperature_of(p.a, r), piece, w);
     double s = 0.0;
 #pragma unroll
     for (uint32_t i = 0; i < kPerLane; ++i) s += w[i];
@@ -353,38 +425,30 @@ __global__ __launch_bounds__(kVThreads) void rest_kernel(VerifyArgs p) {
     if (threadIdx.x % kWave == 0) p.rest[uint64_t(r) * p.pieces + piece] = s;
 }
 
-// Inclusive prefix sum over the wavefront.
-__device__ __forceinline__ double scan_of(double x) {
-#pragma unroll
-    for (uint32_t d = 1; d < kWave; d *= 2) {
-        const double y = __shfl_up(x, d);
-        if (threadIdx.x % kWave >= d) x += y;
-    }
-    return x;
-}
-
 // The token: first the piece in which the sums pass the random number's share
 // of them all, then the value.  The sum of all pieces is the last of the prefix
 // sums that are searched, so some piece passes; within it the sums are added in
 // another order, and where none passes by a rounding the last value with any
-// weight is it.
+// weight is it.  A wavefront's work: the prefix sums of the first kAhead pieces a
+// lane are kept, those of larger vocabularies are added up twice.
 template <typename E>
 __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r, float u) {
-    constexpr uint32_t W = 16u / sizeof(E);
-    const dfc_verify_args &a = p.a;
+    constexpr uint32_t W = 16u / sizeof(E), kAhead = 4;
     const uint32_t lane = threadIdx.x % kWave;
-    const float t = temperature_of(a, r);
-    const double inv = 1.0 / double(t);
+    const float t = temperature_of(p.a, r);
+    const double rate = rate_of(t);
     const Part *parts = p.target + uint64_t(f.row) * p.pieces;
-    double all = 0.0, w[kPerLane];
-    double without = 0.0;  // the drafted token's piece without it
+    const double *rest = p.rest + uint64_t(r) * p.pieces;
+    double all = 0.0, without = 0.0;  // without: the drafted token's piece without it
+    double w[kPerLane], ahead[kAhead];
     auto weight = [&](uint32_t k) -> double {
         if (k >= p.pieces) return 0.0;
-        if (f.mode == kRest) return p.rest[uint64_t(r) * p.pieces + k];
-        if (f.drafted >= 0 && uint32_t(f.drafted) / kPiece == k) return without;
+        if (f.mode == kRest) return rest[k];
         const Part x = parts[k];
-        return x.sum > 0.0 ? x.sum * exp((double(x.top) - double(f.p_top)) * inv) : 0.0;
+        if (f.drafted >= 0 && uint32_t(f.drafted) / kPiece == k) return without;
+        return x.sum > 0.0 ? x.sum * weight_of(x.top, f.p_top, rate) : 0.0;
     };
+#pragma unroll 1
     for (int turn = 0; turn < 2; ++turn) {
         if (f.mode == kPlain && f.drafted >= 0) {
             weights_of<E>(p, f, t, uint32_t(f.drafted) / kPiece, w);
@@ -392,7 +456,15 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
             for (uint32_t i = 0; i < kPerLane; ++i) without += w[i];
             without = over_wave<Sum>(without);
         }
-        for (uint32_t k0 = 0; k0 < p.pieces; k0 += kWave) all += __shfl(scan_of(weight(k0 + lane)), kWave - 1);
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) ahead[i] = weight(i * kWave + lane);
+#pragma unroll
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            ahead[i] = scan_of<Sum>(ahead[i]);
+            all += of_lane(ahead[i], kWave - 1);
+        }
+#pragma unroll 1
+        for (uint32_t k0 = kAhead * kWave; k0 < p.pieces; k0 += kWave) all += over_wave<Sum>(weight(k0 + lane));
         if (all > 0.0) break;
         f.mode = kPlain;  // nothing is left: of p
         f.drafted = -1;
@@ -401,17 +473,23 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
     const double share = double(u) * all;
     double before = 0.0;
     uint32_t piece = 0;
-    for (uint32_t k0 = 0; k0 < p.pieces; k0 += kWave) {
-        const double sum = scan_of(weight(k0 + lane));
+    bool found = false;
+    auto look = [&](uint32_t k0, double sum) {
         const uint64_t past = __ballot(before + sum > share);
         if (past) {
             const uint32_t who = uint32_t(__builtin_ctzll(past));
             piece = k0 + who;
-            if (who) before += __shfl(sum, int(who) - 1);
-            break;
+            if (who) before += of_lane(sum, who - 1u);
+            found = true;
+        } else {
+            before += of_lane(sum, kWave - 1);
         }
-        before += __shfl(sum, kWave - 1);
-    }
+    };
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i)
+        if (!found) look(i * kWave, ahead[i]);
+#pragma unroll 1
+    for (uint32_t k0 = kAhead * kWave; k0 < p.pieces && !found; k0 += kWave) look(k0, scan_of<Sum>(weight(k0 + lane)));
     weights_of<E>(p, f, t, piece, w);
     uint32_t last = 0;
 #pragma unroll
@@ -422,35 +500,37 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
             own += w[g * W + j];
             if (w[g * W + j] > 0.0) last = index_of<W>(piece, g * W + j);
         }
-        const double sum = scan_of(own);
+        const double sum = scan_of<Sum>(own);
         const uint64_t past = __ballot(before + sum > share);
         if (past) {
-            const uint32_t who = uint32_t(__builtin_ctzll(past));
-            double at = before + __shfl_up(sum, 1);
-            if (lane == 0) at = before;
+            double at = before + shifted<0x138, 0xf>(sum, 0.0);  // of the lanes below
             uint32_t token = last;  // (of this lane: its last with any weight)
-            bool found = false;
+            bool here = false;
 #pragma unroll
             for (uint32_t j = 0; j < W; ++j) {
                 at += w[g * W + j];
-                if (!found && at > share && w[g * W + j] > 0.0) token = index_of<W>(piece, g * W + j), found = true;
+                if (!here && at > share && w[g * W + j] > 0.0) token = index_of<W>(piece, g * W + j), here = true;
             }
-            return int64_t(__shfl(token, int(who)));
+            return int64_t(of_lane(token, uint32_t(__builtin_ctzll(past))));
         }
-        before += __shfl(sum, kWave - 1);
+        before += of_lane(sum, kWave - 1);
     }
-#pragma unroll
-    for (int d = 32; d; d /= 2) last = max(last, uint32_t(__shfl_xor(int(last), d)));
-    return int64_t(last);
+    // (0 for lanes without any)
+    return int64_t(~over_wave<Least>(~last));
 }
 
-template <typename E>
-__global__ __launch_bounds__(kVThreads) void token_kernel(VerifyArgs p) {
-    __shared__ Decision lds;
+template <typename E, bool Decided>
+__global__ __launch_bounds__(Decided ? kWave : kDecideThreads) void token_kernel(VerifyArgs p) {
     const dfc_verify_args &a = p.a;
     const uint32_t r = blockIdx.x;
-    const Found f = a.draft_logits_dev ? p.found[r] : decide<E>(p, r, lds);
-    if (threadIdx.x >= kWave) return;
+    Found f;
+    if constexpr (Decided) {
+        f = p.found[r];
+    } else {
+        __shared__ Decision lds;
+        f = decide<E>(p, r, lds);
+        if (threadIdx.x >= kWave) return;
+    }
     int64_t token = -1;
     if (f.mode == kGreedy) {
         token = f.drafted;
@@ -489,8 +569,13 @@ dfc_status launch_verify(const VerifyArgs &p, hipStream_t st) {
     const uint64_t parts = rows * p.groups, rests = uint64_t(a.n_requests) * p.groups;
     if (parts > 0x7fffffffull || rests > 0x7fffffffull) return DFC_EUNSUPPORTED;
     if (parts) hipLaunchKernelGGL((parts_kernel<E>), dim3(uint32_t(parts)), dim3(kVThreads), 0, st, p);
-    if (a.draft_logits_dev) hipLaunchKernelGGL((rest_kernel<E>), dim3(uint32_t(rests)), dim3(kVThreads), 0, st, p);
-    hipLaunchKernelGGL((token_kernel<E>), dim3(a.n_requests), dim3(kVThreads), 0, st, p);
+    if (a.draft_logits_dev) {
+        hipLaunchKernelGGL((decide_kernel<E>), dim3(a.n_requests), dim3(kDecideThreads), 0, st, p);
+        hipLaunchKernelGGL((rest_kernel<E>), dim3(uint32_t(rests)), dim3(kVThreads), 0, st, p);
+        hipLaunchKernelGGL((token_kernel<E, true>), dim3(a.n_requests), dim3(kWave), 0, st, p);
+    } else {
+        hipLaunchKernelGGL((token_kernel<E, false>), dim3(a.n_requests), dim3(kDecideThreads), 0, st, p);
+    }
     return hipGetLastError() == hipSuccess ? DFC_OK : DFC_EHIP;
 }
 
