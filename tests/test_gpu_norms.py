@@ -1,9 +1,9 @@
 """GPU: the append with norms of queries and keys (dfc_paged_append_normed)
 against the oracle's definition in 64 bits.
 
-The square sum and the root are in 64 bits, so a normed value carries one
-rounding to 32 bits of x / root and one of the product with its weight, 2^-24
-each.  A rotation adds three roundings of 2^-24 of |a cos| + |b sin|, the store
+The square sum and the root are in 64 bits, so a normed value carries the
+root's rounding to 32 bits, one of x by it and one of the product with its
+weight, 2^-24 each.  A rotation adds three roundings of 2^-24 of |a cos| + |b sin|, the store
 one rounding u to the cache's type (2^-8 for bfloat16, 2^-11 for float16, below
 their normal ranges half the smallest step, 2^-134 and 2^-25).  All in all
 |got - ref| <= u |ref| + 6 2^-24 (|a cos| + |b sin|) (1 + u) + that."""
