@@ -42,13 +42,15 @@ __device__ __forceinline__ uint64_t lanes_below() { return (uint64_t(1) << (thre
 
 // A cursor's free entries; none where it does not fit the ring.
 struct Ring {
-    uint64_t head, size;
+    uint32_t head, size, length;  // the head in the ring
     bool ok;
+    // the place of entry i < length from the head on
+    __device__ __forceinline__ uint32_t at(uint32_t i) const { return i < length - head ? head + i : i - (length - head); }
 };
 __device__ __forceinline__ Ring ring_of(const int64_t *cursor, uint32_t n_ring) {
     const int64_t head = cursor[0], tail = cursor[1];
     const bool ok = head >= 0 && tail >= head && uint64_t(tail - head) <= n_ring;
-    return Ring{ok ? uint64_t(head) : 0u, ok ? uint64_t(tail - head) : 0u, ok};
+    return Ring{ok ? uint32_t(uint64_t(head) % n_ring) : 0u, ok ? uint32_t(tail - head) : 0u, n_ring, ok};
 }
 
 // The sum of a value over the workgroup, for every thread.  `part` is LDS for
@@ -63,6 +65,22 @@ __device__ __forceinline__ uint32_t sum_of(uint32_t x, uint32_t *part) {
 #pragma unroll
     for (uint32_t k = 0; k < NT / kWave; ++k) all += part[k];
     return all;
+}
+
+// Exclusive prefix sum over the workgroup, the sum in `all`.  `part` as in sum_of.
+__device__ __forceinline__ uint32_t before_of(uint32_t x, uint32_t *part, uint32_t &all) {
+    const uint32_t inc = wave_inclusive_scan(x), wave = threadIdx.x / kWave;
+    __syncthreads();  // the part before has been read
+    if (threadIdx.x % kWave == kWave - 1) part[wave] = inc;
+    __syncthreads();
+    uint32_t before = inc - x;
+    all = 0;
+#pragma unroll
+    for (uint32_t k = 0; k < kPageWaves; ++k) {
+        if (k < wave) before += part[k];
+        all += part[k];
+    }
+    return before;
 }
 
 // ------------------------------------------------------- slabs of pages
@@ -105,44 +123,71 @@ struct ReleaseArgs {
     uint32_t shift, slabs, rounds;
 };
 
-// A workgroup takes a request at a time and its lanes the entries that it
-// gives up.
-__global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
+// The entries that a request gives up: [hole, hole + n_hole), behind the window,
+// and [begin, end), behind what it keeps.
+struct Given {
+    uint32_t hole, n_hole, begin, n;  // n: of all
+    __device__ __forceinline__ uint32_t at(uint32_t j) const { return j < n_hole ? hole + j : begin + (j - n_hole); }
+};
+__device__ __forceinline__ Given given_of(const ReleaseArgs &p, uint32_t r, uint32_t &bad) {
     const dfc_release_args &a = p.a;
     const uint32_t P = a.page_size;
-    uint32_t bad = 0;
-    for (uint32_t r = blockIdx.x; r < a.n_requests; r += gridDim.x) {
-        const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
-        if (held < 0 || keep < 0 || keep > held) {
-            bad |= kStatusCorrupt;
-            continue;
-        }
-        uint32_t end = (uint32_t(held) + P - 1u) >> p.shift;
-        if (end > a.max_pages) {
-            bad |= uint32_t(DFC_ESIZE);
-            end = a.max_pages;
-        }
-        const uint32_t begin = min((uint32_t(keep) + P - 1u) >> p.shift, end);
-        // behind the window: [hole, hole + n_hole)
-        const uint32_t hole = uint32_t((uint64_t(a.sinks) + P - 1u) >> p.shift);
-        uint32_t n_hole = 0;
-        if (a.window && uint32_t(keep) + 1u > a.window) {
-            const uint32_t passed = min((uint32_t(keep) + 1u - a.window) >> p.shift, begin);
-            n_hole = passed > hole ? passed - hole : 0u;
-        }
-        int32_t *row = a.block_table + int64_t(r) * a.table_stride;
-        for (uint32_t j = threadIdx.x; j < n_hole + (end - begin); j += kRowThreads) {
-            const uint32_t i = j < n_hole ? hole + j : begin + (j - n_hole);
-            const int32_t page = row[i];
-            if (page < 0) continue;
-            row[i] = -1;
-            if (uint32_t(page) >= a.n_pages)
-                bad |= kStatusCorrupt;
-            else if (atomicSub(a.shared + page, 1) < 0)
-                bad |= kStatusCorrupt;  // given up more often than held
-        }
+    const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
+    Given g{0u, 0u, 0u, 0u};
+    if (held < 0 || keep < 0 || keep > held) {
+        bad |= kStatusCorrupt;
+        return g;
     }
-    tell(a.status_dev, bad);
+    uint32_t end = (uint32_t(held) + P - 1u) >> p.shift;
+    if (end > a.max_pages) {
+        bad |= uint32_t(DFC_ESIZE);
+        end = a.max_pages;
+    }
+    g.begin = min((uint32_t(keep) + P - 1u) >> p.shift, end);
+    g.hole = uint32_t((uint64_t(a.sinks) + P - 1u) >> p.shift);
+    if (a.window && uint32_t(keep) + 1u > a.window) {
+        const uint32_t passed = min((uint32_t(keep) + 1u - a.window) >> p.shift, g.begin);
+        g.n_hole = passed > g.hole ? passed - g.hole : 0u;
+    }
+    g.n = g.n_hole + (end - g.begin);
+    return g;
+}
+
+// An entry given up; the page if nobody holds it any more, else -1.
+__device__ __forceinline__ int32_t give(const ReleaseArgs &p, uint32_t r, uint32_t i, uint32_t &bad) {
+    const dfc_release_args &a = p.a;
+    int32_t *entry = a.block_table + int64_t(r) * a.table_stride + i;
+    const int32_t page = *entry;
+    if (page < 0) return -1;
+    *entry = -1;
+    if (uint32_t(page) >= a.n_pages) {
+        bad |= kStatusCorrupt;
+        return -1;
+    }
+    const int32_t before = atomicSub(a.shared + page, 1);
+    if (before < 0) bad |= kStatusCorrupt;  // given up more often than held
+    return before <= 0 ? page : -1;
+}
+
+// A request that is cut inside a page that others hold after the call.
+__device__ __forceinline__ void look_at_cut(const ReleaseArgs &p, uint32_t r, uint32_t &bad) {
+    const dfc_release_args &a = p.a;
+    const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
+    if (keep <= 0 || keep >= held || !(uint32_t(keep) & (a.page_size - 1u))) return;
+    const uint32_t i = uint32_t(keep) >> p.shift;
+    if (i >= a.max_pages) return;
+    const int32_t page = a.block_table[int64_t(r) * a.table_stride + i];
+    if (page >= 0 && uint32_t(page) < a.n_pages && a.shared[page] > 0) bad |= uint32_t(DFC_EUNSUPPORTED);
+}
+
+// A workgroup takes a request at a time and its lanes the entries.
+__global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
+    uint32_t bad = 0;
+    for (uint32_t r = blockIdx.x; r < p.a.n_requests; r += gridDim.x) {
+        const Given g = given_of(p, r, bad);
+        for (uint32_t j = threadIdx.x; j < g.n; j += kRowThreads) give(p, r, g.at(j), bad);
+    }
+    tell(p.a.status_dev, bad);
 }
 
 // Free pages of every slab.
@@ -160,8 +205,7 @@ __global__ __launch_bounds__(kPageThreads) void freed_write_kernel(ReleaseArgs p
     __shared__ uint32_t part[kPageWaves], of_wave[kPageWaves];
     const dfc_release_args &a = p.a;
     const uint32_t tid = threadIdx.x, wave = tid / kWave;
-    uint32_t bad = 0;
-    uint32_t before = 0, total = 0;
+    uint32_t bad = 0, before = 0, total = 0;
     if (p.slabs > 1) {
         uint32_t mine = 0, all = 0;
         for (uint32_t k = tid; k < p.slabs; k += kPageThreads) {
@@ -187,31 +231,80 @@ __global__ __launch_bounds__(kPageThreads) void freed_write_kernel(ReleaseArgs p
     const bool fits = ring.ok && total <= a.n_ring - ring.size;
     if (!fits) bad |= kStatusCorrupt;
     if (n) {  // (of the wavefront)
-        // the place of the wavefront's next page
-        uint64_t to = (ring.head + ring.size + before) % a.n_ring;
+        uint32_t to = ring.size + before;  // the entry of the wavefront's next page
         each_page(a.shared, a.n_pages, p.rounds, [&](uint32_t page, bool, int32_t v) {
             const uint64_t who = __ballot(v < 0);
             if (v < 0) {
-                uint64_t at = to + uint32_t(__popcll(who & lanes_below()));
-                if (at >= a.n_ring) at %= a.n_ring;
-                if (fits) a.free_pages[at] = int32_t(page);
+                if (fits) a.free_pages[ring.at(to + uint32_t(__popcll(who & lanes_below())))] = int32_t(page);
                 a.shared[page] = 0;
             }
             to += uint32_t(__popcll(who));
         });
     }
-    // requests cut inside a page that others hold
-    for (uint32_t r = blockIdx.x * kPageThreads + tid; r < a.n_requests; r += gridDim.x * kPageThreads) {
-        const int32_t held = a.held_lens[r], keep = a.keep_lens[r];
-        if (keep <= 0 || keep >= held || !(uint32_t(keep) & (a.page_size - 1u))) continue;
-        const uint32_t i = uint32_t(keep) >> p.shift;
-        if (i >= a.max_pages) continue;
-        const int32_t page = a.block_table[int64_t(r) * a.table_stride + i];
-        if (page >= 0 && uint32_t(page) < a.n_pages && a.shared[page] > 0) bad |= uint32_t(DFC_EUNSUPPORTED);
-    }
+    for (uint32_t r = blockIdx.x * kPageThreads + tid; r < a.n_requests; r += gridDim.x * kPageThreads)
+        look_at_cut(p, r, bad);
     if (blockIdx.x == 0 && tid == 0) {
         const int64_t head = a.cursor[0], tail = a.cursor[1];
         a.cursor_out[0] = head;
+        a.cursor_out[1] = fits ? tail + int64_t(total) : tail;
+    }
+    tell(a.status_dev, bad);
+}
+
+// All of it by one workgroup, for few requests: the pages that become free are
+// bits in LDS, a run of words a thread, so that nothing is looked through.  A lane
+// reads a request's lengths and gives up a few entries by itself, as after
+// refused drafts; longer runs are taken by the wavefront, one after the other.
+constexpr uint32_t kFewRequests = 64, kFreedWords = 8, kFewFreed = 32u * kPageThreads * kFreedWords;
+__global__ __launch_bounds__(kPageThreads) void release_few_kernel(ReleaseArgs p) {
+    constexpr uint32_t kAlone = 2, kEach = kFewRequests / kPageWaves;
+    __shared__ uint32_t freed[kPageThreads * kFreedWords], part[kPageWaves];
+    const dfc_release_args &a = p.a;
+    const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    uint32_t bad = 0;
+    Given g{0u, 0u, 0u, 0u};
+    const uint32_t mine = wave * kEach + lane;
+    if (lane < kEach && mine < a.n_requests) g = given_of(p, mine, bad);
+#pragma unroll
+    for (uint32_t i = 0; i < kFreedWords; ++i) freed[i * kPageThreads + tid] = 0;
+    __syncthreads();
+    auto give_up = [&](uint32_t r, uint32_t i) {
+        const int32_t page = give(p, r, i, bad);
+        if (page >= 0) atomicOr(&freed[page >> 5], 1u << (page & 31));
+    };
+    if (g.n <= kAlone)
+        for (uint32_t j = 0; j < g.n; ++j) give_up(mine, g.at(j));
+#pragma unroll
+    for (uint32_t k = 0; k < kEach; ++k) {
+        const uint32_t n = __builtin_amdgcn_readlane(g.n, k);
+        if (n <= kAlone) continue;
+        const Given o{uint32_t(__builtin_amdgcn_readlane(g.hole, k)), uint32_t(__builtin_amdgcn_readlane(g.n_hole, k)),
+                      uint32_t(__builtin_amdgcn_readlane(g.begin, k)), n};
+        for (uint32_t j = lane; j < n; j += kWave) give_up(wave * kEach + k, o.at(j));
+    }
+    __syncthreads();
+    uint32_t n = 0, total;
+#pragma unroll
+    for (uint32_t i = 0; i < kFreedWords; ++i) n += uint32_t(__popc(freed[tid * kFreedWords + i]));
+    const uint32_t before = before_of(n, part, total);
+    const bool fits = ring.ok && total <= a.n_ring - ring.size;
+    if (!fits) bad |= kStatusCorrupt;
+    if (n) {
+        uint32_t to = ring.size + before;
+        for (uint32_t i = 0; i < kFreedWords; ++i)
+            for (uint32_t left = freed[tid * kFreedWords + i]; left; left &= left - 1u) {
+                const uint32_t page = 32u * (tid * kFreedWords + i) + uint32_t(__builtin_ctz(left));
+                if (fits) a.free_pages[ring.at(to)] = int32_t(page);
+                ++to;
+                a.shared[page] = 0;
+            }
+    }
+    // (pages that others hold are none of those)
+    if (lane < kEach && mine < a.n_requests) look_at_cut(p, mine, bad);
+    if (tid == 0) {
+        const int64_t tail = a.cursor[1];
+        a.cursor_out[0] = a.cursor[0];
         a.cursor_out[1] = fits ? tail + int64_t(total) : tail;
     }
     tell(a.status_dev, bad);
@@ -293,7 +386,7 @@ __global__ __launch_bounds__(kRowThreads) void fork_kernel(ForkArgs p) {
             bad |= uint32_t(DFC_ESIZE);
             c.forked = false;
         } else {
-            page = a.free_pages[(ring.head + before) % a.n_ring];
+            page = a.free_pages[ring.at(before)];
             if (page < 0 || uint32_t(page) >= a.n_pages) {
                 bad |= kStatusCorrupt;
                 c.forked = false;
@@ -374,8 +467,8 @@ __global__ __launch_bounds__(kRowThreads) void compact_mark_kernel(CompactArgs p
     }
     const Ring ring = ring_of(a.cursor, a.n_ring);
     wrong |= !ring.ok;
-    for (uint64_t i = uint64_t(blockIdx.x) * kRowThreads + threadIdx.x; i < ring.size; i += uint64_t(gridDim.x) * kRowThreads) {
-        const int32_t page = a.free_pages[(ring.head + i) % a.n_ring];
+    for (uint32_t i = blockIdx.x * kRowThreads + threadIdx.x; i < ring.size; i += gridDim.x * kRowThreads) {
+        const int32_t page = a.free_pages[ring.at(i)];
         if (page >= 0 && uint32_t(page) < a.n_pages)
             wrong |= (atomicOr(p.flags + page, kFree) & kFree) != 0;  // twice on the ring
         else
@@ -444,7 +537,7 @@ __global__ __launch_bounds__(kPageThreads) void compact_place_kernel(CompactArgs
             if (v == kFree && rank < held) a.dst[rank - before] = int32_t(page);
             // (the first `stay` held pages are those up to a_{U-1})
             if (v && rank + 1u == held) *p.stay = before + (v == kHeld);
-            if (v && rank >= held) a.free_pages[(ring.head + (rank - held)) % a.n_ring] = int32_t(page);
+            if (v && rank >= held) a.free_pages[ring.at(rank - held)] = int32_t(page);
         }
         h += uint32_t(__popcll(hs));
         e += uint32_t(__popcll(es));
@@ -477,6 +570,116 @@ __global__ __launch_bounds__(kRowThreads) void compact_finish_kernel(CompactArgs
             if (k <= -2) row[i] = a.dst[uint32_t(-2 - k) - stay];
         }
     }
+}
+
+// All of it by one workgroup, where pages and rows' entries are a few for each of
+// its threads: two bits a page in LDS, from whose sums a page's rank is read.  64
+// requests of up to 500 tokens among 512 free pages take 5.4 us in place of 10 in
+// five launches, whose gaps come on top (27 and 34 us with the copying);
+// 17,000 entries over 16,700 pages took 23 in place of 20, since one compute unit
+// did all of it.
+constexpr uint32_t kFewPages = kSlab, kEntries = 8, kFewEntries = kEntries * kPageThreads, kFewRows = 1024;
+static_assert(kFewPages <= 32u * kPageThreads && kFewPages <= 65536u, "a word a thread, a page in 16 bits");
+
+__global__ __launch_bounds__(kPageThreads) void compact_few_kernel(CompactArgs p) {
+    __shared__ uint32_t held[kPageThreads], free[kPageThreads];
+    __shared__ uint16_t pages_of[kFewRows], held_before[kPageThreads], before[kPageThreads], from[kFewPages / 2], to[kFewPages / 2];
+    __shared__ uint32_t part[kPageWaves], wrong, stay;
+    const dfc_compact_args &a = p.a;
+    const uint32_t tid = threadIdx.x;
+    const uint32_t entries = a.n_requests * a.max_pages;
+    const Ring ring = ring_of(a.cursor, a.n_ring);
+    uint32_t bad = 0;
+    held[tid] = free[tid] = 0;
+    if (tid == 0) wrong = !ring.ok, stay = 0;
+    if (tid < a.n_requests) {
+        const int32_t n = a.context_lens[tid];
+        const uint32_t end = (uint32_t(max(n, 0)) + a.page_size - 1u) >> p.shift;
+        if (n < 0) bad |= kStatusCorrupt;
+        if (end > a.max_pages) bad |= uint32_t(DFC_ESIZE);
+        pages_of[tid] = uint16_t(min(end, a.max_pages));
+    }
+    for (uint32_t i = tid; i < a.n_pages / 2u; i += kPageThreads) a.src[i] = a.dst[i] = -1;
+    __syncthreads();
+    // f(k, entry) for the thread's entries of the rows, kPageThreads apart
+    const uint32_t rows = kPageThreads / a.max_pages, rest = kPageThreads - rows * a.max_pages;
+    auto each_entry = [&](auto &&f) {
+        uint32_t r = tid / a.max_pages, at = tid - r * a.max_pages;
+#pragma unroll
+        for (uint32_t k = 0; k < kEntries; ++k) {
+            if (k * kPageThreads >= entries) continue;
+            f(k, r < a.n_requests && at < pages_of[r] ? a.block_table + int64_t(r) * a.table_stride + at : nullptr);
+            r += rows;
+            at += rest;
+            if (at >= a.max_pages) at -= a.max_pages, ++r;
+        }
+    };
+    int32_t page[kEntries];  // -1: none
+    each_entry([&](uint32_t k, const int32_t *e) { page[k] = e ? *e : -1; });
+    bool odd = false;
+#pragma unroll 8
+    for (uint32_t i = tid; i < ring.size; i += kPageThreads) {
+        const int32_t x = a.free_pages[ring.at(i)];
+        if (x >= 0 && uint32_t(x) < a.n_pages)
+            odd |= atomicOr(&free[x >> 5], 1u << (x & 31)) >> (x & 31) & 1u;  // twice on the ring
+        else
+            odd = true;
+    }
+#pragma unroll
+    for (uint32_t k = 0; k < kEntries; ++k) {
+        if (k * kPageThreads >= entries || page[k] < 0) continue;
+        if (uint32_t(page[k]) < a.n_pages)
+            atomicOr(&held[page[k] >> 5], 1u << (page[k] & 31));
+        else
+            odd = true;
+    }
+    __syncthreads();
+    const uint32_t h = held[tid], f = free[tid];
+    if (odd || (h & f)) wrong = 1u;
+    uint32_t n_held, n_either;
+    held_before[tid] = uint16_t(before_of(uint32_t(__popc(h)), part, n_held));
+    before[tid] = uint16_t(before_of(uint32_t(__popc(h | f)), part, n_either));
+    __syncthreads();
+    if (tid == 0) *a.used = int32_t(n_held);
+    if (wrong) {  // (written before the barriers of the sums)
+        tell(a.status_dev, bad | kStatusCorrupt);
+        return;
+    }
+    // a page's rank among the held ones and all, from its word's
+    auto place = [&](uint32_t x, uint32_t &h_rank, uint32_t &rank) {
+        const uint32_t word = x >> 5, below = (1u << (x & 31)) - 1u, hw = held[word];
+        h_rank = held_before[word] + uint32_t(__popc(hw & below));
+        rank = before[word] + uint32_t(__popc((hw | free[word]) & below));
+        return hw >> (x & 31) & 1u;
+    };
+    for (uint32_t x = tid; x < a.n_pages; x += kPageThreads) {
+        if (!((held[x >> 5] | free[x >> 5]) >> (x & 31) & 1u)) continue;
+        uint32_t h_rank, rank;
+        const bool is_held = place(x, h_rank, rank);
+        if (!is_held && rank < n_held) to[rank - h_rank] = uint16_t(x);
+        if (rank >= n_held) a.free_pages[ring.at(rank - n_held)] = int32_t(x);
+        if (rank + 1u == n_held) stay = h_rank + is_held;
+    }
+    __syncthreads();
+    for (uint32_t x = tid; x < a.n_pages; x += kPageThreads) {
+        uint32_t h_rank, rank;
+        if (place(x, h_rank, rank) && rank >= n_held) from[h_rank - stay] = uint16_t(x);
+    }
+    __syncthreads();
+    for (uint32_t i = tid; i < n_held - stay; i += kPageThreads) {
+        const int32_t s = from[i], d = to[i];
+        a.src[i] = s;
+        a.dst[i] = d;
+        a.shared[d] = a.shared[s];
+        a.shared[s] = 0;
+    }
+    each_entry([&](uint32_t k, int32_t *e) {
+        uint32_t h_rank, rank;
+        if (!e || page[k] < 0) return;
+        place(uint32_t(page[k]), h_rank, rank);
+        if (rank >= n_held) *e = to[h_rank - stay];
+    });
+    tell(a.status_dev, bad);
 }
 
 // ------------------------------------------------------------------- copy
@@ -587,6 +790,10 @@ dfc_status dfc_paged_release(const dfc_release_args *args, void *stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     const Slabs s = slabs_of(a.n_pages);
     const ReleaseArgs p{a, dfc::log2_of(a.page_size), s.count, s.rounds};
+    if (a.n_requests <= kFewRequests && a.n_pages <= kFewFreed) {
+        hipLaunchKernelGGL(release_few_kernel, dim3(1), dim3(kPageThreads), 0, st, p);
+        return launched();
+    }
     if (a.n_requests) hipLaunchKernelGGL(release_kernel, dim3(std::min(a.n_requests, 4096u)), dim3(kRowThreads), 0, st, p);
     if (s.count > 1) hipLaunchKernelGGL(freed_count_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
     hipLaunchKernelGGL(freed_write_kernel, dim3(s.count), dim3(kPageThreads), 0, st, p);
@@ -639,6 +846,10 @@ dfc_status dfc_paged_compact(const dfc_compact_args *args, void *stream) {
     p.either = p.held + kMostSlabs;
     p.flags = reinterpret_cast<int32_t *>(p.either + kMostSlabs);
     p.place = p.flags + a.n_pages;
+    if (a.n_pages <= kFewPages && a.n_requests <= kFewRows && uint64_t(a.n_requests) * a.max_pages <= kFewEntries) {
+        hipLaunchKernelGGL(compact_few_kernel, dim3(1), dim3(kPageThreads), 0, st, p);
+        return launched();
+    }
     const uint32_t pages = std::min(uint32_t(dfc::ceil_div(uint64_t(a.n_pages), uint64_t(kRowThreads))), 2048u);
     const uint32_t ring = std::min(uint32_t(dfc::ceil_div(uint64_t(a.n_ring), uint64_t(kRowThreads))), 2048u);
     const uint32_t rows = std::min(a.n_requests, 4096u);
