@@ -208,7 +208,7 @@ struct Rows {
     f32x16 acc[ND];
     float m, l, slack;              // reference (raw scores); this lane's share of the sum
     int32_t see_lo, see_hi;         // the keys of the row,
-    int32_t sinks, see_sinks;       // and the first so many; those before see_hi
+    int32_t see_sinks;              // and the first so many
     int32_t hi_min, hi_max, lo_min, lo_max;  // over the wavefront's rows
     bool idle;                      // no rows
     uint32_t odd;                   // a tile with masked keys held a value that is not finite
@@ -221,13 +221,11 @@ struct Rows {
         const int32_t row_c = min(row, n_rows - 1);
         const int32_t tok = row_c / int32_t(a.group), g = row_c - tok * int32_t(a.group);
         const int32_t pos = w.kv_len - w.q_len + tok;
-        const int32_t end = end_of<Sinks>(a, w);
-        see_hi = a.causal ? min(pos + 1, end) : end;
-        if constexpr (Sinks) {
-            sinks = a.sinks;
-            see_sinks = max(min(sinks, see_hi), 0);
-        }
-        see_lo = a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0;
+        // (as the piece counts its keys: no row sees one of the gap)
+        const int32_t gap = Sinks ? w.gap : 0;
+        see_hi = a.causal ? min(pos + 1 - gap, w.hi) : w.hi;
+        if constexpr (Sinks) see_sinks = max(min(a.sinks, see_hi), 0);
+        see_lo = (a.window ? int32_t(max(int64_t(0), int64_t(pos) + 1 - int64_t(a.window))) : 0) - gap;
         // positions ascend with the row
         hi_min = __builtin_amdgcn_readfirstlane(see_hi), lo_min = __builtin_amdgcn_readfirstlane(see_lo);
         hi_max = __builtin_amdgcn_readlane(see_hi, 31), lo_max = __builtin_amdgcn_readlane(see_lo, 31);
@@ -264,13 +262,13 @@ struct Rows {
         for (int s = 0; s < NQ; ++s) asm volatile("" ::"v"(qf[s]));
     }
 
-    // No row sees a key of the tile; some row does not see all of them.
+    // No row sees a key of the tile; some row does not see all of them.  With
+    // sinks, a tile before the wavefront's windows counts as one that some row
+    // sees in part: those are the sinks' own and what the tile's other rows see.
     __device__ __forceinline__ bool skips(int32_t start) const {
-        return idle || start >= hi_max || (start + KT <= lo_min && !(Sinks && start < sinks));
+        return idle || start >= hi_max || (!Sinks && start + KT <= lo_min);
     }
-    __device__ __forceinline__ bool masks(int32_t start) const {
-        return start + KT > hi_min || (start < lo_max && !(Sinks && start + KT <= sinks));
-    }
+    __device__ __forceinline__ bool masks(int32_t start) const { return start + KT > hi_min || start < lo_max; }
 
     // O^T += V^T P^T (PV), S^T = K Q^T (QK), in groups of four products whose
     // operands are read kAhead groups before they are used: four wavefronts
@@ -356,6 +354,8 @@ struct Rows {
                     bool hidden = first + at >= width;
                     if constexpr (Sinks) hidden = hidden && first + uint32_t(see_lo) + at >= uint32_t(see_sinks);
                     if (hidden) s[b][r] = -INFINITY;
+                    // (each comparison's lanes are 2 of the loop's scalar registers)
+                    if constexpr (Sinks) __builtin_amdgcn_sched_barrier(0);
                 }
         }
         float top = s[0][0];
@@ -399,7 +399,7 @@ struct Rows {
 
 // Tiles of K and V on their way from the cache to LDS through the registers of
 // NT threads, thread gtid of them: NL pieces of 16 bytes of each.
-template <typename E, int DP, int KT, int NT, bool Same>
+template <typename E, int DP, int KT, int NT, bool Same, bool Sinks>
 struct Loader {
     static constexpr int CPR = DP / 8;             // pieces per row
     static constexpr int NL = KT * CPR / NT;       // pieces per thread
@@ -412,11 +412,12 @@ struct Loader {
     uint32_t n_pages, page_shift;
     uint32_t k_page, k_slot, v_page, v_slot;       // strides in pieces
     bool whole_dim, same;
+    int32_t sink_end, gap;                         // see key_at
     int32_t pages[NL];
     bool absent, missing;                          // a page that is none of the cache's: under way, ever (wavefront)
     uint4 kr[NL], vr[NL];
 
-    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, int32_t end, uint32_t kvh, uint32_t rw) {
+    __device__ __forceinline__ void init(const AttnArgs &a, const Piece &w, uint32_t kvh, uint32_t rw) {
         gtid = rw * 64u + threadIdx.x % kWave;
         row = gtid / CPR;
         chunk = gtid % CPR * 8u < a.dim ? gtid % CPR : 0u;
@@ -426,10 +427,16 @@ struct Loader {
         vbase = static_cast<const uint8_t *>(a.v) + uint64_t(kvh) * a.v_units[2] * 16u;
         k_page = a.k_units[0], k_slot = a.k_units[1], v_page = a.v_units[0], v_slot = a.v_units[1];
         same = k_page == v_page && k_slot == v_slot;
-        hi = end;
+        hi = end_of<Sinks>(a, w);
+        if constexpr (Sinks) sink_end = a.sink_end, gap = w.gap;
         n_pages = a.n_pages;
         page_shift = a.page_shift;
         absent = missing = false;
+    }
+
+    // The token that a tile begins with.
+    __device__ __forceinline__ int32_t token(int32_t start) const {
+        return Sinks && start >= sink_end ? start + gap : start;
     }
 
     // The block table's entries for the thread's rows of the tile at `start`
@@ -440,7 +447,7 @@ struct Loader {
     }
     __device__ __forceinline__ void fetch_pages(int32_t start) {
 #pragma unroll
-        for (int n = 0; n < NL; ++n) pages[n] = page_of(start, n);
+        for (int n = 0; n < NL; ++n) pages[n] = page_of(token(start), n);
     }
 
     // A page that is none of the cache's is noted and the last one read in
@@ -449,6 +456,7 @@ struct Loader {
     __device__ __forceinline__ void load(int32_t start) {
         const uint32_t page_mask = (1u << page_shift) - 1u;
         uint32_t most = 0;
+        start = token(start);
 #pragma unroll
         for (int n = 0; n < NL; ++n) {
             const uint32_t in_page = (uint32_t(start) + row + uint32_t(n * kStep)) & page_mask;
@@ -469,6 +477,7 @@ struct Loader {
     // Into LDS; rows past the piece, columns past the head and pages that are
     // none of the cache's become zeros.
     __device__ __forceinline__ void put(uint8_t *kt, uint8_t *vt, int32_t start) {
+        start = token(start);
         if (!whole_dim || start + KT > hi || absent) {
             const bool in_dim = whole_dim || gtid % CPR == chunk;
 #pragma unroll
@@ -624,16 +633,15 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
     if (!find_piece<kThreads, Sinks>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const uint32_t rw = wave % RW, kw = wave / RW;
-    Loader<E, DP, KT, 64 * RW, false> ld;
-    ld.init(a, w, end_of<Sinks>(a, w), kvh, rw);
+    Loader<E, DP, KT, 64 * RW, false, Sinks> ld;
+    ld.init(a, w, kvh, rw);
     const int32_t n_tiles = (w.hi - w.lo + KT - 1) / KT;
     const int32_t n_steps = (n_tiles + KW - 1) / KW;  // the same for every group: they meet at barriers
-    auto tile_key = [&](int32_t step) { return w.lo + (step * KW + int32_t(kw)) * KT; };
-    auto tile_start = [&](int32_t step) { return key_at<Sinks>(a, w, tile_key(step)); };
+    auto tile_start = [&](int32_t step) { return w.lo + (step * KW + int32_t(kw)) * KT; };
     R x;
     if (n_steps) ld.fetch_pages(tile_start(0));
     x.init(a, w, kvh, 32u * rw);
-    if (tile_key(0) < w.hi) {
+    if (tile_start(0) < w.hi) {
         ld.load(tile_start(0));
         ld.fetch_pages(tile_start(1));
     }
@@ -651,7 +659,7 @@ __global__ __launch_bounds__(kThreads, DP > 128 ? 1 : 2) void attention_kernel(A
             __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         else
             __syncthreads();
-        if (tile_key(step + 1) < w.hi) {
+        if (tile_start(step + 1) < w.hi) {
             ld.load(tile_start(step + 1));
             ld.fetch_pages(tile_start(step + 2));
         }
@@ -718,10 +726,10 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     if (!find_piece<512, Sinks>(again(a), index, blockIdx.x == 0, reinterpret_cast<uint32_t *>(lds), w)) return;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const bool second = wave >= 4u;
-    Loader<E, DP, KT, 512, true> ld;  // (the launcher sees to it)
-    ld.init(a, w, end_of<Sinks>(a, w), kvh, wave);
+    Loader<E, DP, KT, 512, true, Sinks> ld;  // (the launcher sees to it)
+    ld.init(a, w, kvh, wave);
     const int32_t n = (w.hi - w.lo + KT - 1) / KT;
-    auto tile_start = [&](int32_t t) { return key_at<Sinks>(a, w, w.lo + t * KT); };
+    auto tile_start = [&](int32_t t) { return w.lo + t * KT; };
     auto k_tile = [&](int32_t t) { return lds + uint32_t(t & 1) * Sh::kTileBytes; };
     R x;
     if (n) ld.fetch_pages(tile_start(0));
@@ -753,14 +761,9 @@ __global__ __launch_bounds__(512, 2) void attention8_kernel(AttnArgs a) {
     // the wavefront's own tiles: t0 .. t1 - 1
     int32_t t = 0, t0 = 0, t1 = 0;
     if (!x.idle) {
-        int32_t first = x.lo_min, end = x.hi_max;
-        if constexpr (Sinks) {
-            // from the sinks on, where the piece has them; else all of it is behind the gap
-            first = w.lo < a.sink_end ? w.lo : first - w.gap;
-            if (end > a.sink_end) end -= w.gap;
-        }
+        const int32_t first = Sinks && w.lo < a.sink_end ? w.lo : x.lo_min;  // every row sees the sinks
         t0 = min(max((first - w.lo) / KT, 0), n);
-        t1 = min(max((end - w.lo + KT - 1) / KT, t0), n);
+        t1 = min(max((x.hi_max - w.lo + KT - 1) / KT, t0), n);
     }
     auto turn_without_rows = [&]() {
         load(t + lead);
