@@ -153,20 +153,17 @@ __device__ __forceinline__ Given given_of(const ReleaseArgs &p, uint32_t r, uint
     return g;
 }
 
-// An entry given up; the page if nobody holds it any more, else -1.
-__device__ __forceinline__ int32_t give(const ReleaseArgs &p, uint32_t r, uint32_t i, uint32_t &bad) {
-    const dfc_release_args &a = p.a;
-    int32_t *entry = a.block_table + int64_t(r) * a.table_stride + i;
-    const int32_t page = *entry;
+__device__ __forceinline__ int32_t *entry_of(const ReleaseArgs &p, uint32_t r, uint32_t i) {
+    return p.a.block_table + int64_t(r) * p.a.table_stride + i;
+}
+
+// The page of an entry that is given up, -1 if it is none.
+__device__ __forceinline__ int32_t given_up(const ReleaseArgs &p, int32_t *entry, int32_t page, uint32_t &bad) {
     if (page < 0) return -1;
     *entry = -1;
-    if (uint32_t(page) >= a.n_pages) {
-        bad |= kStatusCorrupt;
-        return -1;
-    }
-    const int32_t before = atomicSub(a.shared + page, 1);
-    if (before < 0) bad |= kStatusCorrupt;  // given up more often than held
-    return before <= 0 ? page : -1;
+    if (uint32_t(page) < p.a.n_pages) return page;
+    bad |= kStatusCorrupt;
+    return -1;
 }
 
 // A request that is cut inside a page that others hold after the call.
@@ -185,7 +182,11 @@ __global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
     uint32_t bad = 0;
     for (uint32_t r = blockIdx.x; r < p.a.n_requests; r += gridDim.x) {
         const Given g = given_of(p, r, bad);
-        for (uint32_t j = threadIdx.x; j < g.n; j += kRowThreads) give(p, r, g.at(j), bad);
+        for (uint32_t j = threadIdx.x; j < g.n; j += kRowThreads) {
+            int32_t *entry = entry_of(p, r, g.at(j));
+            const int32_t page = given_up(p, entry, *entry, bad);
+            if (page >= 0 && atomicSub(p.a.shared + page, 1) < 0) bad |= kStatusCorrupt;  // more often than held
+        }
     }
     tell(p.a.status_dev, bad);
 }
@@ -252,53 +253,99 @@ __global__ __launch_bounds__(kPageThreads) void freed_write_kernel(ReleaseArgs p
 }
 
 // All of it by one workgroup, for few requests: the pages that become free are
-// bits in LDS, a run of words a thread, so that nothing is looked through.  A lane
-// reads a request's lengths and gives up a few entries by itself, as after
-// refused drafts; longer runs are taken by the wavefront, one after the other.
-constexpr uint32_t kFewRequests = 64, kFreedWords = 8, kFewFreed = 32u * kPageThreads * kFreedWords;
+// bits in LDS, so that nothing is looked through.  A page without other holders
+// becomes free at once; one with others counts one less, and whoever finds none
+// left frees it and puts the count back to 0.  Both may happen to one page, whose
+// bit then is set by one of them: which one makes no difference.  A lane reads a
+// request's lengths and gives up a few entries by itself, as after refused drafts;
+// longer runs are taken by the wavefront, eight entries a lane at a time.
+//
+// The call's own time here and in three launches, pages of 16 tokens: 64 requests
+// of up to 8191 cut by up to five 4 and 10 us, eight of 8191 that end 6 and 8, a
+// window's pages of 64 8 and 11, of 16 with 32768 7 and 11; but 32 of up to 8191
+// that end 15 and 12, and 64 of 8191 37 and 13, which no size on the host tells
+// from the first: one step of a program that cuts drafts at every step.
+constexpr uint32_t kFewRequests = 64, kFreedWords = 4, kFewFreed = 32u * kPageThreads * kFreedWords, kFewGiven = 65536;
 __global__ __launch_bounds__(kPageThreads) void release_few_kernel(ReleaseArgs p) {
     constexpr uint32_t kAlone = 2, kEach = kFewRequests / kPageWaves;
-    __shared__ uint32_t freed[kPageThreads * kFreedWords], part[kPageWaves];
+    __shared__ uint32_t freed[kPageThreads * kFreedWords], rank[kPageThreads * kFreedWords], part[kPageWaves];
     const dfc_release_args &a = p.a;
     const uint32_t tid = threadIdx.x, lane = tid % kWave, wave = __builtin_amdgcn_readfirstlane(tid / kWave);
     const Ring ring = ring_of(a.cursor, a.n_ring);
     uint32_t bad = 0;
     Given g{0u, 0u, 0u, 0u};
-    const uint32_t mine = wave * kEach + lane;
+    const uint32_t mine = wave + lane * kPageWaves;
     if (lane < kEach && mine < a.n_requests) g = given_of(p, mine, bad);
 #pragma unroll
     for (uint32_t i = 0; i < kFreedWords; ++i) freed[i * kPageThreads + tid] = 0;
     __syncthreads();
-    auto give_up = [&](uint32_t r, uint32_t i) {
-        const int32_t page = give(p, r, i, bad);
-        if (page >= 0) atomicOr(&freed[page >> 5], 1u << (page & 31));
+    auto drop = [&](int32_t page, int32_t others) {
+        if (page < 0) return;
+        if (others > 0) {
+            if (atomicSub(a.shared + page, 1) > 0) return;
+            atomicAdd(a.shared + page, 1);
+        }
+        const uint32_t bit = 1u << (page & 31);
+        if ((atomicOr(&freed[page >> 5], bit) & bit) || others < 0) bad |= kStatusCorrupt;  // more often than held
     };
     if (g.n <= kAlone)
-        for (uint32_t j = 0; j < g.n; ++j) give_up(mine, g.at(j));
+        for (uint32_t j = 0; j < g.n; ++j) {
+            int32_t *entry = entry_of(p, mine, g.at(j));
+            const int32_t page = given_up(p, entry, *entry, bad);
+            drop(page, page < 0 ? 0 : a.shared[page]);
+        }
 #pragma unroll
     for (uint32_t k = 0; k < kEach; ++k) {
         const uint32_t n = __builtin_amdgcn_readlane(g.n, k);
         if (n <= kAlone) continue;
         const Given o{uint32_t(__builtin_amdgcn_readlane(g.hole, k)), uint32_t(__builtin_amdgcn_readlane(g.n_hole, k)),
                       uint32_t(__builtin_amdgcn_readlane(g.begin, k)), n};
-        for (uint32_t j = lane; j < n; j += kWave) give_up(wave * kEach + k, o.at(j));
+        for (uint32_t j0 = 0; j0 < n; j0 += kAtOnce * kWave) {
+            int32_t *entry[kAtOnce], page[kAtOnce], others[kAtOnce];
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                const uint32_t j = j0 + i * kWave + lane;
+                entry[i] = entry_of(p, wave + k * kPageWaves, o.at(min(j, n - 1u)));
+                page[i] = j < n ? *entry[i] : -1;
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) {
+                page[i] = given_up(p, entry[i], page[i], bad);
+                others[i] = page[i] < 0 ? 0 : a.shared[page[i]];
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < kAtOnce; ++i) drop(page[i], others[i]);
+        }
     }
     __syncthreads();
-    uint32_t n = 0, total;
+    uint32_t n[kFreedWords], sum = 0, total;
 #pragma unroll
-    for (uint32_t i = 0; i < kFreedWords; ++i) n += uint32_t(__popc(freed[tid * kFreedWords + i]));
-    const uint32_t before = before_of(n, part, total);
+    for (uint32_t i = 0; i < kFreedWords; ++i) sum += n[i] = uint32_t(__popc(freed[tid * kFreedWords + i]));
+    uint32_t before = before_of(sum, part, total);
+#pragma unroll
+    for (uint32_t i = 0; i < kFreedWords; ++i) {
+        rank[tid * kFreedWords + i] = before;
+        before += n[i];
+    }
+    __syncthreads();
     const bool fits = ring.ok && total <= a.n_ring - ring.size;
     if (!fits) bad |= kStatusCorrupt;
-    if (n) {
-        uint32_t to = ring.size + before;
-        for (uint32_t i = 0; i < kFreedWords; ++i)
-            for (uint32_t left = freed[tid * kFreedWords + i]; left; left &= left - 1u) {
-                const uint32_t page = 32u * (tid * kFreedWords + i) + uint32_t(__builtin_ctz(left));
-                if (fits) a.free_pages[ring.at(to)] = int32_t(page);
-                ++to;
-                a.shared[page] = 0;
-            }
+    // a wavefront takes every 16th word, 64 of them at once and, of those that are
+    // not 0, two at a time
+#pragma unroll
+    for (uint32_t i = 0; i < kFreedWords; ++i) {
+        const uint32_t first = wave + i * kWave * kPageWaves;
+        for (uint64_t words = __ballot(freed[first + lane * kPageWaves] != 0); words;) {
+            const uint32_t one = uint32_t(__builtin_ctzll(words));
+            words &= words - 1u;
+            const uint32_t two = words ? uint32_t(__builtin_ctzll(words)) : one;
+            const uint32_t word = first + (lane < 32u ? one : two) * kPageWaves, bit = lane % 32u, x = freed[word];
+            if (!words && lane >= 32u) break;  // an odd one
+            words &= words - 1u;
+            if (!(x >> bit & 1u)) continue;
+            const uint32_t page = 32u * word + bit;
+            if (fits) a.free_pages[ring.at(ring.size + rank[word] + uint32_t(__popc(x & ((1u << bit) - 1u))))] = int32_t(page);
+        }
     }
     // (pages that others hold are none of those)
     if (lane < kEach && mine < a.n_requests) look_at_cut(p, mine, bad);
@@ -744,10 +791,10 @@ __global__ __launch_bounds__(kCopyThreads) void copy_kernel(CopyArgs a) {
             // (past the last pair, its piece again, not stored)
             there[i] = pair < n;
             const int2 l = list[min(pair, n - 1u)];
-            uint32_t in_page = piece;
+            uint64_t in_page = piece;
             if constexpr (!Run) {
                 const uint32_t head = piece / a.row;
-                in_page = head / a.heads * place_stride + head % a.heads * head_stride + piece % a.row;
+                in_page = uint64_t(head / a.heads) * place_stride + uint64_t(head % a.heads) * head_stride + piece % a.row;
             }
             x[i] = base[uint64_t(uint32_t(l.x)) * page_stride + in_page];
             to[i] = uint64_t(uint32_t(l.y)) * page_stride + in_page;
@@ -790,7 +837,7 @@ dfc_status dfc_paged_release(const dfc_release_args *args, void *stream) {
     hipStream_t st = static_cast<hipStream_t>(stream);
     const Slabs s = slabs_of(a.n_pages);
     const ReleaseArgs p{a, dfc::log2_of(a.page_size), s.count, s.rounds};
-    if (a.n_requests <= kFewRequests && a.n_pages <= kFewFreed) {
+    if (a.n_requests <= kFewRequests && a.n_pages <= kFewFreed && uint64_t(a.n_requests) * a.max_pages <= kFewGiven) {
         hipLaunchKernelGGL(release_few_kernel, dim3(1), dim3(kPageThreads), 0, st, p);
         return launched();
     }

@@ -153,6 +153,22 @@ def test_release_of_pages_held_by_all():
         same(got, want)
 
 
+@pytest.mark.parametrize("requests,longest,page", [(1, 5000, 1), (64, 1000, 1), (64, 8191, 16), (40, 1600, 1), (65, 900, 2)])
+def test_release_of_all_that_few_requests_hold(requests, longest, page):
+    # up to 64 requests are one workgroup's work, whose pages are bits in LDS
+    rng = np.random.default_rng(requests)
+    held = rng.integers(0, longest + 1, requests)
+    pool = Pool(held, page, seed=requests, share=0.5)
+    for keep in ([0] * requests, [0 if r % 3 else int(h) for r, h in enumerate(held)],
+                 [int(h) // page * page // 2 // page * page if r % 2 else int(h) for r, h in enumerate(held)]):
+        for window, sinks in ((0, 0), (100, 9)):
+            say("release of few", requests, longest, page, window)
+            got, st = release(pool, held, keep, window, sinks)
+            *want, cut = op.release(held, keep, pool.table, pool.ring, pool.cursor, pool.shared, page, window, sinks)
+            assert st == 0 and cut == []
+            same(got, want)
+
+
 def test_release_without_requests():
     e, c = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.tensor([3, 5], device="cuda")
     ring, shared = torch.arange(6, dtype=torch.int32, device="cuda"), torch.zeros(6, dtype=torch.int32, device="cuda")
@@ -504,6 +520,23 @@ def test_copy_past_2_to_the_32_bytes():
     dfc.paged_copy([(cache, other)], dev([1099999, 1099998]), dev([1, 1099990]))
     torch.cuda.synchronize()
     assert (cache[1] == 3).all() and (other[1099990] == 5).all() and not cache[2:1099990].any()
+
+
+def test_copy_where_a_pages_rows_lie_past_2_to_the_36_bytes():
+    # tokens of a page outside the pages: 4 x 1.6e6 pages of 14 KB
+    if torch.cuda.mem_get_info()[0] < 130 << 30:
+        pytest.skip("too little memory")
+    pages, heads, dim = 1600000, 28, 256
+    cache = torch.empty(4, pages, heads, dim, dtype=torch.bfloat16, device="cuda").transpose(0, 1)
+    assert cache.stride(1) * 3 // 8 > 2 ** 32 > cache.stride(1) // 8
+    for i in range(4):
+        cache[pages - 2, i], cache[1, i] = i + 1, -1
+    say("copy, rows far apart")
+    dfc.paged_copy([(cache, cache)], dev([pages - 2]), dev([1]))
+    torch.cuda.synchronize()
+    assert all((cache[p, i] == i + 1).all() for p in (1, pages - 2) for i in range(4))
+    del cache
+    torch.cuda.empty_cache()
 
 
 def test_copy_inputs_that_make_no_sense_and_refusals():
