@@ -215,6 +215,45 @@ def test_release_inputs_that_make_no_sense():
     assert st == 0
 
 
+def test_release_of_many_requests_that_make_no_sense():
+    # the same by several launches: 70 requests more, that hold nothing
+    more = [0] * 70
+
+    def go(pool, held, keep):
+        return release(pool, held + more, keep + more)
+
+    pool = Pool([40, 40, 40] + more, 16, seed=5)
+    for held, keep in (([-1, 40, 40], [0, 40, 40]), ([40, 40, 40], [-2, 40, 40]), ([40, 40, 40], [41, 40, 40])):
+        got, st = go(pool, held, keep)
+        assert st == dfc.ECORRUPT
+        same(got, (pool.table, pool.ring, pool.cursor, pool.shared))
+    got, st = go(pool, [40, 40, 16 * 5 + 1], [40, 40, 0])
+    assert st == dfc.ESIZE and (got[0][2] < 0).all()
+    pool.table[0, 1] = 10 ** 6
+    got, st = go(pool, [40, 40, 40], [0, 40, 40])
+    assert st == dfc.ECORRUPT and (got[0][0, :3] == -1).all() and int(got[2][1]) == pool.cursor[1] + 2
+    pool = Pool([40, 40, 40] + more, 16, seed=5)
+    pool.table[1, 0] = pool.table[0, 0]
+    got, st = go(pool, [40, 40, 40], [0, 0, 40])
+    assert st == dfc.ECORRUPT and int(got[2][1]) == pool.cursor[1] + 5 and not got[3].any()
+    for cursor in ([7, 7 + len(pool.ring) - 2], [9, 8], [-1, 3], [0, len(pool.ring) + 1]):
+        pool = Pool([40, 40, 40] + more, 16, seed=5)
+        pool.cursor = np.array(cursor, np.int64)
+        got, st = go(pool, [40, 40, 40], [0, 40, 40])
+        assert st == dfc.ECORRUPT and got[2].tolist() == cursor
+        same(got[1:2], [pool.ring])
+    pool = Pool([40, 40] + more, 16, seed=6)
+    pool.table[1, :2] = pool.table[0, :2]
+    pool.shared[pool.table[0, :2]] = 1
+    got, st = go(pool, [40, 40], [20, 40])
+    assert st == dfc.EUNSUPPORTED
+    *want, cut = op.release([40, 40] + more, [20, 40] + more, pool.table, pool.ring, pool.cursor, pool.shared, 16)
+    assert cut == [0]
+    same(got, want)
+    got, st = go(pool, [40, 40], [20, 0])
+    assert st == 0
+
+
 def test_release_refusals_and_results():
     pool = Pool([40, 20], 16, seed=7)
     table, ring, cursor, shared = pool.on_device()
@@ -381,7 +420,8 @@ def compact(pool, context):
 
 @pytest.mark.parametrize("page", [1, 16])
 @pytest.mark.parametrize("requests,longest,spare,reserve", [(1, 1, 0, 0), (1, 5, 1, 0), (3, 100, 30, 0), (64, 300, 9, 5),
-                                                            (64, 30, 5000, 11), (700, 40, 300, 0), (300, 900, 20000, 7)])
+                                                            (64, 30, 5000, 11), (700, 40, 300, 0), (300, 900, 20000, 7),
+                                                            (1025, 9, 100, 3), (30, 4000, 500, 0), (2, 8100, 1, 0)])
 @pytest.mark.parametrize("share", [0.0, 0.6])
 def test_compact(requests, longest, spare, reserve, page, share):
     rng = np.random.default_rng(requests + spare + page)
@@ -406,10 +446,11 @@ def test_compact_where_nothing_moves():
     same(again, [g.cpu().numpy() for g in got])
 
 
-def test_compact_where_ring_and_tables_contradict():
+@pytest.mark.parametrize("spare", [30, 20000])  # by one workgroup, by several launches
+def test_compact_where_ring_and_tables_contradict(spare):
     lens = [100, 50]
     for spoil in ("twice on the ring", "held and on the ring", "past the cache", "negative", "cursor", "held past"):
-        pool = Pool(lens, 4, seed=2, spare=30)
+        pool = Pool(lens, 4, seed=2, spare=spare)
         n, head = len(pool.ring), int(pool.cursor[0])
         if spoil == "twice on the ring":
             pool.ring[(head + 5) % n] = pool.ring[(head + 2) % n]
@@ -428,7 +469,7 @@ def test_compact_where_ring_and_tables_contradict():
         assert st == dfc.ECORRUPT, spoil
         same(got[:3], (pool.table, pool.ring, pool.shared))
         assert (got[3] == -1).all() and (got[4] == -1).all()
-    pool = Pool(lens, 4, seed=2, spare=30)
+    pool = Pool(lens, 4, seed=2, spare=spare)
     got, st = compact(pool, [100, 4 * pool.table.shape[1] + 1])   # past the row, whose rest is no page
     assert st == dfc.ESIZE
     same(got, op.compact(lens, pool.table, pool.ring, pool.cursor, pool.shared, 4))

@@ -222,6 +222,49 @@ def test_a_program_over_many_steps(window, sinks):
     assert not p.shared.any() and int(p.cursor[1] - p.cursor[0]) == p.pages
 
 
+@pytest.mark.parametrize("given", ["another stream", "the default stream"])
+def test_what_a_call_allocates_belongs_to_its_stream(given):
+    # a given stream does not wait for the current one, whose earlier work may
+    # still use memory that torch hands out on the current stream
+    from test_gpu_paged import pool_of
+    R, P, pages = 3, 8, 40
+    lens, keep, parents = i32([50, 23, 0]), i32([44, 0, 0]), i32([-1, -1, 0])
+    table = i32([[*range(7)], [*range(10, 13)] + [-1] * 4, [-1] * 7])
+    free = torch.tensor([p for p in range(pages) if p > 6 and not 10 <= p < 13], device="cuda").int()
+    logits, cu = torch.randn(5, 700, device="cuda"), i32([0, 3, 4, 5])
+    u, x = torch.rand(5, device="cuda"), torch.randint(0, 700, (5,), device="cuda")
+    cache = torch.randn(2, pages, P, 2, 64, device="cuda").bfloat16()
+    k, w = torch.randn(4, 2, 64, device="cuda"), torch.ones(64, device="cuda")
+    slots = torch.arange(4, device="cuda")
+
+    def calls(stream):
+        t, ring, cursor, shared = table.clone(), free.clone(), torch.tensor([0, free.numel()], device="cuda"), i32([0] * pages)
+        ring = torch.cat([ring, i32([0] * 20)])
+        c = cache.clone()
+        torch.cuda.synchronize()
+        end = dfc.paged_release(lens, keep, t, ring, cursor, shared, P, stream=stream)
+        f = dfc.paged_fork(keep, parents, t, ring, end, shared, P, stream=stream)
+        dfc.paged_copy([(c[0], c[1])], f.src, f.dst, stream=stream)
+        m = dfc.paged_compact(f.context_lens, t, ring, f.cursor, shared, P, stream=stream)
+        dfc.paged_copy([(c[0], c[1])], m.src, m.dst, stream=stream)
+        v = dfc.verify_drafts(logits, cu, x, u, draft_logits=logits.flip(0), stream=stream)
+        q = dfc.paged_append(k, k, c[0], c[1], slots, q=k, q_norm=w, k_norm=w, stream=stream)
+        torch.cuda.synchronize()
+        return [end, *f, *m, *v, q], [t, ring, shared, c]
+
+    plain, kept = calls(None)
+    side = torch.cuda.Stream()
+    say("allocations", given)
+    if given == "another stream":
+        handle, (got, left) = side.cuda_stream, calls(side.cuda_stream)
+    else:
+        with torch.cuda.stream(side):
+            handle, (got, left) = 0, calls(0)
+    for a, b in zip(plain, got):
+        assert pool_of(b) == handle and torch.equal(a, b)
+    assert all(torch.equal(a, b) for a, b in zip(kept, left))
+
+
 def test_captured_steps_follow_their_inputs():
     """Plan, append, attention, verification and release captured once, fork and
     copy and compact each once; replays with other lengths between them, with
