@@ -11,7 +11,8 @@
 // dfc_paged_append.  Token t's keys and values go to row slots[t] of the
 // cache, rounded to its type; q and k are first rotated by the angles of
 // their position: (a, b) -> (a cos - b sin, b cos + a sin) over the pairs
-// (i, i + half) or (2i, 2i + 1).
+// (i, i + half) or (2i, 2i + 1).  With norms each head of q and k is first
+// x w / sqrt(mean(x^2) + eps), in the same pass.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -286,7 +287,9 @@ __device__ __forceinline__ void norm(const AppendArgs &p, const void *weights, u
 // read twice, took 52).  64 tokens from float32 take 6 us, a launch and one chain of
 // loads.
 // With norms the threads of a head are a power of two side by side (those past
-// its chunks only lend a hand to the sum).
+// its chunks only lend a hand to the sum); 8,192 tokens then take 43-47 us (4.4-4.8
+// TB/s), the weights' loads and the sum in 64 bits on top of what bounds them
+// without (2 us each; four tokens a thread, which load the weights once, 59).
 template <typename S, typename E, bool Past, bool Norm>
 __global__ __launch_bounds__(256) void append_kernel(AppendArgs p) {
     using E8 = __attribute__((ext_vector_type(8))) E;

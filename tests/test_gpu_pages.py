@@ -436,6 +436,16 @@ def test_compact(requests, longest, spare, reserve, page, share):
     same(got, op.compact(lens, pool.table, pool.ring, pool.cursor, pool.shared, page))
 
 
+def test_compact_without_requests():
+    e, cursor = torch.zeros(0, dtype=torch.int32, device="cuda"), torch.tensor([4, 8], device="cuda")
+    for width in (0, 5):
+        ring, shared = dev([9, 2, 7, -1, 0]), dev([0] * 10)
+        m = dfc.paged_compact(e, torch.zeros(0, width, dtype=torch.int32, device="cuda"), ring, cursor, shared, 16)
+        # the ring in ascending order from its head on
+        assert ring.tolist() == [2, 7, 9, -1, 0]
+        assert m.src.tolist() == [-1] * 5 and m.dst.tolist() == [-1] * 5 and m.used.tolist() == [0]
+
+
 def test_compact_where_nothing_moves():
     for lens, spare in (([0, 0], 20), ([100, 50], 0)):
         pool = Pool(lens, 4, seed=1, spare=spare)
