@@ -700,7 +700,8 @@ typedef struct {
  * (DFC_ECORRUPT).  Uniforms outside [0, 1) count as the nearest value in it, NaN
  * as 0 for the token and as not holding for a draft.  A request without rows:
  * 0 and -1.  Errors: DFC_EINVAL, DFC_ESIZE (workspace), DFC_EUNSUPPORTED
- * (types, sizes), DFC_EHIP. */
+ * (types; sizes: rows, with a drafter's twice, or requests times
+ * ceil(vocab / 4096) past 2^24 - 1), DFC_EHIP. */
 dfc_status dfc_verify_drafts(const dfc_verify_args *args, void *stream);
 
 /* Bytes of the workspace for those sizes (host; rows, vocab and n_requests

@@ -984,7 +984,7 @@ dfc_status dfc_paged_copy(const dfc_paged_cache *caches, uint32_t n_caches, cons
         const uint64_t pairs = std::min<uint64_t>(std::max(fill, few), kCopyList);
         a.groups = uint32_t(dfc::ceil_div(uint64_t(n), pairs));
         const uint64_t blocks = uint64_t(a.groups) * a.parts;
-        if (blocks > 0x7fffffffull) return DFC_EUNSUPPORTED;
+        if (blocks > 0xffffffffu / kCopyThreads) return DFC_EUNSUPPORTED;  // threads of a launch, in 32 bits
         if (whole)
             hipLaunchKernelGGL((copy_kernel<true>), dim3(uint32_t(blocks)), dim3(kCopyThreads), 0, st, a);
         else

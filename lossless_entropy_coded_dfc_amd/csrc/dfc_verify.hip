@@ -42,6 +42,7 @@ constexpr uint32_t kVWaves = kVThreads / kWave;
 constexpr uint32_t kPerLane = 16;                    // values
 constexpr uint32_t kPiece = kPerLane * kWave;
 constexpr uint32_t kMostRequests = 65536;
+constexpr uint32_t kMostGroups = 0xffffffffu / kVThreads;  // a launch counts its threads in 32 bits
 
 // What a row's piece holds; top is NaN where a value is NaN or +inf.
 struct alignas(16) Part {
@@ -150,6 +151,11 @@ __device__ __forceinline__ double weight_of(float z, float top, double rate) {
     return exp2_of((double(z) - double(top)) * rate);
 }
 __device__ __forceinline__ double rate_of(float t) { return t > 0.0f ? 1.4426950408889634 / double(t) : 0.0; }
+
+// The value in [0, 1) nearest to a random number that is none; NaN stays.
+__device__ __forceinline__ float within(float u) {
+    return u != u ? u : fminf(fmaxf(u, 0.0f), 0x1.fffffep-1f);
+}
 
 // The request of a row: the number of requests that end at or before it.
 __device__ __forceinline__ uint32_t request_of(const dfc_verify_args &a, uint32_t row) {
@@ -368,7 +374,7 @@ __device__ __forceinline__ Found decide(const VerifyArgs &p, uint32_t r, Decisio
                         if (!v.ok) f.mode = kNone;  // nothing can be drawn against what is not known
                         if (there) qx = share(a.draft_logits_dev, a.draft_stride, v);
                     }
-                    stops = f.mode == kNone || !(double(a.uniforms[row]) * qx < px);
+                    stops = f.mode == kNone || !(double(within(a.uniforms[row])) * qx < px);
                     if (stops && f.mode == kPlain) {
                         if (against)
                             f.mode = kRest;
@@ -451,6 +457,7 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
     const double *rest = p.rest + uint64_t(r) * p.pieces;
     double all = 0.0, without = 0.0;  // without: the drafted token's piece without it
     double w[kPerLane], ahead[kAhead];
+    bool some[kAhead];
     auto weight = [&](uint32_t k) -> double {
         if (k >= p.pieces) return 0.0;
         if (f.mode == kRest) return rest[k];
@@ -467,7 +474,10 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
             without = over_wave<Sum>(without);
         }
 #pragma unroll
-        for (uint32_t i = 0; i < kAhead; ++i) ahead[i] = weight(i * kWave + lane);
+        for (uint32_t i = 0; i < kAhead; ++i) {
+            ahead[i] = weight(i * kWave + lane);
+            some[i] = ahead[i] > 0.0;
+        }
 #pragma unroll
         for (uint32_t i = 0; i < kAhead; ++i) {
             ahead[i] = scan_of<Sum>(ahead[i]);
@@ -479,13 +489,13 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
         f.mode = kPlain;  // nothing is left: of p
         f.drafted = -1;
     }
-    u = !(u >= 0.0f) ? 0.0f : fminf(u, 0x1.fffffep-1f);
-    const double share = double(u) * all;
+    const double share = u == u ? double(within(u)) * all : 0.0;
     double before = 0.0;
     uint32_t piece = 0;
     bool found = false;
-    auto look = [&](uint32_t k0, double sum) {
-        const uint64_t past = __ballot(before + sum > share);
+    // (prefix sums round apart: one may pass where nothing was added)
+    auto look = [&](uint32_t k0, double sum, bool has) {
+        const uint64_t past = __ballot(has && before + sum > share);
         if (past) {
             const uint32_t who = uint32_t(__builtin_ctzll(past));
             piece = k0 + who;
@@ -497,9 +507,12 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
     };
 #pragma unroll
     for (uint32_t i = 0; i < kAhead; ++i)
-        if (!found) look(i * kWave, ahead[i]);
+        if (!found) look(i * kWave, ahead[i], some[i]);
 #pragma unroll 1
-    for (uint32_t k0 = kAhead * kWave; k0 < p.pieces && !found; k0 += kWave) look(k0, scan_of<Sum>(weight(k0 + lane)));
+    for (uint32_t k0 = kAhead * kWave; k0 < p.pieces && !found; k0 += kWave) {
+        const double own = weight(k0 + lane);
+        look(k0, scan_of<Sum>(own), own > 0.0);
+    }
     weights_of<E>(p, f, t, piece, w);
     uint32_t last = 0;
 #pragma unroll
@@ -511,7 +524,7 @@ __device__ __forceinline__ int64_t draw(const VerifyArgs &p, Found f, uint32_t r
             if (w[g * W + j] > 0.0) last = index_of<W>(piece, g * W + j);
         }
         const double sum = scan_of<Sum>(own);
-        const uint64_t past = __ballot(before + sum > share);
+        const uint64_t past = __ballot(own > 0.0 && before + sum > share);
         if (past) {
             double at = before + shifted<0x138, 0xf>(sum, 0.0);  // of the lanes below
             uint32_t token = last;  // (of this lane: its last with any weight)
@@ -557,6 +570,7 @@ __global__ __launch_bounds__(Decided ? kWave : kDecideThreads) void token_kernel
 }
 
 uint32_t pieces_of(const dfc_verify_args &a) { return uint32_t(dfc::ceil_div(uint64_t(a.vocab), uint64_t(kPiece))); }
+uint32_t groups_of(const dfc_verify_args &a) { return uint32_t(dfc::ceil_div(uint64_t(pieces_of(a)), uint64_t(kVWaves))); }
 
 uint64_t workspace_of(const dfc_verify_args &a) {
     const uint64_t pieces = pieces_of(a), parts = a.rows * pieces * sizeof(Part);
@@ -568,8 +582,9 @@ uint64_t workspace_of(const dfc_verify_args &a) {
 
 dfc_status check_verify(const dfc_verify_args &a) {
     if (a.dtype != DFC_F32 && a.dtype != DFC_BF16 && a.dtype != DFC_F16) return DFC_EUNSUPPORTED;
-    if (!a.vocab || a.vocab > (1u << 30) || a.n_requests > kMostRequests || a.rows > 0x3fffffffull) return DFC_EUNSUPPORTED;
-    return DFC_OK;
+    if (!a.vocab || a.vocab > (1u << 30) || a.n_requests > kMostRequests || a.rows > kMostGroups) return DFC_EUNSUPPORTED;
+    const uint64_t rows = std::max<uint64_t>(a.draft_logits_dev ? 2u * a.rows : a.rows, a.n_requests);
+    return rows * groups_of(a) > kMostGroups ? DFC_EUNSUPPORTED : DFC_OK;
 }
 
 template <typename E>
@@ -577,7 +592,6 @@ dfc_status launch_verify(const VerifyArgs &p, hipStream_t st) {
     const dfc_verify_args &a = p.a;
     const uint64_t rows = a.rows * (a.draft_logits_dev ? 2u : 1u);
     const uint64_t parts = rows * p.groups, rests = uint64_t(a.n_requests) * p.groups;
-    if (parts > 0x7fffffffull || rests > 0x7fffffffull) return DFC_EUNSUPPORTED;
     if (parts) hipLaunchKernelGGL((parts_kernel<E>), dim3(uint32_t(parts)), dim3(kVThreads), 0, st, p);
     if (a.draft_logits_dev) {
         hipLaunchKernelGGL((decide_kernel<E>), dim3(a.n_requests), dim3(kDecideThreads), 0, st, p);
@@ -616,7 +630,7 @@ dfc_status dfc_verify_drafts(const dfc_verify_args *args, void *stream) {
     std::memset(&p, 0, sizeof(p));
     p.a = a;
     p.pieces = pieces_of(a);
-    p.groups = uint32_t(dfc::ceil_div(uint64_t(p.pieces), uint64_t(kVWaves)));
+    p.groups = groups_of(a);
     uint8_t *work = static_cast<uint8_t *>(a.workspace_dev);
     const uint64_t parts = a.rows * p.pieces * sizeof(Part);
     p.target = reinterpret_cast<Part *>(work);

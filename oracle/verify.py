@@ -56,7 +56,8 @@ def request(logits, drafts, uniforms, draft_logits=None, temperature=1.0):
             if q is None:
                 return i, -1, margin
         px, qx = (p[x], q[x]) if there else (0.0, 1.0)
-        bar = float(uniforms[i]) * qx
+        u = float(uniforms[i])
+        bar = (u if u != u else min(max(u, 0.0), 1 - 2.0 ** -24)) * qx
         if px > 0 and temperature > 0:
             margin = min(margin, abs(bar - px) / px)
         if not bar < px:

@@ -179,6 +179,57 @@ def test_random_numbers_at_the_ends():
                 assert 0 <= got[1][r] < 2000
 
 
+def test_random_numbers_that_are_none():
+    """Below 0 they count as 0, from 1 on as the largest below it; NaN holds no draft."""
+    # p: 0.25, 0.75, 0, 0; all of it on token 1; the drafts have p > 0, p = 0, p = 1 and none
+    z = torch.tensor([[0.0, np.log(3.0), -np.inf, -np.inf], [-np.inf, 0.0, -np.inf, -np.inf]],
+                     dtype=torch.float32)
+    cases = [(0, 0), (0, 2), (1, 1), (0, 7), (0, -3)]
+    us = [-1.0, -0.0, float("-inf"), 1.0, 2.0, float("inf"), float("nan")]
+    for drafter in (False, True):
+        logits = torch.cat([z[[row, 0]] for row, _ in cases for _ in us])
+        drafts = torch.tensor([[x, 0] for _, x in cases for _ in us]).flatten()
+        u = torch.tensor([[v, 0.5] for _ in cases for v in us]).flatten()
+        cu = torch.arange(0, len(u) + 1, 2, dtype=torch.int32)
+        q = torch.zeros_like(logits) if drafter else None
+        say("verify, random numbers that are none", drafter)
+        got = dfc.verify_drafts(logits.cuda(), cu.cuda(), drafts.cuda(), u.cuda(),
+                                draft_logits=None if q is None else q.cuda())
+        torch.cuda.synchronize()
+        for r in range(len(cu) - 1):
+            i = slice(2 * r, 2 * r + 2)
+            want = ov.request(logits[i].double().numpy(), drafts[i].tolist(), u[i].tolist(),
+                              None if q is None else q[i].double().numpy())[:2]
+            assert (int(got.accepted[r]), int(got.tokens[r])) == want, (drafter, r)
+        if not drafter:
+            held = got.accepted.reshape(len(cases), len(us)).tolist()
+            assert held[0] == [1, 1, 1, 0, 0, 0, 0] and held[2] == [1] * 6 + [0]
+            assert held[1] == held[3] == held[4] == [0] * 7
+
+
+@pytest.mark.parametrize("vocab", [70, 5000, 300001])
+def test_random_numbers_at_the_borders_of_few_tokens(vocab):
+    """Most logits -inf, random numbers next to the sums' borders: whatever
+    the roundings do there, a token without probability is never drawn."""
+    g = torch.Generator().manual_seed(vocab)
+    row = torch.full((vocab,), float("-inf"))
+    at = torch.randperm(vocab, generator=g)[:20].sort().values
+    row[at] = torch.randn(20, generator=g)
+    p = ov.softmax(row.numpy(), 1.0)
+    sums = np.cumsum(p)[at.numpy()]
+    u = torch.tensor(sums, dtype=torch.float32)
+    u = torch.cat([u, torch.nextafter(u, torch.zeros(1)), torch.nextafter(u, torch.ones(1))])
+    cu = torch.arange(len(u) + 1, dtype=torch.int32)
+    say("verify, borders of few tokens", vocab)
+    v = dfc.verify_drafts(row.cuda().expand(len(u), vocab).contiguous(), cu.cuda(),
+                          torch.zeros(len(u), dtype=torch.int64, device="cuda"), u.cuda())
+    tokens = v.tokens.cpu()
+    assert torch.isin(tokens, at).all()
+    for t, x in zip(tokens.tolist(), u.tolist()):
+        j, near = ov.pick(p, x)
+        assert near <= NEAR or t == j
+
+
 def test_the_same_logits_for_drafter_and_model_hold_everything():
     s = Step([6] * 20, 700, seed=10, temperature=1.3)
     s.store[1] = s.store[0]

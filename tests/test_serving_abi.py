@@ -181,6 +181,10 @@ def test_verify_refusals_and_workspace():
     good.draft_logits_dev = None
     assert lib.dfc_verify_workspace(good, ctypes.byref(size)) == dfc.OK and size.value < both
     refused("dfc_verify_drafts", good, dfc.OK, n_requests=0)
+    # groups of 4096 values: 2^24 - 1 of all rows, the drafter's too, and of all requests
+    for change in (dict(rows=1 << 24), dict(rows=1 << 20, vocab=65536 + 1), dict(vocab=1 << 30, n_requests=64, rows=64),
+                   dict(rows=1 << 23, draft_logits_dev=256)):
+        refused("dfc_verify_drafts", good, dfc.EUNSUPPORTED, **dict(dict(logits_stride=1 << 30, draft_stride=1 << 30), **change))
     logits = torch.zeros(5, 1000)
     assert dfc.verify_drafts_workspace(logits, torch.zeros(3, dtype=torch.int32)) == size.value
     assert dfc.verify_drafts_workspace(logits, torch.zeros(3, dtype=torch.int32), logits) == both
