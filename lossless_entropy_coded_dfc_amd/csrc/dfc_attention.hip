@@ -945,7 +945,8 @@ int tile_height(const dfc_attention_args &a, uint32_t sinks) {
     return rw == 8 && !same ? 4 : rw;
 }
 
-LaunchPlan launch_plan(const dfc_attention_args &a, uint32_t sinks, int rw) {
+// `cut`: a split counts for as little as it costs under a window, see below.
+LaunchPlan launch_plan(const dfc_attention_args &a, uint32_t sinks, int rw, bool cut = false) {
     LaunchPlan p;
     const uint32_t group = a.heads / a.cache.kv_heads;
     p.dp = padded_dim(a);
@@ -962,6 +963,12 @@ LaunchPlan launch_plan(const dfc_attention_args &a, uint32_t sinks, int rw) {
     // of it 300 over 700 took 33.6 and not 29.8
     p.piece_cost = 4.0f;
     p.split_cost = float(p.most_rows) / 4.0f;
+    // Tall tiles under a window are longer than those: with sinks a split counts
+    // for less (us with a quarter and a tenth of the rows, 32 heads over 8 of 128:
+    // 1000 tokens over 32000 under 4096 + 64 138 and 102, 768 under 8192 + 64 250
+    // and 142, 513 over 8192 under 2048 + 16 63 and 48, eight times 128 over 8000
+    // 140 and 105; prompts the same).  Calls without sinks are left as they round.
+    if (cut && p.rw >= 4) p.split_cost = float(p.most_rows) / 10.0f;
     p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
     const uint64_t tiles = most_tiles(a, p.rw);
     // a tile of c key tiles has at most ceil(c / min_piece) pieces
@@ -1098,8 +1105,12 @@ dfc_status dfc_paged_attention_sinks(const dfc_attention_args *args, uint32_t si
     if (reinterpret_cast<uintptr_t>(in.workspace_dev) & 255u) return DFC_EINVAL;
     for (int i = 0; i < 2; ++i)
         if (in.q_stride[i] % 8 || in.out_stride[i] % 8) return DFC_EINVAL;
-    const LaunchPlan p = launch_plan(in, sinks, tile_height(in, sinks));
-    if (in.workspace_bytes < workspace_bytes(in)) return DFC_ESIZE;
+    const uint64_t bytes = workspace_bytes(in);
+    if (in.workspace_bytes < bytes) return DFC_ESIZE;
+    const int rw = tile_height(in, sinks);
+    LaunchPlan p = launch_plan(in, sinks, rw, sinks > 0);
+    // where no call without a window splits its tiles there is no room for it
+    if (p.bytes > bytes) p = launch_plan(in, sinks, rw);
     AttnArgs a;
     std::memset(&a, 0, sizeof(a));
     a.q = in.q_dev;

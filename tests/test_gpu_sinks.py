@@ -213,3 +213,30 @@ def test_layouts_workspace_and_refusals():
             dfc.paged_attention(q, k, v, table, cu, lens, window=3, sinks=sinks)
     with pytest.raises(TypeError):
         dfc.paged_attention(q, k, v, table, cu, lens, window=3, sinks=2.5)
+
+
+@pytest.mark.parametrize("total,new,heads,kv_heads,dim,window,sinks", [
+    ([8200], [513], 32, 8, 128, 2048, 16),     # tiles of 128 rows, split
+    ([9000], [1000], 32, 8, 128, 4096, 64),    # of 256, split
+    ([9000], [700], 16, 4, 64, 5000, 3),
+    ([1024], [1024], 32, 8, 128, 1000, 4),     # a table as short as the window
+    ([1100, 5000], [600, 100], 32, 8, 128, 1000, 4),
+    ([3000] * 6, [128] * 6, 32, 8, 128, 1500, 40),
+    ([4000], [500], 8, 2, 256, 2500, 10),
+])
+def test_tall_tiles_stay_in_the_workspace(total, new, heads, kv_heads, dim, window, sinks):
+    s = Step(total, new, heads, kv_heads, dim, 16, torch.bfloat16, seed=sum(new))
+    q, k, v, table, cu, lens = s.q.cuda(), s.k.cuda(), s.v.cuda(), s.table.cuda(), s.cu.cuda(), s.lens.cuda()
+    for most in (0, max(new)):
+        size = dfc.paged_attention_workspace(q, k, v, table, cu, lens, most)
+        store = torch.full((size + 4096,), 170, dtype=torch.uint8, device="cuda")
+        say("sinks, tall tiles", total[:2], new[:2], window, most)
+        first = [t.clone() for t in dfc.paged_attention(q, k, v, table, cu, lens, window=window, sinks=sinks, lse=True,
+                                                        max_q_len=most, workspace=store[:size])]
+        again = dfc.paged_attention(q, k, v, table, cu, lens, window=window, sinks=sinks, lse=True, max_q_len=most)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(first, again))
+        assert (store[size:] == 170).all()
+        assert torch.isfinite(first[0].float()).all() and torch.isfinite(first[1]).all()
+        rows = sorted({i for i in (0, 31, 32, 63, 64, new[0] // 2, new[0] - 2, new[0] - 1) if 0 <= i < new[0]})
+        check(s, *first, window, sinks, rows=rows)
