@@ -693,7 +693,7 @@ typedef struct {
  * token drawn from the logits.  T = 0: p is 1 at the lowest index of the
  * largest logit, so a draft holds if it is that.  Logits of -inf have
  * probability 0.  Exponentials, sums and comparisons are in 64 bits, whose
- * roundings move the border between two tokens by some 1e-14.  A row that holds
+ * errors move the border between two tokens by less than 1e-13.  A row that holds
  * NaN or +inf or nothing above -inf, and a temperature that is negative or not
  * finite, give no probabilities: no draft holds there and the token is -1
  * (DFC_ECORRUPT in the status).  A draft outside the vocabulary does not hold

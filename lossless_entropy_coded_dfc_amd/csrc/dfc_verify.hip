@@ -20,11 +20,11 @@
 // two rows read again, since max(p - q, 0) needs both of their sums first.
 //
 // Bounds (one MI355X, 128256 values a row in fp32).  64 requests of five drafts,
-// 328 MB of logits that count: the pass over them 72-82 us, 4.0-4.6 TB/s, by its
-// instructions in 64 bits (three quarters of the time the vector units are busy;
-// with sums of the values in place of their exponentials it took 50), then 7 us to
-// decide, 14 for the refused rows (66 MB, 4.7 TB/s), 6 for the tokens.  One row:
-// 2.5 and 5 us, latency.
+// 328 MB of logits that count: the pass over them 68-75 us, 4.4-4.8 TB/s, nearly
+// the rate of a copy and nearly as long as its 23 instructions a value take (with
+// sums of the values in place of their exponentials it took 50), then 7 us to
+// decide, 14 for the refused rows (66 MB, 4.7 TB/s), 5 for the tokens.  One row:
+// 3.5 and 6 us, latency.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -123,25 +123,25 @@ __device__ __forceinline__ T over_wave(T x) {
     return of_lane(scan_of<F>(x), kWave - 1);
 }
 
-// 2^t for t <= 0, within 5e-16 of it: t = n + f with |f| <= 1/2 by adding and
-// taking off a number whose last bit is 1, and 2^f by the polynomial of degree 10
-// through its values at the Chebyshev nodes of [-1/2, 1/2].  A library's
-// exponential has twice the instructions, which decide: 64 requests of five drafts
-// 129 us with it and 106 with this.  (With a table of 64 roots and degree 4, a
-// quarter fewer, it took the same.)
+// 2^t for t <= 0, within 4e-14 of it and 1 for 0: t = n + f with |f| <= 1/2 by
+// adding and taking off a number whose last bit is 1, and 2^f as 1 + f q(f), q the
+// polynomial of degree 8 through (2^f - 1) / f at the Chebyshev nodes of
+// [-1/2, 1/2].  Its instructions decide: 64 requests of five drafts 129 us with a
+// library's exponential, which has twice as many, and 106 with a degree more than
+// here, of which each is 3.  (With a table of 64 roots and degree 4, a quarter
+// fewer, it took the same.)
 __device__ __forceinline__ double exp2_of(double t) {
     t = fmax(t, -1100.0);  // (2^-1100 is 0)
     const double whole = t + 0x1.8p52, f = t - (whole - 0x1.8p52);
-    double y = 0x1.e6063f7217bc6p-28;
-    y = fma(y, f, 0x1.b675bca4eeebbp-24);
-    y = fma(y, f, 0x1.62bfd47773353p-20);
-    y = fma(y, f, 0x1.ffcb54062e698p-17);
-    y = fma(y, f, 0x1.430913096fd9fp-13);
-    y = fma(y, f, 0x1.5d87fe9d7a584p-10);
-    y = fma(y, f, 0x1.3b2ab6fba1ddap-7);
-    y = fma(y, f, 0x1.c6b08d703ce49p-5);
-    y = fma(y, f, 0x1.ebfbdff82c598p-3);
-    y = fma(y, f, 0x1.62e42fefa3a19p-1);
+    double y = 0x1.b63880a30e9ffp-24;
+    y = fma(y, f, 0x1.63d136366db24p-20);
+    y = fma(y, f, 0x1.ffcb9515a8016p-17);
+    y = fma(y, f, 0x1.4308ac85aa947p-13);
+    y = fma(y, f, 0x1.5d87fe86fe88ep-10);
+    y = fma(y, f, 0x1.3b2ab7181b755p-7);
+    y = fma(y, f, 0x1.c6b08d7047e52p-5);
+    y = fma(y, f, 0x1.ebfbdff823cedp-3);
+    y = fma(y, f, 0x1.62e42fefa39efp-1);
     y = fma(y, f, 1.0);
     return __builtin_ldexp(y, int(uint32_t(__builtin_bit_cast(uint64_t, whole))));
 }
@@ -188,8 +188,8 @@ __device__ __forceinline__ uint32_t index_of(uint32_t piece, uint32_t i) {
 }
 
 // A lane's 16 values of a piece of a row; -inf past the row.  Loads pass the
-// caches by: most logits are read once (64 requests of five drafts 101 us and not
-// 104, one row the same).
+// caches by: most logits are read once (64 requests of five drafts 3% faster, one
+// row the same).
 template <typename E>
 __device__ __forceinline__ void load_piece(const E *row, uint32_t vocab, uint32_t piece, float (&x)[kPerLane]) {
     constexpr uint32_t W = 16u / sizeof(E);
@@ -214,13 +214,10 @@ __device__ __forceinline__ void load_piece(const E *row, uint32_t vocab, uint32_
 template <typename E>
 __device__ __forceinline__ Part part_of(const float (&x)[kPerLane], uint32_t piece, float t) {
     constexpr uint32_t W = 16u / sizeof(E);
-    float top = -INFINITY;
-    bool odd = false;
+    float top = x[0];  // NaN if one is: an instruction for two values, where fmaxf took four
 #pragma unroll
-    for (uint32_t i = 0; i < kPerLane; i += 2) {
-        top = fmaxf(top, fmaxf(x[i], x[i + 1]));
-        odd |= __builtin_isunordered(x[i], x[i + 1]);
-    }
+    for (uint32_t i = 1; i < kPerLane; ++i) top = __builtin_elementwise_maximum(top, x[i]);
+    const bool odd = top != top;
     top = over_wave<Largest>(top);
     Part p{top, 0u, 0.0};
     if (__any(odd) || top == INFINITY) {
