@@ -349,3 +349,61 @@ def test_captured_steps_follow_their_inputs():
                     a, b = a[:n], b[:n]
                 assert torch.equal(a, b), (i, call.__name__, j)
     assert int(status.item()) == 0
+
+
+def test_two_programs_at_once():
+    """Steps of two programs on two streams, neither waiting for the other: each
+    one's results are those it has alone."""
+    R, H, K, D, P, V, T, pages, rounds = 70, 4, 2, 64, 8, 9000, 210, 1024, 6
+
+    def program(seed):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        randn = lambda *s: torch.randn(s, generator=g, device="cuda")
+        context = torch.randint(0, 60, (R,), generator=g, device="cuda").int()
+        new = torch.full((R,), 3, dtype=torch.int32, device="cuda")
+        table, ring = i32([[-1] * 20] * R), torch.randperm(pages, generator=g, device="cuda").int()
+        cursor, shared, status = torch.tensor([0, pages], device="cuda"), i32([0] * pages), i32([0])
+        caches = randn(2, pages, P, K, D).bfloat16()
+        q, k, v, u, w = randn(T, H, D), randn(T, K, D), randn(T, K, D), torch.rand(T, generator=g, device="cuda"), randn(D)
+        logits, drafter, drafts = randn(T, V), randn(T, V), torch.randint(0, V, (T,), generator=g, device="cuda")
+        parents = i32([-1] * (R - 3) + [0, 1, 2])
+        torch.cuda.synchronize()
+        outs, none = [], torch.zeros_like(context)
+        # what they hold at first
+        first = dfc.paged_plan(none, context, table, ring, cursor, P, int(R * 60), status=status)
+        cursor, keep = first.cursor, context
+        for _ in range(rounds):
+            plan = dfc.paged_plan(keep, new, table, ring, cursor, P, T, status=status)
+            x = dfc.paged_append(k, v, caches[0], caches[1], plan.slots, q=q, q_norm=w, k_norm=w, status=status)
+            x = dfc.paged_attention(x, caches[0], caches[1], table, plan.cu_q, plan.seq_lens, window=30, sinks=9,
+                                    status=status)
+            ver = dfc.verify_drafts(logits, plan.cu_q, drafts, u, draft_logits=drafter, status=status)
+            keep = keep + 1 + ver.accepted
+            keep[-3:] = 0
+            cursor = dfc.paged_release(plan.seq_lens, keep, table, ring, plan.cursor, shared, P, status=status)
+            f = dfc.paged_fork(keep, parents, table, ring, cursor, shared, P, status=status)
+            dfc.paged_copy([tuple(caches)], f.src, f.dst, status=status)
+            m = dfc.paged_compact(f.context_lens, table, ring, f.cursor, shared, P, status=status)
+            dfc.paged_copy([tuple(caches)], m.src, m.dst, status=status)
+            keep, cursor = f.context_lens, f.cursor
+            outs += [x, *ver, *f, *m]
+            yield None
+        yield [*outs, table, ring, shared, status, caches]
+
+    alone = []
+    for seed in (1, 2):
+        say("alone", seed)
+        *_, got = program(seed)
+        torch.cuda.synchronize()
+        alone.append(got)
+        assert int(got[-2]) == 0
+    streams, programs = [torch.cuda.Stream() for _ in range(2)], [program(1), program(2)]
+    got = [None, None]
+    say("both")
+    for _ in range(rounds + 1):
+        for i, (stream, p) in enumerate(zip(streams, programs)):
+            with torch.cuda.stream(stream):
+                got[i] = next(p)
+    torch.cuda.synchronize()
+    for a, b in zip(alone, got):
+        assert all(torch.equal(x, y) for x, y in zip(a, b))
