@@ -9,8 +9,8 @@
 // Which token that is changes where the sums cross u sum(w).  Of V tokens whose
 // sums are off by a factor of 1 + e, a random number lands next to a border with
 // a probability of up to 2 e V: one call in 40 for e = 1e-7 and a vocabulary of
-// 128256.  Exponentials and sums are therefore in 64 bits, where it is one in
-// 10^8.
+// 128256.  Exponentials and sums are therefore in 64 bits, to their last bits, where
+// it is one in 10^8 at most.
 //
 // A row is cut into pieces of 1,024 values, one a wavefront and 16 a lane, which
 // are read once: their largest, its first index, and the sum of
@@ -21,7 +21,7 @@
 //
 // Bounds (one MI355X, 128256 values a row in fp32).  64 requests of five drafts,
 // 328 MB of logits that count: the pass over them 68-75 us, 4.4-4.8 TB/s, nearly
-// the rate of a copy and nearly as long as its 23 instructions a value take (with
+// the rate of a copy and nearly as long as its 24 instructions a value take (with
 // sums of the values in place of their exponentials it took 50), then 7 us to
 // decide, 14 for the refused rows (66 MB, 4.7 TB/s), 5 for the tokens.  One row:
 // 3.5 and 6 us, latency.
@@ -123,25 +123,28 @@ __device__ __forceinline__ T over_wave(T x) {
     return of_lane(scan_of<F>(x), kWave - 1);
 }
 
-// 2^t for t <= 0, within 4e-14 of it and 1 for 0: t = n + f with |f| <= 1/2 by
+// 2^t for t <= 0, within 6.3e-16 of it and 1 for 0: t = n + f with |f| <= 1/2 by
 // adding and taking off a number whose last bit is 1, and 2^f as 1 + f q(f), q the
-// polynomial of degree 8 through (2^f - 1) / f at the Chebyshev nodes of
-// [-1/2, 1/2].  Its instructions decide: 64 requests of five drafts 129 us with a
-// library's exponential, which has twice as many, and 106 with a degree more than
-// here, of which each is 3.  (With a table of 64 roots and degree 4, a quarter
-// fewer, it took the same.)
+// polynomial of degree 9 through (2^f - 1) / f at the Chebyshev nodes of
+// [-1/2, 1/2].  A degree less is off by 4e-14, as much as some 300 roundings of 64
+// bits: it answered for drafts next to the border what the definition does not.  Its
+// instructions decide, 3 a degree: 64 requests of five drafts 98.6 us in a graph with
+// this, 96.0 with the degree less; some 30 more with a library's exponential, which
+// has twice as many.  (With a table of 64 roots and degree 4, a quarter fewer, it
+// took the same.)
 __device__ __forceinline__ double exp2_of(double t) {
     t = fmax(t, -1100.0);  // (2^-1100 is 0)
     const double whole = t + 0x1.8p52, f = t - (whole - 0x1.8p52);
-    double y = 0x1.b63880a30e9ffp-24;
-    y = fma(y, f, 0x1.63d136366db24p-20);
-    y = fma(y, f, 0x1.ffcb9515a8016p-17);
-    y = fma(y, f, 0x1.4308ac85aa947p-13);
-    y = fma(y, f, 0x1.5d87fe86fe88ep-10);
-    y = fma(y, f, 0x1.3b2ab7181b755p-7);
-    y = fma(y, f, 0x1.c6b08d7047e52p-5);
-    y = fma(y, f, 0x1.ebfbdff823cedp-3);
-    y = fma(y, f, 0x1.62e42fefa39efp-1);
+    double y = 0x1.e5e9f548e5725p-28;
+    y = fma(y, f, 0x1.b6571de2f2351p-24);
+    y = fma(y, f, 0x1.62bfe46117445p-20);
+    y = fma(y, f, 0x1.ffcb76789860fp-17);
+    y = fma(y, f, 0x1.4309130378460p-13);
+    y = fma(y, f, 0x1.5d87fe908f88ap-10);
+    y = fma(y, f, 0x1.3b2ab6fba385fp-7);
+    y = fma(y, f, 0x1.c6b08d7044119p-5);
+    y = fma(y, f, 0x1.ebfbdff82c590p-3);
+    y = fma(y, f, 0x1.62e42fefa39f7p-1);
     y = fma(y, f, 1.0);
     return __builtin_ldexp(y, int(uint32_t(__builtin_bit_cast(uint64_t, whole))));
 }

@@ -1,0 +1,53 @@
+"""GPU: verification of drafted tokens where little decides (dfc_verify_drafts):
+drafts whose random number lies next to the border to within a few roundings of
+64 bits."""
+import numpy as np
+import pytest
+
+import lossless_entropy_coded_dfc_amd as dfc
+import test_gpu_verify as gv
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+REAL = np.longdouble  # 64 bits of mantissa: the definition's side
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _device():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+
+
+def next_to_the_border():
+    """Logits z of float32, as many as there are in (-16, -2], for which the
+    probability p = e^z / (1 + e^z) lies next to a number u of float32: by 5e-15
+    to 3e-14 of itself."""
+    z = np.arange(np.float32(2).view(np.uint32), np.float32(16).view(np.uint32), dtype=np.uint32).view(np.float32)
+    found = []
+    for some in np.array_split(z, 64):
+        p = 1 / (1 + np.exp(some.astype(REAL)))
+        u = p.astype(np.float32)
+        far = np.abs(u.astype(REAL) / p - 1)
+        keep = (far > 5e-15) & (far < 3e-14)
+        found += [(-a, b, b < c) for a, b, c in zip(some[keep], u[keep], p[keep])]
+    return found
+
+
+def test_drafts_next_to_the_border():
+    """Errors of a probability here, of itself: 2^t 6.3e-16 and Horner's
+    roundings 1.2e-16; t = z log2(e), |t| < 24, is off by half a unit, 2^-49, and
+    by 24 2^-53 of the constant's, together 4.4e-15, times ln 2: 3.1e-15; sum,
+    quotient and product 3 2^-53.  5e-15 covers them: 4.2e-15."""
+    cases = next_to_the_border()
+    assert len(cases) >= 10 and 0 < sum(h for _, _, h in cases) < len(cases)
+    n = len(cases)
+    logits = torch.zeros(2 * n, 2)
+    logits[::2, 1] = torch.tensor([float(z) for z, _, _ in cases])
+    u = torch.full((2 * n,), 0.5)
+    u[::2] = torch.tensor([float(x) for _, x, _ in cases])
+    drafts = torch.tensor([1, 0] * n)
+    gv.say("verify, drafts next to the border", n)
+    got = dfc.verify_drafts(logits.cuda(), torch.arange(0, 2 * n + 1, 2, dtype=torch.int32, device="cuda"), drafts.cuda(),
+                            u.cuda())
+    assert got.accepted.tolist() == [int(h) for _, _, h in cases]
