@@ -622,7 +622,8 @@ dfc_status dfc_verify_drafts(const dfc_verify_args *args, void *stream) {
     if (s != DFC_OK) return s;
     if (!a.n_requests) return DFC_OK;
     if (!a.cu_rows || !a.accepted || !a.tokens) return DFC_EINVAL;
-    if (a.rows && (!a.logits_dev || !a.drafts || !a.uniforms || !a.workspace_dev)) return DFC_EINVAL;
+    if (a.rows && (!a.logits_dev || !a.drafts || !a.uniforms)) return DFC_EINVAL;
+    if (!a.workspace_dev && workspace_of(a)) return DFC_EINVAL;
     if (a.logits_stride < int64_t(a.vocab) || (a.draft_logits_dev && a.draft_stride < int64_t(a.vocab))) return DFC_EINVAL;
     if (reinterpret_cast<uintptr_t>(a.workspace_dev) & 255u) return DFC_EINVAL;
     if (a.workspace_bytes < workspace_of(a)) return DFC_ESIZE;
