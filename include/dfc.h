@@ -692,8 +692,12 @@ typedef struct {
  * that is 0 everywhere) and p_a if there are no more.  One row and no draft: a
  * token drawn from the logits.  T = 0: p is 1 at the lowest index of the
  * largest logit, so a draft holds if it is that.  Logits of -inf have
- * probability 0.  Exponentials, sums and comparisons are in 64 bits, whose
- * errors move the border between two tokens by less than 1e-13.  A row that holds
+ * probability 0.  Exponentials, sums and comparisons are in 64 bits.  Their errors
+ * move the border between two tokens by less than 2e-14, and after a draft that was
+ * refused against a drafter's logits, where probabilities are subtracted, by less
+ * than 5e-14 / (the sum of max(p_a - q_a, 0)): rows that nearly agree leave little to
+ * draw from.  A draft's own border p / q moves by less than 1e-12 of itself (for p
+ * and q above 1e-300).  A row that holds
  * NaN or +inf or nothing above -inf, and a temperature that is negative or not
  * finite, give no probabilities: no draft holds there and the token is -1
  * (DFC_ECORRUPT in the status).  A draft outside the vocabulary does not hold

@@ -10,7 +10,9 @@
 // sums are off by a factor of 1 + e, a random number lands next to a border with
 // a probability of up to 2 e V: one call in 40 for e = 1e-7 and a vocabulary of
 // 128256.  Exponentials and sums are therefore in 64 bits, to their last bits, where
-// it is one in 10^8 at most.
+// it is one in 10^8 at most.  (Differences of rows that nearly agree are off by more
+// of themselves: by 5e-14 over the sum of max(p - q, 0), which is also about how
+// often such a draft is refused.)
 //
 // A row is cut into pieces of 1,024 values, one a wavefront and 16 a lane, which
 // are read once: their largest, its first index, and the sum of

@@ -1,6 +1,6 @@
 """GPU: verification of drafted tokens where little decides (dfc_verify_drafts):
 drafts whose random number lies next to the border to within a few roundings of
-64 bits."""
+64 bits, and what is left of rows that nearly agree."""
 import numpy as np
 import pytest
 
@@ -51,3 +51,47 @@ def test_drafts_next_to_the_border():
     got = dfc.verify_drafts(logits.cuda(), torch.arange(0, 2 * n + 1, 2, dtype=torch.int32, device="cuda"), drafts.cuda(),
                             u.cuda())
     assert got.accepted.tolist() == [int(h) for _, _, h in cases]
+
+
+def probabilities(z):
+    e = np.exp(z.numpy().astype(REAL) - z.max().numpy().astype(REAL))
+    return e / e.sum()
+
+
+@pytest.mark.parametrize("vocab", [50, 3000, 128256])
+@pytest.mark.parametrize("apart", ["masked 8e-8", "masked 3e-11", "an ulp"])
+def test_rows_that_nearly_agree(vocab, apart):
+    """A draft refused against a drafter that is the model but for one token.
+    What is left sums to that little, and the token drawn is the definition's to
+    within 5e-14 of a probability: a probability's errors (6.3e-16 and 1.2e-16, and
+    3.1e-16 |t| of four roundings in t = (z - top) / T log2(e)) come to 3.1e-16 times
+    the mean of |t|, below 24.5, and 7.5e-16, over a row 8.4e-15; twice that, for the
+    sum's, and 3.3e-15 of 30 additions make 2e-14, of two rows 4e-14."""
+    g = torch.Generator().manual_seed(vocab)
+    z = 2 * torch.randn(vocab, generator=g)
+    x = vocab // 3
+    model, drafter = z.clone(), z.clone()
+    n = 40
+    u = torch.rand(2 * n, generator=g)
+    if apart == "an ulp":
+        model[x] = drafter[x] = 4.5
+        drafter[x] = torch.nextafter(drafter[x], torch.tensor(20.0))
+        u[::2] = 1 - 2.0 ** -24
+    else:
+        model[x] = -torch.inf
+        others = probabilities(model[torch.arange(vocab) != x])
+        top = model.max()
+        drafter[x] = float(top - np.log(float(others.max())) + np.log(float(apart.split()[1])))
+    p, q = probabilities(model), probabilities(drafter)
+    left = np.maximum(p - q, 0)
+    sums = np.concatenate([[REAL(0)], np.cumsum(left)])
+    assert 0 < sums[-1] < 1e-6
+    rows = torch.stack([model, z]).repeat(n, 1)
+    drafts = torch.full((2 * n,), x)
+    gv.say("verify, rows that nearly agree", vocab, apart, float(sums[-1]))
+    got = dfc.verify_drafts(rows.cuda(), torch.arange(0, 2 * n + 1, 2, dtype=torch.int32, device="cuda"), drafts.cuda(),
+                            u.cuda(), draft_logits=torch.stack([drafter, z]).repeat(n, 1).cuda())
+    assert not got.accepted.any()
+    for token, v in zip(got.tokens.tolist(), u[1::2].tolist()):
+        share = REAL(v) * sums[-1]
+        assert token != x and sums[token] - 5e-14 <= share <= sums[token + 1] + 5e-14
