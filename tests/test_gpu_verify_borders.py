@@ -1,6 +1,7 @@
 """GPU: verification of drafted tokens where little decides (dfc_verify_drafts):
 drafts whose random number lies next to the border to within a few roundings of
-64 bits, and what is left of rows that nearly agree."""
+64 bits, what is left of rows that nearly agree, and vocabularies beyond the
+262,144 values whose sums are kept."""
 import numpy as np
 import pytest
 
@@ -95,3 +96,26 @@ def test_rows_that_nearly_agree(vocab, apart):
     for token, v in zip(got.tokens.tolist(), u[1::2].tolist()):
         share = REAL(v) * sums[-1]
         assert token != x and sums[token] - 5e-14 <= share <= sums[token + 1] + 5e-14
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("drafter", [True, False])
+@pytest.mark.parametrize("vocab", [262145, 300001])
+def test_vocabularies_past_the_sums_that_are_kept(vocab, drafter, dtype):
+    """A row of more than 256 pieces of 1,024 values: those past them are added
+    up again for each token."""
+    for spread, seed in ((2.0, 0), (0.01, 1)):
+        s = gv.Step([3, 1, 2, 2], vocab, dtype, drafter, seed=seed, spread=spread, temperature=0.9)
+        # the last request's draft lies in the last piece; where it is certain it
+        # has a good part of the weight and is refused
+        s.x[6] = vocab - 1
+        s.z[6, vocab - 1] = s.z[6].max() + 8 * spread
+        if drafter:
+            s.d[6, vocab - 1] = s.z[6, vocab - 1] + 4 * spread
+        gv.say("verify, large vocabulary", vocab, drafter, dtype, spread)
+        for u in (0.3, 0.9, 0.99, 1 - 2.0 ** -13, 1 - 2.0 ** -24):
+            s.u[:] = u
+            s.u[6] = 1 - 2.0 ** -20
+            got = s.run()
+            assert got[2] == 0 and got[0][3] == 0
+            s.check(got)

@@ -36,7 +36,8 @@ def verify_drafts(logits, cu_rows, drafts, uniforms, temperature=None):
 
 def paged_release(held, keep, table, ring, cursor, shared, page_size, window=0, sinks=0):
     assert ((0 <= keep) & (keep <= held)).all(), (keep, held)     # or the request is passed over
-    got = op.release(held.tolist(), keep.tolist(), table, ring, cursor, shared, page_size, window, sinks)
+    got = op.release(held.tolist(), keep.tolist(), table.numpy(), ring.numpy(), cursor.numpy(), shared.numpy(), page_size,
+                     window, sinks)
     for t, x in zip((table, ring, shared), (got[0], got[1], got[3])):
         t.copy_(torch.from_numpy(x))
     return torch.from_numpy(got[2])
