@@ -34,7 +34,9 @@
 // 15-17 us).  With a window and sinks the keys of the sinks' last tile and of the
 // window's first count whole: 64 requests of up to 8191 tokens under 1000 + 4
 // 57 us (4.4 TB/s of what they see), 513 tokens over 32000 under 4096 + 64 in
-// float16 71, a tile more than the window alone takes 74 for 78 in a graph.  Other
+// float16 70; with heads of 64, 80 and 256 33, 49 and 142 us (floors 25, 31 and 99)
+// and 48, 70 and 188 (13, 17 and 54).  Tiles wholly inside long sinks take the masked
+// path: 4096 + 1024 and 4096 + 4096 over 32000 98 and 152 us (33 and 53).  Other
 // heads have only been looked at: 64 ragged requests with
 // heads of 64, 80 and 256 take 130, 180 and 602 us (floors 107, 134 and 428),
 // prompts of 8192 349, 529 and 1864 (204, 255 and 815).
@@ -967,7 +969,8 @@ LaunchPlan launch_plan(const dfc_attention_args &a, uint32_t sinks, int rw, bool
     // for less (us with a quarter and a tenth of the rows, 32 heads over 8 of 128:
     // 1000 tokens over 32000 under 4096 + 64 138 and 102, 768 under 8192 + 64 250
     // and 142, 513 over 8192 under 2048 + 16 63 and 48, eight times 128 over 8000
-    // 140 and 105; prompts the same).  Calls without sinks are left as they round.
+    // 140 and 105; prompts the same).  The same would hold under a window without
+    // sinks; those calls keep the old price, and with it the bits of their results.
     if (cut && p.rw >= 4) p.split_cost = float(p.most_rows) / 10.0f;
     p.join_cost = p.rw >= 4 ? 2.0f : 8.0f;
     const uint64_t tiles = most_tiles(a, p.rw);

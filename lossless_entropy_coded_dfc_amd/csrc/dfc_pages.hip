@@ -22,8 +22,14 @@
 // count, ring), so the small sizes are one launch each, by one workgroup, and the
 // large ones as few as their order allows without workgroups that wait for
 // others.  Pages copied are bound by HBM: 4,200 pages of 16 tokens of 8 heads of
-// 128 in four layers (2.2 GB read and written) 411-421 us, 5.2-5.35 TB/s, where a
-// device copy reaches 5.05.
+// 128 in four layers (2.2 GB read and written) 416-422 us, 5.2-5.3 TB/s, where a
+// device copy reaches 5.05; 300 of 128 tokens in eight layers (2.5 GB) 503, 5.0.  A
+// page of one K or V is one workgroup's however large it is, so few large ones take
+// its time: one page of 16, 64 and 128 tokens in one layer 3.9, 6.3 and 9.8 us,
+// seven in eight layers 4.3, 7.9 and 14.2 (1.7, 3.7 and 4.1 TB/s).
+//
+// Times of single kernels below are medians of calls that the host waits for, 1 us
+// above those in a full queue.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -190,7 +196,7 @@ __device__ __forceinline__ void look_at_cut(const ReleaseArgs &p, uint32_t r, ui
 }
 
 // A workgroup takes a request at a time and its lanes the entries.  300 requests,
-// 97 of which give up all of up to 2,048 pages, 3.5 us.
+// 97 of which give up all of up to 2,048 pages, 5.2 us.
 __global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
     uint32_t bad = 0;
     for (uint32_t r = blockIdx.x; r < p.a.n_requests; r += gridDim.x) {
@@ -204,7 +210,7 @@ __global__ __launch_bounds__(kRowThreads) void release_kernel(ReleaseArgs p) {
     tell(p.a.status_dev, bad);
 }
 
-// Free pages of every slab.  (307,000 pages 3.6 us, and 5.8 to write those that
+// Free pages of every slab.  (307,000 pages 4.7 us, and 6.5 to write those that
 // are free: a chain of loads, sums and stores each.)
 __global__ __launch_bounds__(kPageThreads) void freed_count_kernel(ReleaseArgs p) {
     __shared__ uint32_t part[kPageWaves];
@@ -274,11 +280,12 @@ __global__ __launch_bounds__(kPageThreads) void freed_write_kernel(ReleaseArgs p
 // request's lengths and gives up a few entries by itself, as after refused drafts;
 // longer runs are taken by the wavefront, eight entries a lane at a time.
 //
-// The call's own time here and in three launches, pages of 16 tokens: 64 requests
-// of up to 8191 cut by up to five 4 and 10 us, eight of 8191 that end 6 and 8, a
-// window's pages of 64 8 and 11, of 16 with 32768 7 and 11; but 32 of up to 8191
-// that end 15 and 12, and 64 of 8191 37 and 13, which no size on the host tells
-// from the first: one step of a program that cuts drafts at every step.
+// The call's own time here and in three launches, pages of 16 tokens, in a graph: 64
+// requests of up to 8191 cut by up to five 4 and 11 us, eight of 8191 that end 6 and
+// 8, a window's pages of 64 8 and 11, of 16 with 32768 8 and 12; but 32 of up to 8191
+// that end 16 and 12, and 64 of 8191 37 and 13: the freed pages are written two words
+// a wavefront at a time.  No size on the host tells these from the first, which a
+// program makes at every step, and few of its requests end at once.
 constexpr uint32_t kFewRequests = 64, kFreedWords = 4, kFewFreed = 32u * kPageThreads * kFreedWords, kFewGiven = 65536;
 __global__ __launch_bounds__(kPageThreads) void release_few_kernel(ReleaseArgs p) {
     constexpr uint32_t kAlone = 2, kEach = kFewRequests / kPageWaves;
@@ -417,8 +424,10 @@ __device__ __forceinline__ Child child_of(const dfc_fork_args &a, uint32_t shift
 
 // A workgroup a request.  Those that are forked, and the last one for the
 // cursor, count the pages that the requests before them take: each for itself,
-// which costs a few loads a thread and saves a second launch.  7 children of one
-// request of 8191 tokens 3.4 us, 112 of 16 requests 3.9.
+// which costs a few loads a thread for some hundred requests and saves a second
+// launch.  7 children of one request of 8191 tokens 5.3 us, 112 of 16 requests 5.8.
+// The work grows with the square of the requests: as many children as parents, 64 of
+// each 4.5 us in a graph, 512 6, 2,048 18, 8,192 133, 32,768 1,700.
 __global__ __launch_bounds__(kRowThreads) void fork_kernel(ForkArgs p) {
     __shared__ uint32_t part[kRowThreads / kWave];
     const dfc_fork_args &a = p.a;
@@ -638,8 +647,8 @@ __global__ __launch_bounds__(kRowThreads) void compact_finish_kernel(CompactArgs
 
 // All of it by one workgroup, where pages and rows' entries are a few for each of
 // its threads: two bits a page in LDS, from whose sums a page's rank is read.  64
-// requests of up to 500 tokens among 512 free pages take 5.4 us in place of 10 in
-// five launches, whose gaps come on top (27 and 34 us with the copying);
+// requests of up to 500 tokens among 512 free pages take 4.5 us in a graph, and 13.5
+// in five launches;
 // 17,000 entries over 16,700 pages took 23 in place of 20, since one compute unit
 // did all of it.
 constexpr uint32_t kFewPages = kSlab, kEntries = 8, kFewEntries = kEntries * kPageThreads, kFewRows = 1024;

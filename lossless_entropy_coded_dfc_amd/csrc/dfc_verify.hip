@@ -21,12 +21,17 @@
 // token itself; only where a draft is refused against a drafter's logits are the
 // two rows read again, since max(p - q, 0) needs both of their sums first.
 //
-// Bounds (one MI355X, 128256 values a row in fp32).  64 requests of five drafts,
-// 328 MB of logits that count: the pass over them 68-75 us, 4.4-4.8 TB/s, nearly
+// Bounds (one MI355X, 128256 values a row in fp32, medians).  64 requests of five
+// drafts, 328 MB of logits that count: the pass over them 74 us, 4.4 TB/s, nearly
 // the rate of a copy and nearly as long as its 24 instructions a value take (with
 // sums of the values in place of their exponentials it took 50), then 7 us to
-// decide, 14 for the refused rows (66 MB, 4.7 TB/s), 5 for the tokens.  One row:
-// 3.5 and 6 us, latency.
+// decide, 15 for the refused rows (66 MB, 4.4 TB/s), 6 for the tokens.  One row:
+// 3.8 and 6.4 us, latency.  The whole call (98 us, floor 65): without a drafter's
+// logits 50 (39).  In 16 bits the bytes halve and the instructions stay: 91 (33),
+// without a drafter's logits 47 (20).  Rows that are not 16-byte aligned come a value
+// at a time: a vocabulary of 128257 114 and, in 16 bits, 153.  Every wavefront looks
+// through all of cu_rows: 512 single rows 78 (52), 1,024 of 32000 57 (26), 4,096 of
+// them 335 (104).
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
