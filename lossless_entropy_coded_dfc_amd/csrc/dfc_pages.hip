@@ -22,7 +22,7 @@
 // count, ring), so the small sizes are one launch each, by one workgroup, and the
 // large ones as few as their order allows without workgroups that wait for
 // others.  Pages copied are bound by HBM: 4,200 pages of 16 tokens of 8 heads of
-// 128 in four layers (2.2 GB read and written) 416-422 us, 5.2-5.3 TB/s, where a
+// 128 in four layers (2.2 GB read and written) 415-422 us, 5.2-5.3 TB/s, where a
 // device copy reaches 5.05; 300 of 128 tokens in eight layers (2.5 GB) 503, 5.0.  A
 // page of one K or V is one workgroup's however large it is, so few large ones take
 // its time: one page of 16, 64 and 128 tokens in one layer 3.9, 6.3 and 9.8 us,

@@ -22,7 +22,7 @@
 // two rows read again, since max(p - q, 0) needs both of their sums first.
 //
 // Bounds (one MI355X, 128256 values a row in fp32, medians).  64 requests of five
-// drafts, 328 MB of logits that count: the pass over them 74 us, 4.4 TB/s, nearly
+// drafts, 328 MB of logits that count: the pass over them 71-74 us, 4.4-4.6 TB/s, nearly
 // the rate of a copy and nearly as long as its 24 instructions a value take (with
 // sums of the values in place of their exponentials it took 50), then 7 us to
 // decide, 15 for the refused rows (66 MB, 4.4 TB/s), 6 for the tokens.  One row:
